@@ -10,10 +10,16 @@ import fails loudly; there is no CPU or PyTorch fallback.
         -> (o, lse)          tiled exact forward (bf16 on tcgen05, or fp32 SIMT)
     attn_naive_fwd(...)      materialising baseline (S and P in the input dtype)
     attn_deviation(a, b)     max-abs, Wasserstein-1 (via sort), mean/std |a-b|
+
+A paged key/value cache (``PagedCache``): pages are handed out, shared and
+released on the device by attn_cache_reserve / _free / _fork / _compact, new
+tokens are written by attn_cache_append and attended to by attn_paged_fwd.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -33,6 +39,8 @@ ATTN_ERR_DEVICE_TIMEOUT = -5
 # Every symbol include/attn.h declares.
 EXPORTS = ("attn_fwd", "attn_fwd_host_workspace_size", "attn_fwd_host", "attn_fwd_block_sparse", "attn_naive_workspace_size", "attn_naive_fwd", "attn_deviation_workspace_size",
            "attn_deviation", "attn_deviation_noalloc", "attn_decode_workspace_size", "attn_decode_fwd",
+           "attn_cache_workspace_size", "attn_cache_reserve", "attn_cache_free", "attn_cache_fork", "attn_cache_compact",
+           "attn_cache_append", "attn_paged_workspace_size", "attn_paged_fwd",
            "attn_bwd_workspace_size", "attn_bwd", "attn_emul_fwd", "attn_emul_round", "attn_status",
            "attn_strerror", "attn_last_variant", "attn_debug_wait_timeout")
 DEVIATION_NOALLOC_MAX_N = 1 << 20
@@ -49,6 +57,16 @@ class AttnError(RuntimeError):
 class DevT(ctypes.Structure):
     _fields_ = [("max_abs", ctypes.c_double), ("w1", ctypes.c_double), ("mean_abs", ctypes.c_double),
                 ("std_abs", ctypes.c_double), ("mean_signed", ctypes.c_double), ("n", ctypes.c_longlong)]
+
+
+class CacheT(ctypes.Structure):
+    """attn_cache_t"""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("seq_lens", ctypes.c_void_p), ("ref_counts", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("layers", ctypes.c_int), ("pages", ctypes.c_int), ("heads", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("d", ctypes.c_int), ("seqs", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("layer_stride", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("slot_stride", ctypes.c_longlong)]
 
 
 def _load() -> ctypes.CDLL:
@@ -79,6 +97,23 @@ def _load() -> ctypes.CDLL:
     lib.attn_decode_workspace_size.restype = sz
     lib.attn_decode_fwd.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, vp, sz, vp]
     lib.attn_decode_fwd.restype = i
+    cp = ctypes.POINTER(CacheT)
+    lib.attn_cache_workspace_size.argtypes = [i, i]
+    lib.attn_cache_workspace_size.restype = sz
+    lib.attn_cache_reserve.argtypes = [cp, vp, vp, i, vp, vp, sz, vp]
+    lib.attn_cache_reserve.restype = i
+    lib.attn_cache_free.argtypes = [cp, vp, vp, i, vp]
+    lib.attn_cache_free.restype = i
+    lib.attn_cache_fork.argtypes = [cp, vp, vp, i, i, vp, vp, sz, vp]
+    lib.attn_cache_fork.restype = i
+    lib.attn_cache_compact.argtypes = [cp, vp, vp, vp, vp, sz, vp]
+    lib.attn_cache_compact.restype = i
+    lib.attn_cache_append.argtypes = [cp, i, vp, vp, ll, ll, i, vp, vp, i, vp]
+    lib.attn_cache_append.restype = i
+    lib.attn_paged_workspace_size.argtypes = [i, i, i, i, i]
+    lib.attn_paged_workspace_size.restype = sz
+    lib.attn_paged_fwd.argtypes = [cp, i, vp, vp, vp, ll, ll, ll, ll, i, i, vp, vp, i, i, i, f, vp, sz, vp]
+    lib.attn_paged_fwd.restype = i
     lib.attn_bwd_workspace_size.argtypes = [i, i, i, i]
     lib.attn_bwd_workspace_size.restype = sz
     lib.attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp, vp, sz, vp]
@@ -359,6 +394,228 @@ def attn_decode_fwd(q, k, v, causal: bool = False, scale: float | None = None, k
                              float(scale), _DTYPE[q.dtype], _ptr(m), _ptr(ws), ws.numel(),
                              ctypes.c_void_p(_stream(stream)))
     _check(rc, "attn_decode_fwd")
+    return o, l
+
+
+# ---------------------------------------------------------------------------
+# paged key/value cache
+# ---------------------------------------------------------------------------
+class PagedCache:
+    """A paged key/value cache over the caller's device tensors (attn_cache_t).
+
+    k, v: pools of pages, [layers, pages, heads, page_size, d], bfloat16 or
+    float32, with equal strides; a page of one layer is one contiguous block,
+    head by head (a contiguous tensor) or token by token (a tensor of
+    [layers, pages, page_size, heads, d] seen through transpose(2, 3)).
+    page_table: int32 [seqs, max_pages], -1 where a sequence has no page;
+    seq_lens: int32 [seqs]; ref_counts: int32 [pages].  The object keeps the
+    tensors; all are changed in place by the operators below.
+    """
+
+    def __init__(self, k, v, page_table, seq_lens, ref_counts):
+        if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be [layers, pages, heads, page_size, d] with one shape, dtype and strides")
+        if k.dtype not in _DTYPE:
+            raise ValueError(f"unsupported dtype {k.dtype}")
+        if k.shape[4] > 1 and k.stride(4) != 1:
+            raise ValueError("the last dimension of k and v must be contiguous")
+        layers, pages, heads, page_size, d = k.shape
+        for t, shape, name in ((page_table, 2, "page_table [seqs, max_pages]"), (seq_lens, 1, "seq_lens [seqs]"),
+                               (ref_counts, 1, "ref_counts [pages]")):
+            if t.dtype != torch.int32 or t.dim() != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor")
+        if seq_lens.shape[0] != page_table.shape[0] or ref_counts.shape[0] != pages:
+            raise ValueError("page_table, seq_lens and ref_counts do not fit each other or the pools")
+        for t in (k, v, page_table, seq_lens, ref_counts):
+            if not t.is_cuda or t.device != k.device:
+                raise ValueError("the tensors of a cache must be on one CUDA device")
+        self.k, self.v, self.page_table, self.seq_lens, self.ref_counts = k, v, page_table, seq_lens, ref_counts
+        self.device, self.dtype = k.device, k.dtype
+        self.layers, self.pages, self.heads, self.page_size, self.d = layers, pages, heads, page_size, d
+        self.seqs, self.max_pages = page_table.shape
+        self._index = k.device.index
+        self._c = CacheT(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+                         _DTYPE[k.dtype], layers, pages, heads, page_size, d, self.seqs, self.max_pages, k.stride(0),
+                         k.stride(1), k.stride(2), k.stride(3))
+        self._p = ctypes.pointer(self._c)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, heads: int, page_size: int, d: int, seqs: int, max_pages: int,
+              dtype=torch.bfloat16, device="cuda", token_major: bool = False):
+        """A new cache without sequences.  token_major: pages lie token by
+        token instead of head by head."""
+        def pool():
+            if token_major:
+                return torch.empty((layers, pages, page_size, heads, d), dtype=dtype, device=device).transpose(2, 3)
+            return torch.empty((layers, pages, heads, page_size, d), dtype=dtype, device=device)
+
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+        return cls(pool(), pool(), ints(seqs, max_pages) - 1, ints(seqs), ints(pages))
+
+
+def _paged_list(t, cache, name, n=None):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != cache.device:
+        raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} elements")
+    return t.data_ptr()
+
+
+@contextlib.contextmanager
+def _paged_scope(cache, stream):
+    """The cache's device is current, and `stream` too, so that memory
+    allocated inside belongs to it.  Yields the stream's handle."""
+    with torch.cuda.device(cache.device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(st):
+                yield st.cuda_stream
+
+
+def _paged_workspace(workspace, need, cache):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    if not workspace.is_cuda or workspace.device != cache.device or workspace.dtype != torch.uint8 or \
+            not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
+    return workspace
+
+
+def attn_cache_workspace_size(pages: int, n: int) -> int:
+    return int(lib.attn_cache_workspace_size(pages, n))
+
+
+def _granted(granted, cache, n):
+    if granted is None:
+        return torch.empty(n, dtype=torch.int32, device=cache.device)
+    _paged_list(granted, cache, "granted", n)
+    return granted
+
+
+def attn_cache_reserve(cache, seqs, n_new, granted=None, workspace=None, stream=None):
+    """Room for n_new[i] more tokens in sequence seqs[i] (int32 device
+    vectors): free pages, lowest first, in list order; lengths grow.  Returns
+    granted, int32 [n]: 1, or 0 for an entry that got nothing."""
+    n = seqs.shape[0]
+    a, b = _paged_list(seqs, cache, "seqs"), _paged_list(n_new, cache, "n_new", n)
+    with _paged_scope(cache, stream) as st:
+        g = _granted(granted, cache, n)
+        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache)
+        rc = lib.attn_cache_reserve(cache._p, a, b, n, g.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "attn_cache_reserve")
+    return g
+
+
+def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
+    """Cuts sequence seqs[i] to its first keep[i] tokens (None: to none)."""
+    n = seqs.shape[0]
+    a = _paged_list(seqs, cache, "seqs")
+    b = None if keep is None else _paged_list(keep, cache, "keep", n)
+    with _paged_scope(cache, stream) as st:
+        rc = lib.attn_cache_free(cache._p, a, b, n, st)
+    _check(rc, "attn_cache_free")
+
+
+def attn_cache_fork(cache, parents, children, copy: bool = False, granted=None, workspace=None, stream=None):
+    """Makes the empty sequence children[i] a copy of parents[i]: full pages
+    shared and a partly filled last page copied, or (copy=True) every page
+    copied.  Returns granted, int32 [n]."""
+    n = parents.shape[0]
+    a, b = _paged_list(parents, cache, "parents"), _paged_list(children, cache, "children", n)
+    with _paged_scope(cache, stream) as st:
+        g = _granted(granted, cache, n)
+        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache)
+        rc = lib.attn_cache_fork(cache._p, a, b, n, int(bool(copy)), g.data_ptr(), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "attn_cache_fork")
+    return g
+
+
+def attn_cache_compact(cache, inplace: bool = True, workspace=None, stream=None):
+    """Moves the live pages to the bottom of the pool.  Returns (page_table,
+    ref_counts, n_live): the cache's own tensors, updated, or with
+    inplace=False new ones, the cache's staying as they were (and valid, since
+    only free pages are written); n_live is an int32 device tensor [1]."""
+    with _paged_scope(cache, stream) as st:
+        table = cache.page_table if inplace else torch.empty_like(cache.page_table)
+        refs = cache.ref_counts if inplace else torch.empty_like(cache.ref_counts)
+        n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
+        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, 0), cache)
+        rc = lib.attn_cache_compact(cache._p, table.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), st)
+    _check(rc, "attn_cache_compact")
+    return table, refs, n_live
+
+
+def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None) -> None:
+    """Writes the keys and values of new tokens into one layer.  k_new, v_new:
+    [T, heads, d] of the cache's dtype, any strides with a contiguous last
+    dimension (one pair of strides for both).  Entry i: sequence seqs[i]
+    (seqs None: sequence i), tokens q_start[i] .. q_start[i+1] - 1, the last
+    ones of the sequence (reserved before)."""
+    if (k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or
+            k_new.shape[1:] != (cache.heads, cache.d) or k_new.stride(2) != 1):
+        raise ValueError("k_new and v_new must be [T, heads, d] with one shape and strides, the last dimension contiguous")
+    if k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or k_new.device != cache.device or \
+            v_new.device != cache.device:
+        raise ValueError("k_new and v_new must have the cache's dtype and device")
+    n = q_start.shape[0] - 1
+    a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
+    b = _paged_list(q_start, cache, "q_start")
+    with _paged_scope(cache, stream) as st:
+        rc = lib.attn_cache_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0), k_new.stride(1),
+                                   k_new.shape[0], a, b, n, st)
+    _check(rc, "attn_cache_append")
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_size(Hq, heads, max_q, d, dtype) -> int:
+    return int(lib.attn_paged_workspace_size(Hq, heads, max_q, d, dtype))
+
+
+def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) -> int:
+    return _paged_workspace_size(Hq, heads, max_q, d, _DTYPE[dtype] if not isinstance(dtype, int) else dtype)
+
+
+def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None, causal: bool = True,
+                   scale: float | None = None, out=None, lse=None, workspace=None, stream=None, want_lse: bool = True):
+    """Attention of new tokens over one layer of a paged cache.  q: [T, Hq, d]
+    of the cache's dtype, any strides with a contiguous last dimension; Hq a
+    multiple of the cache's heads (query head j reads kv head j // (Hq /
+    heads)).  Entry i: sequence seqs[i] (seqs None: sequence i), whose last
+    tokens are rows q_start[i] .. q_start[i+1] - 1 of q; causal: token t of the
+    entry's n sees keys j <= len - n + t.  max_q: at least the most new tokens
+    of an entry (default T; a close bound lets short entries take the path for
+    few rows).  Returns (o, lse): o like q, lse [T, Hq] float32; rows outside
+    the list are left as they were."""
+    if q.dim() != 3 or q.shape[2] != cache.d or (q.shape[2] > 1 and q.stride(2) != 1):
+        raise ValueError("q must be [T, Hq, d] with a contiguous last dimension")
+    if q.dtype != cache.dtype or q.device != cache.device:
+        raise ValueError("q must have the cache's dtype and device")
+    T, Hq, d = q.shape
+    n = q_start.shape[0] - 1
+    a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
+    b = _paged_list(q_start, cache, "q_start")
+    if max_q is None:
+        max_q = T
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or out.stride(2) != 1):
+        raise ValueError("out must be like q, with a contiguous last dimension")
+    if lse is not None and (lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            lse.device != q.device):
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq] on q's device")
+    with _paged_scope(cache, stream) as st:
+        o = out if out is not None else torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        l = lse if lse is not None else (torch.empty((T, Hq), dtype=torch.float32, device=q.device) if want_lse else None)
+        # (arguments the library rejects give 0 here; it then says which)
+        ws = _paged_workspace(workspace, _paged_workspace_size(Hq, cache.heads, max(int(max_q), 1), d, cache._c.dtype), cache)
+        rc = lib.attn_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(),
+                                q.stride(0), q.stride(1), o.stride(0), o.stride(1), T, Hq, a, b, n, int(max_q),
+                                int(bool(causal)), float(scale), ws.data_ptr(), ws.numel(), st)
+    _check(rc, "attn_paged_fwd")
     return o, l
 
 

@@ -8,6 +8,7 @@
 
 #include "../../include/attn.h"
 #include "internal.h"
+#include "paged.cuh"
 #include "ptx.cuh"
 
 namespace eta {
@@ -379,6 +380,214 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
         return kErrWorkspace;
     return launch_decode(Q, K, V, O, LSE, B, H, Nq, Nk, d, causal, scale, dtype == ATTN_BF16 ? 1 : 0, key_mask,
                          workspace, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+// Checks a cache descriptor; fills the page kernels' view of it.
+int check_cache(const attn_cache_t *c, CacheView &w) {
+    if (!c || !c->K || !c->V || !c->page_table || !c->seq_lens || !c->ref_counts) return kErrArg;
+    if (c->dtype != ATTN_F32 && c->dtype != ATTN_BF16) return c->dtype == ATTN_F64 ? kErrUnsupported : kErrArg;
+    if (c->layers <= 0 || c->pages <= 0 || c->heads <= 0 || c->page_size <= 0 || c->d <= 0 || c->seqs <= 0 ||
+        c->max_pages <= 0)
+        return kErrArg;
+    if (c->d > 128 || c->d % 32 != 0) return kErrUnsupported;
+    if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return kErrUnsupported;
+    if (static_cast<long long>(c->max_pages) * c->page_size >= (1LL << 31)) return kErrArg;
+    if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->ref_counts)) return kErrArg;
+    if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u)) return kErrArg;
+    const long long per = 16 / (c->dtype == ATTN_BF16 ? 2 : 4);   // elements of a 16-byte piece
+    const long long block = static_cast<long long>(c->heads) * c->page_size * c->d;
+    if (block / per >= (1LL << 30)) return kErrArg;
+    const bool by_head = c->head_stride == static_cast<long long>(c->page_size) * c->d && c->slot_stride == c->d;
+    const bool by_token = c->slot_stride == static_cast<long long>(c->heads) * c->d && c->head_stride == c->d;
+    // (with one head, or as strides of a single head may be given, both agree)
+    const bool one_head = c->heads == 1 && c->slot_stride == c->d && c->head_stride >= 0 && c->head_stride % per == 0;
+    if (!by_head && !by_token && !one_head) return kErrArg;
+    if (c->page_stride < 0 || c->layer_stride < 0 || c->page_stride % per || c->layer_stride % per) return kErrArg;
+    // blocks of different (layer, page) do not overlap, whichever stride is the outer one
+    const bool many_l = c->layers > 1, many_p = c->pages > 1;
+    if (many_p && c->page_stride < block) return kErrArg;
+    if (many_l && c->layer_stride < block) return kErrArg;
+    if (many_l && many_p) {
+        const bool pages_in = c->layer_stride >= (c->pages - 1) * c->page_stride + block;
+        const bool layers_in = c->page_stride >= (c->layers - 1) * c->layer_stride + block;
+        if (!pages_in && !layers_in) return kErrArg;
+    }
+    w.k = static_cast<uint4 *>(c->K);
+    w.v = static_cast<uint4 *>(c->V);
+    w.page_table = c->page_table;
+    w.seq_lens = c->seq_lens;
+    w.ref_counts = c->ref_counts;
+    w.layers = c->layers;
+    w.pages = c->pages;
+    w.heads = c->heads;
+    w.page_size = c->page_size;
+    w.rows = c->seqs;
+    w.max_pages = c->max_pages;
+    w.layer_vecs = c->layer_stride / per;
+    w.page_vecs = c->page_stride / per;
+    w.head_stride_vecs = c->head_stride / per;
+    w.slot_stride_vecs = c->slot_stride / per;
+    w.block_vecs = static_cast<int>(block / per);
+    w.slot_vecs = static_cast<int>(c->slot_stride / per);
+    w.row_vecs = static_cast<int>(c->d / per);
+    return kOk;
+}
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int check_workspace(const void *ws, size_t have, size_t need) {
+    return !ws || have < need || !aligned16(ws) ? kErrWorkspace : kOk;
+}
+// sm_103a only
+int check_device() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return kErrCuda;
+    return major == 10 && minor == 3 ? kOk : kErrUnsupported;
+}
+}  // namespace
+
+size_t attn_cache_workspace_size(int pages, int n) {
+    if (pages <= 0 || n < 0) return 0;
+    return cache_workspace_bytes(pages, n);
+}
+
+int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_new, int n, int *granted, void *workspace,
+                       size_t ws_bytes, void *stream) {
+    CacheView w;
+    int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (n < 0) return kErrArg;
+    if (n == 0) return kOk;
+    if (!seqs || !n_new || !granted || !aligned4(seqs) || !aligned4(n_new) || !aligned4(granted)) return kErrArg;
+    rc = check_workspace(workspace, ws_bytes, cache_workspace_bytes(w.pages, n));
+    if (rc != kOk) return rc;
+    return launch_cache_reserve(w, seqs, n_new, n, granted, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep, int n, void *stream) {
+    CacheView w;
+    const int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (n < 0) return kErrArg;
+    if (n == 0) return kOk;
+    if (!seqs || !aligned4(seqs) || !aligned4(keep)) return kErrArg;
+    return launch_cache_free(w, seqs, keep, n, static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_fork(const attn_cache_t *cache, const int *parents, const int *children, int n, int copy, int *granted,
+                    void *workspace, size_t ws_bytes, void *stream) {
+    CacheView w;
+    int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (n < 0 || (copy != 0 && copy != 1)) return kErrArg;
+    if (n == 0) return kOk;
+    if (!parents || !children || !granted || !aligned4(parents) || !aligned4(children) || !aligned4(granted)) return kErrArg;
+    rc = check_workspace(workspace, ws_bytes, cache_workspace_bytes(w.pages, n));
+    if (rc != kOk) return rc;
+    return launch_cache_fork(w, parents, children, n, copy, granted, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_counts_out, int *n_live, void *workspace,
+                       size_t ws_bytes, void *stream) {
+    CacheView w;
+    int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (!page_table_out || !ref_counts_out || !n_live) return kErrArg;
+    if (!aligned4(page_table_out) || !aligned16(ref_counts_out) || !aligned4(n_live)) return kErrArg;
+    rc = check_workspace(workspace, ws_bytes, cache_workspace_bytes(w.pages, 0));
+    if (rc != kOk) return rc;
+    return launch_cache_compact(w, page_table_out, ref_counts_out, n_live, workspace, static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
+                      long long head_stride, int T, const int *seqs, const int *q_start, int n, void *stream) {
+    CacheView w;
+    const int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (n < 0 || T < 0 || layer < 0 || layer >= w.layers) return kErrArg;
+    const long long per = 16 / (cache->dtype == ATTN_BF16 ? 2 : 4);
+    if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
+    if (n == 0 || T == 0) return kOk;
+    if (!Knew || !Vnew || !q_start || !aligned16(Knew) || !aligned16(Vnew) || !aligned4(q_start) || !aligned4(seqs))
+        return kErrArg;
+    return launch_cache_append(w, layer, Knew, Vnew, token_stride / per, head_stride / per, T, seqs, q_start, n,
+                               static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_paged_workspace_size(int Hq, int heads, int max_q, int d, int dtype) {
+    if (Hq <= 0 || heads <= 0 || Hq % heads || Hq / heads > 64 || max_q <= 0 || d <= 0 || d > 128 || d % 32) return 0;
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return 0;
+    return paged_workspace_bytes(Hq / heads, max_q, d, dtype == ATTN_BF16);
+}
+
+int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE, long long q_token_stride,
+                   long long q_head_stride, long long o_token_stride, long long o_head_stride, int T, int Hq,
+                   const int *seqs, const int *q_start, int n, int max_q, int causal, float scale, void *workspace,
+                   size_t ws_bytes, void *stream) {
+    CacheView w;
+    int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (layer < 0 || layer >= w.layers || T < 0 || n < 0 || Hq <= 0 || Hq % w.heads) return kErrArg;
+    if (Hq / w.heads > 64) return kErrUnsupported;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return kErrArg;
+    if (causal != 0 && causal != 1) return kErrArg;
+    if (static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
+    const int bf16 = cache->dtype == ATTN_BF16;
+    const long long per = bf16 ? 8 : 4;
+    for (long long s : {q_token_stride, q_head_stride, o_token_stride, o_head_stride})
+        if (s < 0 || s % per) return kErrArg;
+    if (T == 0 || n == 0) return kOk;
+    if (max_q <= 0 || max_q > T) return kErrArg;
+    // rows of O must not overlap: one of the strides steps over all of the other's range
+    const long long ht = o_head_stride, tt = o_token_stride;
+    const bool heads_in = (Hq == 1 || ht >= cache->d) && (T == 1 || tt >= (Hq - 1) * ht + cache->d);
+    const bool tokens_in = (T == 1 || tt >= cache->d) && (Hq == 1 || ht >= (T - 1) * tt + cache->d);
+    if (!heads_in && !tokens_in) return kErrArg;
+    if (!Q || !O || !q_start || !aligned16(Q) || !aligned16(O) || !aligned4(q_start) || !aligned4(seqs) || !aligned4(LSE))
+        return kErrArg;
+    rc = check_workspace(workspace, ws_bytes, paged_workspace_bytes(Hq / w.heads, max_q, cache->d, bf16));
+    if (rc != kOk) return rc;
+    rc = check_device();
+    if (rc != kOk) return rc;
+    const size_t es = bf16 ? 2 : 4;
+    PagedParams p = {};
+    p.gm.page_table = w.page_table;
+    p.gm.seq_lens = w.seq_lens;
+    p.gm.seqs = seqs;
+    p.gm.q_start = q_start;
+    p.gm.n = n;
+    p.gm.rows = w.rows;
+    p.gm.max_pages = w.max_pages;
+    p.gm.pages = w.pages;
+    p.gm.page_size = w.page_size;
+    p.gm.T = T;
+    p.gm.max_q = max_q;
+    p.gm.heads = w.heads;
+    p.gm.g = Hq / w.heads;
+    p.gm.causal = causal;
+    p.Q = Q;
+    p.K = static_cast<const char *>(cache->K) + layer * cache->layer_stride * es;
+    p.V = static_cast<const char *>(cache->V) + layer * cache->layer_stride * es;
+    p.O = O;
+    p.LSE = LSE;
+    p.q_token = q_token_stride;
+    p.q_head = q_head_stride;
+    p.o_token = o_token_stride;
+    p.o_head = o_head_stride;
+    p.page_stride = cache->page_stride;
+    p.head_stride = cache->head_stride;
+    p.slot_stride = cache->slot_stride;
+    p.d = cache->d;
+    p.Hq = Hq;
+    p.scale_log2 = scale * kPagedLog2e;
+    p.err = device_error_word();
+    if (!p.err) return kErrCuda;
+    const char *variant = "";
+    rc = launch_paged(p, bf16, workspace, static_cast<cudaStream_t>(stream), &variant);
+    if (rc == kOk) t_last_variant = variant;
+    return rc;
 }
 
 size_t attn_bwd_workspace_size(int B, int H, int N, int d) {

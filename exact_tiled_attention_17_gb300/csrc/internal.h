@@ -82,6 +82,33 @@ int launch_decode(const void *Q, const void *K, const void *V, void *O, float *L
                   int d, int causal, float scale, int bf16, const float *key_mask, void *workspace,
                   cudaStream_t stream);
 
+// Attention of new tokens over a paged cache (paged_*.cu); the parameters are
+// in paged.cuh.
+constexpr int kPagedMaxCtas = 640;    // CTAs a launch may use (sizes the workspace)
+struct PagedParams;
+size_t paged_workspace_bytes(int g, int max_q, int d, int bf16);
+int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant);
+
+// A paged cache as the page kernels see it (cache.cu): strides in 16-byte pieces.
+struct CacheView {
+    uint4 *k, *v;
+    int *page_table, *seq_lens, *ref_counts;
+    int layers, pages, heads, page_size, rows, max_pages;
+    long long layer_vecs, page_vecs, head_stride_vecs, slot_stride_vecs;
+    int block_vecs;   // a page of one layer
+    int slot_vecs;    // distance of two slots of one head
+    int row_vecs;     // one head's row of a slot
+};
+size_t cache_workspace_bytes(int pages, int n);
+int launch_cache_reserve(const CacheView &c, const int *seqs, const int *n_new, int n, int *granted, void *ws,
+                         cudaStream_t stream);
+int launch_cache_free(const CacheView &c, const int *seqs, const int *keep, int n, cudaStream_t stream);
+int launch_cache_fork(const CacheView &c, const int *parents, const int *children, int n, int copy, int *granted, void *ws,
+                      cudaStream_t stream);
+int launch_cache_compact(const CacheView &c, int *table_out, int *refs_out, int *n_live, void *ws, cudaStream_t stream);
+int launch_cache_append(const CacheView &c, int layer, const void *Kn, const void *Vn, long long token_vecs,
+                        long long head_vecs, int T, const int *seqs, const int *q_start, int n, cudaStream_t stream);
+
 // FP32 backward on the CUDA cores (bwd_f32.cu); workspace: B*H*N floats.
 int launch_bwd_f32(const float *Q, const float *K, const float *V, const float *O, const float *dO, const float *LSE,
                    float *dQ, float *dK, float *dV, int B, int H, int N, int d, int causal, float scale,

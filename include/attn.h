@@ -242,6 +242,143 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
                     const float *key_mask, void *workspace, size_t ws_bytes, void *stream);
 
 /*
+ * Paged key/value cache — decode and prompt chunks against a cache whose
+ * sequences differ in length, share pages and grow token by token: the
+ * attention of attn_fwd ("Is Flash Attention Stable?" §II-A) for new tokens,
+ * with the tutorial's rule for joining blocks wherever a sequence's keys are
+ * split, and the operators that hand out, copy and release the pages.
+ *
+ * attn_cache_t describes one cache; all memory is the caller's.
+ *   K, V         pools of pages.  Element (layer l, page p, kv head h, slot s,
+ *                column c) lies at l * layer_stride + p * page_stride +
+ *                h * head_stride + s * slot_stride + c, in elements; K and V
+ *                have the same strides.  The heads * page_size * d elements of
+ *                a page of one layer are one contiguous block, head by head
+ *                (head_stride = page_size * d, slot_stride = d) or token by
+ *                token (slot_stride = heads * d, head_stride = d).  Blocks do
+ *                not overlap.  Bases 16-byte aligned, strides multiples of 16
+ *                bytes.
+ *   dtype        ATTN_BF16 or ATTN_F32;  d in {32, 64, 96, 128};
+ *   page_size    tokens to a page: 16, 32, 64, 128 or 256.
+ *   page_table   [seqs][max_pages] int: the page of tokens page_size * k ..
+ *                of each sequence, -1 where it has none.
+ *   seq_lens     [seqs] int: tokens of each sequence, those reserved included.
+ *   ref_counts   [pages] int, 16-byte aligned: table entries that name each
+ *                page; 0 = free.
+ * A new cache has page_table all -1, seq_lens and ref_counts 0.  Slots at and
+ * past a sequence's length may hold anything, NaN included; what lies before
+ * it must be finite.
+ *
+ * Lists (seqs, n_new, parents, ...) are int arrays in device memory.  Every
+ * decision is taken on the device: no call waits for the host, and all can
+ * be captured into a graph.  An index that is out of range (a sequence, a
+ * page named in the table, a token range) is never followed: that entry is
+ * left out, and the next attn_status() returns ATTN_ERR_ARG.  So is a sequence
+ * that a list names again, where the operator would change it twice (the
+ * first mention counts).  n = 0 is allowed and does nothing.
+ *
+ * Calls on one cache are ordered by the caller (one stream, or events).  A
+ * workspace belongs to one call until that call's work has run: calls that
+ * can overlap, and graphs that can replay at the same time, need one each.
+ */
+typedef struct {
+    void *K, *V;
+    int *page_table, *seq_lens, *ref_counts;
+    int dtype, layers, pages, heads, page_size, d, seqs, max_pages;
+    long long layer_stride, page_stride, head_stride, slot_stride;
+} attn_cache_t;
+
+/* Bytes of device workspace (16-byte aligned) for attn_cache_reserve, _fork
+ * and _compact with lists of up to n entries; 0 for invalid arguments. */
+size_t attn_cache_workspace_size(int pages, int n);
+
+/*
+ * attn_cache_reserve — room for n_new[i] more tokens in sequence seqs[i]: the
+ * sequence gets the pages it lacks (free ones, lowest number first, in list
+ * order) and its length grows by n_new[i].  Entries are granted in list order
+ * as long as the free pages last; one that needs more pages than are left, or
+ * than its table row has, gets nothing and keeps its length (so do later ones
+ * that need pages).  granted: [n] int, written: 1 or 0.  Asynchronous.
+ */
+int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_new, int n, int *granted,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * attn_cache_free — cuts sequence seqs[i] to its first keep[i] tokens (keep
+ * NULL: none; more than it has: no change).  Pages past them leave the table
+ * and lose a reference.  Asynchronous.
+ */
+int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep, int n, void *stream);
+
+/*
+ * attn_cache_fork — sequence children[i], which must hold no tokens, becomes
+ * a copy of sequence parents[i] as it was before the call.  copy = 0: it
+ * shares the parent's full pages, and a partly filled last page is copied to
+ * a free page, so that both can grow.  copy = 1: every page is copied.
+ * Copies are taken in every layer, of the slots that hold tokens.  Pages are
+ * handed out as by attn_cache_reserve; granted: [n] int, written.  A child
+ * that is not empty is refused (granted 0, and attn_status reports
+ * ATTN_ERR_ARG).  Asynchronous.
+ */
+int attn_cache_fork(const attn_cache_t *cache, const int *parents, const int *children, int n, int copy, int *granted,
+                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * attn_cache_compact — moves the live pages together at the bottom of the
+ * pool: with L live pages, the k-th free page below L takes the k-th live page
+ * at or above L (all layers), and table and reference counts follow.
+ * page_table_out, ref_counts_out: the new tables; each may be the cache's own
+ * (in place) or other memory of the same size and alignment.  Only pages that
+ * were free are written, so with other memory the old tables stay valid until
+ * the caller drops them (a step in flight may still read through them).
+ * n_live: one int in device memory, written: L.  Asynchronous.
+ */
+int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_counts_out, int *n_live,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * attn_cache_append — writes the keys and values of new tokens of one layer.
+ * Entry i of the list is sequence seqs[i] (NULL: sequence i) with the tokens
+ * q_start[i] .. q_start[i+1] - 1 of Knew / Vnew; they are the sequence's last
+ * tokens, so the room was reserved before.  Element (token t, head h, column
+ * c) of Knew and Vnew lies at t * token_stride + h * head_stride + c (bases
+ * 16-byte aligned, strides multiples of 16 bytes), T tokens in all; tokens
+ * outside q_start[0] .. q_start[n] - 1 are not read.  q_start: [n + 1], not
+ * decreasing.  Asynchronous.
+ */
+int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
+                      long long head_stride, int T, const int *seqs, const int *q_start, int n, void *stream);
+
+/*
+ * attn_paged_fwd — attention of new tokens over one layer of a paged cache.
+ * Entry i of the list is sequence seqs[i] (NULL: sequence i); its new tokens
+ * are rows q_start[i] .. q_start[i+1] - 1 of Q, the last tokens of the
+ * sequence (their keys and values are in the cache already).  With len the
+ * sequence's length and n_i its new tokens, token t sees keys j <= len - n_i +
+ * t (causal = 1) or every key j < len (causal = 0).  Hq query heads read
+ * cache->heads kv heads: query head j reads head j / (Hq / heads); Hq must be
+ * a multiple, at most 64 to a head.
+ *
+ * Q, O: T rows; element (token t, head j, column c) at t * token_stride +
+ * j * head_stride + c, of the cache's dtype (bases 16-byte aligned, strides
+ * multiples of 16 bytes).  LSE: [T][Hq] float32 natural log, or NULL.  Rows
+ * outside q_start[0] .. q_start[n] - 1 are left as they were.  A row that
+ * sees no key gives O = 0, LSE = -inf.  max_q: at least the largest n_i (T
+ * always is); an entry with more is left out.  A table entry that names no
+ * page of the pool counts as page_size keys that no row sees.
+ *
+ * bf16: scores, softmax and sums in float32, probabilities rounded to bf16
+ * for the product with V; d in {32, 64, 96, 128}.  float32: IEEE float32
+ * throughout.  workspace: at least attn_paged_workspace_size(Hq, heads,
+ * max_q, d, dtype) bytes, 16-byte aligned.  Asynchronous: two launches.
+ */
+size_t attn_paged_workspace_size(int Hq, int heads, int max_q, int d, int dtype);
+int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE, long long q_token_stride,
+                   long long q_head_stride, long long o_token_stride, long long o_head_stride, int T, int Hq,
+                   const int *seqs, const int *q_start, int n, int max_q, int causal, float scale, void *workspace,
+                   size_t ws_bytes, void *stream);
+
+/*
  * attn_bwd — gradients of exact attention: for O = softmax(Q K^T * scale +
  * mask) V ("Is Flash Attention Stable?" §II-A) and an upstream gradient dO,
  * dQ, dK and dV.  As the yadro-code.ru FlashAttention tutorial describes for
@@ -328,8 +465,8 @@ int attn_emul_round(const double *x, double *y, long long n, int mbits, int ebit
 /*
  * attn_status — waits for `stream`, then returns ATTN_ERR_DEVICE_TIMEOUT if a
  * kernel of this library recorded a timed-out wait since the last call,
- * ATTN_ERR_ARG if attn_emul_fwd met an out-of-range row id, and clears the
- * record; ATTN_ERR_CUDA if the stream reports a CUDA error, else ATTN_OK.
+ * ATTN_ERR_ARG if attn_emul_fwd met an out-of-range row id or a paged-cache
+ * operator an index that it left out, and clears the record; ATTN_ERR_CUDA if the stream reports a CUDA error, else ATTN_OK.
  */
 int attn_status(void *stream);
 

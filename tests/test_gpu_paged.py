@@ -1,0 +1,552 @@
+"""The paged key/value cache on the GPU: attention of new tokens against the
+definition in float64 (bounds derived in paged_ref.py), the page operators
+against plain integers, and both together as a server uses them."""
+import math
+import random
+
+import pytest
+import torch
+
+from paged_ref import Pages, check_attention
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def eta():
+    import exact_tiled_attention_17_gb300 as m
+    return m
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def pools(layers, pages, heads, page, d, dtype, layout):
+    """K and V, all NaN."""
+    if layout == "head":
+        kv = [torch.full((layers, pages, heads, page, d), math.nan, dtype=dtype, device="cuda") for _ in range(2)]
+    elif layout == "token":
+        kv = [torch.full((layers, pages, page, heads, d), math.nan, dtype=dtype, device="cuda").transpose(2, 3)
+              for _ in range(2)]
+    elif layout == "side":      # K and V of a page side by side
+        t = torch.full((layers, pages, 2, heads, page, d), math.nan, dtype=dtype, device="cuda")
+        kv = [t[:, :, 0], t[:, :, 1]]
+    else:                       # layers inside a page
+        kv = [torch.full((pages, layers, heads, page, d), math.nan, dtype=dtype, device="cuda").transpose(0, 1)
+              for _ in range(2)]
+    return kv
+
+
+def build(eta, lens, heads, page, d, dtype=BF16, layout="head", layers=1, spare=3, seed=0, size=1.0, max_pages=None):
+    """A cache whose rows hold sequences of the given lengths on random pages;
+    every slot that holds no token is NaN."""
+    rng, g = random.Random(seed), torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + spare
+    cols = max_pages or max(need + [1]) + 1
+    order = list(range(pages))
+    rng.shuffle(order)
+    table = torch.full((len(lens), cols), -1, dtype=torch.int32)
+    refs = torch.zeros(pages, dtype=torch.int32)
+    k, v = pools(layers, pages, heads, page, d, dtype, layout)
+    for r, n in enumerate(lens):
+        for c in range(need[r]):
+            p = order.pop()
+            table[r, c], refs[p] = p, 1
+            m = min(page, n - c * page)
+            for t in (k, v):
+                t[:, p, :, :m] = (size * torch.randn((layers, heads, m, d), generator=g, device="cuda")).to(dtype)
+    return eta.PagedCache(k, v, table.cuda(), ints(lens), refs.cuda())
+
+
+def queries(T, Hq, d, dtype, seed=0, size=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed + 99)
+    return (size * torch.randn((T, Hq, d), generator=g, device="cuda")).to(dtype)
+
+
+def starts(new):
+    v = [0]
+    for n in new:
+        v.append(v[-1] + n)
+    return v
+
+
+def attend(eta, cache, new, g, seqs=None, causal=True, layer=0, seed=0, before=0, behind=0, size=1.0, max_q=None, scale=None,
+           out=None, **kw):
+    """Runs attn_paged_fwd over a list, with rows of Q before and behind it, and checks every row."""
+    T = sum(new) + before + behind
+    Hq = cache.heads * g
+    q = queries(T, Hq, cache.d, cache.dtype, seed, size)
+    o = out if out is not None else torch.full_like(q, 7.0)
+    lse = torch.full((T, Hq), 7.0, device="cuda")
+    held = (o.clone(), lse.clone())
+    qs = ints([before + x for x in starts(new)])
+    sq = None if seqs is None else ints(seqs)
+    eta.attn_paged_fwd(q, cache, layer, sq, qs, max_q=max_q or max(max(new), 1), causal=causal, scale=scale, out=o, lse=lse, **kw)
+    torch.cuda.synchronize()
+    assert eta.attn_status() == eta.ATTN_OK
+    check_attention(q, cache, layer, sq, qs, causal, scale if scale is not None else 1 / math.sqrt(cache.d), o, lse, held)
+
+
+# lengths (with the new tokens) and new tokens of a batch
+BATCHES = {
+    "one": ([1], [1]),
+    "decode": ([1, 15, 16, 17, 63, 64, 65, 129, 300], [1] * 9),
+    "few": ([5, 200, 33, 64, 7], [5, 3, 2, 1, 4]),
+    "chunk": ([40, 200, 129, 90], [40, 77, 129, 1]),
+    "empty": ([0, 70, 0, 3, 20], [0, 0, 2, 5, 0]),       # no tokens; more new tokens than the sequence holds
+}
+
+
+@pytest.mark.parametrize("batch", BATCHES)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,heads,g,d,page,layout", [
+    (BF16, 2, 4, 128, 16, "head"), (BF16, 1, 1, 64, 32, "token"), (BF16, 3, 3, 96, 64, "head"), (BF16, 2, 8, 32, 128, "token"),
+    (BF16, 1, 16, 128, 256, "side"), (BF16, 2, 5, 64, 16, "layers"), (BF16, 1, 64, 64, 16, "head"), (BF16, 4, 2, 128, 64, "token"),
+    (F32, 2, 4, 128, 16, "head"), (F32, 1, 1, 64, 32, "token"), (F32, 3, 3, 96, 64, "side"), (F32, 1, 7, 32, 128, "layers"),
+    (F32, 1, 64, 64, 16, "head"), (F32, 2, 16, 128, 256, "token"),
+])
+def test_attention(eta, batch, causal, dtype, heads, g, d, page, layout):
+    lens, new = BATCHES[batch]
+    cache = build(eta, lens, heads, page, d, dtype, layout, layers=2, seed=len(lens))
+    attend(eta, cache, new, g, causal=causal, layer=1, before=1, behind=2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,new", [(5000, 1), (5000, 4), (4097, 33), (2000, 500), (1023, 1023), (9000, 129)])
+def test_long_and_split(eta, dtype, n, new):
+    """Long axes, which several CTAs share, beside short sequences; large scores."""
+    cache = build(eta, [n, 3, n // 3], 2, 16, 64, dtype, seed=n)
+    new2 = [new, 1, min(new, n // 3)]
+    attend(eta, cache, new2, 4, seed=n)
+    cache = build(eta, [n], 1, 64, 128, dtype, seed=n + 1, size=4.0)
+    attend(eta, cache, [new], 2, seed=n, size=4.0)
+
+
+def test_many_sequences(eta):
+    """More list entries than a block has threads."""
+    lens = [(7 * i) % 90 for i in range(1300)]
+    new = [1 + (i % 3) if i % 5 else 0 for i in range(1300)]
+    cache = build(eta, lens, 1, 16, 64, BF16, seed=5)
+    attend(eta, cache, new, 2, seqs=list(reversed(range(1300))))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 40])
+def test_a_sequence_twice_and_rows_in_any_order(eta, dtype, new):
+    cache = build(eta, [100, 64, 81, 200], 2, 32, 64, dtype)
+    attend(eta, cache, [new] * 5, 4, seqs=[3, 1, 3, 0, 2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 100])
+def test_strides(eta, dtype, new):
+    """Q as a slice of a fused projection, O head by head."""
+    lens, nn = [300, 120], [new, 100]
+    cache = build(eta, lens, 2, 16, 64, dtype)
+    T, Hq, d = sum(nn), 8, 64
+    fused = queries(T, Hq + 4, d, dtype)
+    q = fused[:, 2:2 + Hq]
+    o = torch.full((Hq, T, d), 7.0, dtype=dtype, device="cuda").transpose(0, 1)
+    qs = ints(starts(nn))
+    o2, lse = eta.attn_paged_fwd(q, cache, 0, None, qs, out=o)
+    torch.cuda.synchronize()
+    assert o2 is o and eta.attn_status() == eta.ATTN_OK
+    check_attention(q, cache, 0, None, qs, True, 0.125, o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 70])
+def test_offsets_past_32_bits(eta, dtype, new):
+    """Pages further apart than 2^31 elements."""
+    page, heads, d = 16, 1, 64
+    far = (1 << 31) // (2 if dtype == F32 else 1) + 1024 * 64
+    raw = torch.empty(far + 4096, dtype=dtype, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = raw.as_strided((1, 2, heads, page, d), (0, far, page * d, d, 1))
+    raw[:1024].normal_(generator=g)
+    raw[far:far + 1024].normal_(generator=g)
+    raw2 = torch.empty(far + 4096, dtype=dtype, device="cuda")
+    v2 = raw2.as_strided((1, 2, heads, page, d), (0, far, page * d, d, 1))
+    v2.copy_(k.flip(3))
+    cache = eta.PagedCache(k, v2, ints([[1, 0]]), ints([27]), ints([1, 1]))
+    attend(eta, cache, [min(new, 27)], 4)
+    kn = queries(5, heads, d, dtype, 3)
+    eta.attn_cache_append(cache, 0, kn, -kn, None, ints([0, 5]))
+    torch.cuda.synchronize()
+    for t in range(5):
+        pos = 22 + t
+        assert torch.equal(k[0, [1, 0][pos // 16], :, pos % 16], kn[t])
+        assert torch.equal(v2[0, [1, 0][pos // 16], :, pos % 16], -kn[t])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 60])
+def test_pages_that_do_not_exist(eta, dtype, new):
+    """A table entry outside the pool counts as keys that no row sees, and is reported."""
+    cache = build(eta, [200, 90], 2, 16, 64, dtype)
+    cache.page_table[0, 3] = cache.pages
+    cache.page_table[0, 12] = -5
+    cache.page_table[1, 0] = 2 ** 30
+    q = queries(2 * new, 8, 64, dtype)
+    qs = ints([0, new, 2 * new])
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, qs)
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert eta.attn_status() == eta.ATTN_OK
+    check_attention(q, cache, 0, None, qs, True, 0.125, o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 60])
+def test_bad_entries_are_left_out(eta, dtype, new):
+    cache = build(eta, [200, 90, 77], 2, 16, 64, dtype)
+    q = queries(5 * new, 8, 64, dtype)
+    o, lse = torch.full_like(q, 7.0), torch.full((5 * new, 8), 7.0, device="cuda")
+    qs = [new * i for i in range(6)]
+    eta.attn_paged_fwd(q, cache, 0, ints([0, 9, 1, -1, 2]), ints(qs), max_q=new, out=o, lse=lse)
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    for i, s in enumerate([0, None, 1, None, 2]):
+        a, b = qs[i], qs[i + 1]
+        if s is None:
+            assert (o[a:b] == 7).all() and (lse[a:b] == 7).all()
+        else:
+            check_attention(q[a:b], cache, 0, ints([s]), ints([0, b - a]), True, 0.125, o[a:b], lse[a:b])
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_scores_of_any_size(eta, new):
+    """Scores far above 2^8 apart and all equal: the running maximum must follow."""
+    cache = build(eta, [400], 1, 16, 64, BF16, size=1.0)
+    ids = cache.page_table[0, :25].long()
+    ramp = torch.arange(400, device="cuda", dtype=torch.float32).reshape(25, 1, 16, 1) * 0.05
+    cache.k[0, ids] = ramp.expand(25, 1, 16, 64).to(BF16)     # every query with a positive sum prefers the last keys
+    attend(eta, cache, [new], 2, size=3.0)
+    cache.k[0, ids] = -ramp.expand(25, 1, 16, 64).to(BF16)
+    attend(eta, cache, [new], 2, size=3.0)
+    cache.k[0, ids] = 0.0
+    attend(eta, cache, [new], 2)
+
+
+def test_streams_and_graphs(eta):
+    """A call on another stream; a captured one replayed after the lengths changed."""
+    cache = build(eta, [500, 40, 300], 2, 16, 128, BF16, spare=30, max_pages=40)
+    q = queries(3, 8, 128, BF16)
+    qs = ints([0, 1, 2, 3])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1, stream=side)
+    side.synchronize()
+    check_attention(q, cache, 0, None, qs, True, 128 ** -0.5, o, lse)
+    kn, vn = queries(3, 2, 128, BF16, 1), queries(3, 2, 128, BF16, 2)
+    seqs, one = ints([0, 1, 2]), ints([1, 1, 1])
+    ref = Pages(cache)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        granted = eta.attn_cache_reserve(cache, seqs, one)
+        eta.attn_cache_append(cache, 0, kn, vn, seqs, qs)
+        o, lse = eta.attn_paged_fwd(q, cache, 0, seqs, qs, max_q=1)
+    for step in range(20):
+        kn.normal_()
+        vn.normal_()
+        q.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert granted.tolist() == ref.reserve([0, 1, 2], [1, 1, 1]) == [1, 1, 1]
+        if step in (0, 7, 19):
+            check_attention(q, cache, 0, seqs, qs, True, 128 ** -0.5, o, lse)
+    ref.check(cache)
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype,new", [(BF16, 1), (BF16, 30), (BF16, 300), (F32, 1), (F32, 100)])
+def test_repeated_runs_are_bitwise_equal(eta, dtype, new):
+    cache = build(eta, [3000, 700], 2, 16, 128, dtype)
+    q = queries(2 * new, 8, 128, dtype)
+    qs = ints([0, new, 2 * new])
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, qs)
+    for _ in range(10):
+        a, b = eta.attn_paged_fwd(q, cache, 0, None, qs)
+        assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+def test_refusals(eta):
+    cache = build(eta, [20, 20], 2, 16, 64)
+    q, qs = queries(2, 4, 64, BF16), ints([0, 1, 2])
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q.float(), cache, 0, None, qs)
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q[..., :32], cache, 0, None, qs)
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q, cache, 0, ints([0]), qs)
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q, cache, 0, None, qs.long())
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q, cache, 0, None, qs, out=torch.empty_like(q)[:1])
+    with pytest.raises(ValueError):
+        eta.attn_cache_append(cache, 0, q, q, None, qs)
+    for bad in (dict(layer=1), dict(max_q=3), dict(scale=-1.0), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+        kw = dict(layer=0)
+        kw.update(bad)
+        layer = kw.pop("layer")
+        with pytest.raises(eta.AttnError):
+            eta.attn_paged_fwd(q, cache, layer, None, qs, **kw)
+    with pytest.raises(ValueError):
+        eta.PagedCache(cache.k, cache.v, cache.page_table, cache.seq_lens, ints([0]))
+    with pytest.raises(ValueError):
+        eta.PagedCache(cache.k, cache.v.float(), cache.page_table, cache.seq_lens, cache.ref_counts)
+    o, _ = eta.attn_paged_fwd(q[:0], cache, 0, None, ints([0, 0, 0]))
+    assert o.shape == (0, 4, 64)
+
+
+# ---------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------
+def new_cache(eta, pages, page, seqs, max_pages, layers=2, heads=2, d=32, dtype=BF16, token_major=False):
+    c = eta.PagedCache.empty(layers, pages, heads, page, d, seqs, max_pages, dtype, "cuda", token_major)
+    c.k.normal_()
+    c.v.normal_()
+    return c
+
+
+def check_copies(cache, before, copies):
+    """The pools after a call: the copied slots, and everything else as it was."""
+    for now, was in zip((cache.k, cache.v), before):
+        want = was.clone()
+        for s, t, n in copies:
+            want[:, t, :, :n] = was[:, s, :, :n]
+        assert torch.equal(now, want)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_pages_against_plain_integers(eta, seed):
+    """A long run of random operators, each checked: tables, counts, grants, contents."""
+    rng = random.Random(seed)
+    rows, page = rng.choice([5, 40]), rng.choice([16, 32, 64, 128, 256])
+    pages = rng.choice([7, 60, 300])
+    cache = new_cache(eta, pages, page, rows, rng.choice([4, 30]), layers=rng.choice([1, 3]), heads=rng.choice([1, 3]),
+                      d=rng.choice([32, 64, 96, 128]), dtype=rng.choice([BF16, F32]), token_major=rng.random() < 0.5)
+    ref = Pages(cache)
+    for _ in range(25):
+        n = rng.randint(1, 8)
+        some = rng.sample(range(rows), min(n, rows))
+        before = (cache.k.clone(), cache.v.clone())
+        ref.copies = []
+        op = rng.choice(["reserve", "reserve", "free", "fork", "fork", "compact"])
+        if op == "reserve":
+            add = [rng.choice([0, 1, 5, page, rng.randint(0, 4 * page)]) for _ in some]
+            got = eta.attn_cache_reserve(cache, ints(some), ints(add))
+            assert got.tolist() == ref.reserve(some, add)
+        elif op == "free":
+            keep = None if rng.random() < 0.4 else [rng.choice([0, 1, page, rng.randint(0, 4 * page)]) for _ in some]
+            eta.attn_cache_free(cache, ints(some), None if keep is None else ints(keep))
+            ref.free(some, keep)
+        elif op == "fork":
+            empty = [r for r in range(rows) if ref.lens[r] == 0]
+            kids = rng.sample(empty, min(n, len(empty)))
+            if not kids:
+                continue
+            par, copy = [rng.randrange(rows) for _ in kids], rng.random() < 0.5
+            got = eta.attn_cache_fork(cache, ints(par), ints(kids), copy=copy)
+            assert got.tolist() == ref.fork(par, kids, copy)
+        else:
+            if rng.random() < 0.5:
+                _, _, live = eta.attn_cache_compact(cache)
+                assert live.tolist() == [ref.compact()]
+            else:
+                was = (cache.page_table.clone(), cache.ref_counts.clone())
+                table, refs, live = eta.attn_cache_compact(cache, inplace=False)
+                assert torch.equal(cache.page_table, was[0]) and torch.equal(cache.ref_counts, was[1])
+                assert live.tolist() == [ref.compact()]
+                cache.page_table.copy_(table)
+                cache.ref_counts.copy_(refs)
+        ref.check(cache)
+        ref.consistent()
+        check_copies(cache, before, ref.copies)
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+@pytest.mark.parametrize("pages", [1, 16, 17, 16384, 16385, 70001])
+def test_pools_of_any_size(eta, pages):
+    """The scan over the reference counts: its steps, its tail, a pool that is used up."""
+    rng = random.Random(pages)
+    cols = min(pages, 3000)
+    cache = eta.PagedCache.empty(1, pages, 1, 16, 32, 40, cols)
+    cache.ref_counts.copy_(ints([1 if rng.random() < 0.7 else 0 for _ in range(pages)]))
+    ref = Pages(cache)
+    seqs = rng.sample(range(40), 30)
+    for _ in range(3):
+        add = [rng.randint(0, max(16 * pages // 60, 1)) for _ in seqs]
+        assert eta.attn_cache_reserve(cache, ints(seqs), ints(add)).tolist() == ref.reserve(seqs, add)
+        ref.check(cache)
+    eta.attn_cache_free(cache, ints(seqs[:10]))
+    ref.free(seqs[:10])
+    # pages no table names go, so that compaction's table is whole
+    cache.ref_counts.zero_()
+    names = cache.page_table[cache.page_table >= 0].long()
+    cache.ref_counts[names] = 1
+    ref.refs = cache.ref_counts.tolist()
+    _, _, live = eta.attn_cache_compact(cache)
+    assert live.tolist() == [ref.compact()]
+    ref.check(cache)
+
+
+def test_long_lists(eta):
+    """More list entries than the planning block has threads."""
+    cache = eta.PagedCache.empty(1, 5000, 1, 16, 32, 2500, 4)
+    ref = Pages(cache)
+    rng = random.Random(3)
+    seqs = rng.sample(range(2500), 2400)
+    add = [rng.randint(0, 40) for _ in seqs]
+    assert eta.attn_cache_reserve(cache, ints(seqs), ints(add)).tolist() == ref.reserve(seqs, add)
+    ref.check(cache)
+    eta.attn_cache_free(cache, ints(seqs[:1500]))
+    ref.free(seqs[:1500])
+    ref.check(cache)
+    kids = [r for r in range(2500) if ref.lens[r] == 0][:1300]
+    par = [rng.randrange(2500) for _ in kids]
+    assert eta.attn_cache_fork(cache, ints(par), ints(kids)).tolist() == ref.fork(par, kids, False)
+    ref.check(cache)
+
+
+def test_refused_entries(eta):
+    """Sequences named twice, out of range, too long for their row; children that hold tokens."""
+    cache = new_cache(eta, 12, 16, 6, 4)
+    ref = Pages(cache)
+
+    def status(code):
+        assert eta.attn_status() == code
+
+    assert eta.attn_cache_reserve(cache, ints([0, 1, 0, 7, -1, 2]), ints([20, 65, 5, 5, 5, 64])).tolist() == [1, 0, 0, 0, 0, 1]
+    status(eta.ATTN_ERR_ARG)
+    ref.reserve([0, 1, 0, 7, -1, 2], [20, 65, 5, 5, 5, 64])
+    ref.check(cache)
+    assert eta.attn_cache_reserve(cache, ints([3, 4, 5]), ints([64, 64, 0])).tolist() == ref.reserve([3, 4, 5], [64, 64, 0])
+    ref.check(cache)
+    status(eta.ATTN_OK)
+    assert eta.attn_cache_reserve(cache, ints([5]), ints([-3])).tolist() == [0]
+    status(eta.ATTN_ERR_ARG)
+    # the child holds tokens; the child is named twice; out of range; a child of a child that is empty before the call
+    par, kid = [0, 2, 0, 0, 9, 1], [2, 1, 1, 8, 4, 5]
+    assert eta.attn_cache_fork(cache, ints(par), ints(kid)).tolist() == ref.fork(par, kid, False)
+    status(eta.ATTN_ERR_ARG)
+    ref.check(cache)
+    assert ref.lens[1] == 64 and ref.lens[5] == 0
+    eta.attn_cache_free(cache, ints([1, 1, 77]), ints([3, 0, 0]))
+    status(eta.ATTN_ERR_ARG)
+    ref.free([1, 1, 77], [3, 0, 0])
+    ref.check(cache)
+    assert ref.lens[1] == 3
+    # an entry that names no page of the pool
+    cache.page_table[0, 1] = 12
+    eta.attn_cache_free(cache, ints([0]))
+    status(eta.ATTN_ERR_ARG)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("layout", ["head", "token", "side", "layers"])
+@pytest.mark.parametrize("d,heads", [(32, 1), (64, 5), (96, 2), (128, 3)])
+def test_append(eta, dtype, layout, d, heads):
+    lens, new = [3, 40, 16, 33, 5, 70], [3, 17, 1, 0, 5, 70]
+    cache = build(eta, lens, heads, 16, d, dtype, layout, layers=2)
+    T = sum(new) + 3
+    kv = queries(T, 2 * heads, d, dtype)
+    kn, vn = kv[:, :heads], kv[:, heads:]
+    order = [2, 0, 5, 3, 1, 4]
+    qs = [1 + x for x in starts([new[r] for r in order])]
+    want = [cache.k.clone(), cache.v.clone()]
+    table = cache.page_table.tolist()
+    for i, r in enumerate(order):
+        for t in range(qs[i], qs[i + 1]):
+            pos = lens[r] - new[r] + t - qs[i]
+            want[0][1, table[r][pos // 16], :, pos % 16] = kn[t]
+            want[1][1, table[r][pos // 16], :, pos % 16] = vn[t]
+    eta.attn_cache_append(cache, 1, kn, vn, ints(order), ints(qs))
+    assert eta.attn_status() == eta.ATTN_OK
+    assert torch.equal(cache.k.nan_to_num(9.0), want[0].nan_to_num(9.0))
+    assert torch.equal(cache.v.nan_to_num(9.0), want[1].nan_to_num(9.0))
+
+
+def test_append_bad_places(eta):
+    """Tokens without a place are dropped and reported; the others are written."""
+    cache = build(eta, [20, 4, 30], 2, 16, 64)
+    cache.page_table[2, 1] = cache.pages + 1
+    kn = queries(30, 2, 64, BF16)
+    want = cache.k.clone()
+    table = cache.page_table.tolist()
+    qs = [0, 2, 8, 10, 14, 16]           # 6 new tokens of a sequence of 4; row 7; row 2's page 1; row 0 again
+    for t in range(2):
+        want[0, table[0][(18 + t) // 16], :, (18 + t) % 16] = kn[t]
+    for t in range(4):
+        want[0, table[1][0], :, t] = kn[4 + t]
+    eta.attn_cache_append(cache, 0, kn, kn, ints([0, 1, 7, 2, 0]), ints(qs))
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert torch.equal(cache.k.nan_to_num(9.0), want.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("dtype,token_major", [(BF16, False), (F32, True)])
+def test_a_server_for_a_while(eta, dtype, token_major):
+    """Prompts in chunks, decoding, forks that go their own ways, rejected
+    tokens, sequences that leave, compaction: after every step each sequence's
+    attention is that of its own tokens, kept beside the cache."""
+    rng = random.Random(11)
+    layers, heads, g, d, page = 2, 2, 4, 64, 16
+    cache = new_cache(eta, 90, page, 10, 30, layers, heads, d, dtype, token_major)
+    book = {}        # row -> per layer (k, v) [tokens, heads, d], what the sequence should hold
+
+    def step(rows, new):
+        qs = ints(starts(new))
+        got = eta.attn_cache_reserve(cache, ints(rows), ints(new))
+        assert got.tolist() == [1] * len(rows)
+        for layer in range(layers):
+            kn = torch.randn((sum(new), heads, d), device="cuda").to(dtype)
+            vn = torch.randn((sum(new), heads, d), device="cuda").to(dtype)
+            for i, r in enumerate(rows):
+                a, b = sum(new[:i]), sum(new[:i + 1])
+                k0, v0 = book.setdefault(r, [(kn[:0], vn[:0])] * layers)[layer]
+                book[r] = list(book[r])
+                book[r][layer] = (torch.cat([k0, kn[a:b]]), torch.cat([v0, vn[a:b]]))
+            eta.attn_cache_append(cache, layer, kn, vn, ints(rows), qs)
+            q = torch.randn((sum(new), heads * g, d), device="cuda").to(dtype)
+            o, lse = eta.attn_paged_fwd(q, cache, layer, ints(rows), qs, max_q=max(new))
+            check_attention(q, cache, layer, ints(rows), qs, True, d ** -0.5, o, lse)
+
+    def check():
+        lens = cache.seq_lens.tolist()
+        for r in range(10):
+            n = len(book[r][0][0]) if r in book else 0
+            assert lens[r] == n
+            for layer in range(layers if n else 0):
+                ids = cache.page_table[r, :-(-n // page)].long()
+                for pool, want in zip((cache.k, cache.v), book[r][layer]):
+                    assert torch.equal(pool[layer, ids].transpose(1, 2).reshape(-1, heads, d)[:n], want)
+        assert eta.attn_status() == eta.ATTN_OK
+
+    step([0, 1, 2], [40, 17, 100])
+    step([0, 1, 2], [33, 1, 60])
+    check()
+    assert eta.attn_cache_fork(cache, ints([0, 0, 2]), ints([3, 4, 5])).tolist() == [1, 1, 1]
+    book[3], book[4], book[5] = list(book[0]), list(book[0]), list(book[2])
+    check()
+    for _ in range(18):
+        step([0, 1, 2, 3, 4, 5], [1] * 6)
+    check()
+    keep = {r: len(book[r][0][0]) - rng.randint(0, 3) for r in (1, 3, 5)}
+    eta.attn_cache_free(cache, ints(list(keep)), ints(list(keep.values())))
+    for r, n in keep.items():
+        book[r] = [(k[:n], v[:n]) for k, v in book[r]]
+    step([1, 3, 5, 0], [5, 2, 3, 1])
+    check()
+    eta.attn_cache_free(cache, ints([0, 2]))
+    del book[0], book[2]
+    check()
+    _, _, live = eta.attn_cache_compact(cache)
+    n_live = int(live)
+    assert (cache.ref_counts[:n_live] > 0).all() and (cache.ref_counts[n_live:] == 0).all()
+    check()
+    assert eta.attn_cache_fork(cache, ints([4]), ints([0]), copy=True).tolist() == [1]
+    book[0] = list(book[4])
+    step([0, 4, 5, 1], [20, 1, 1, 7])
+    check()
