@@ -107,6 +107,64 @@ bool make_bf16_rows_map(CUtensorMap *m, const void *base, int D, int N, int BH, 
     return true;
 }
 
+namespace {
+// Maps encoded before, by everything that goes into one: a map depends on
+// nothing else, so a hit is as good as a new one.  Direct-mapped.
+struct MapKey {
+    const void *base;
+    long long dev_rank;
+    cuuint64_t dims[5], strides[4];
+    cuuint32_t box[6];   // (one spare word: no padding to compare)
+};
+struct AnyMapEntry {
+    MapKey key;
+    CUtensorMap map;
+    bool used;
+};
+constexpr unsigned kAnyMaps = 1024;
+AnyMapEntry g_any_maps[kAnyMaps];
+std::mutex g_any_maps_mu;
+}  // namespace
+
+bool make_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box) {
+    int dev = 0;
+    if (rank < 1 || rank > 5 || cudaGetDevice(&dev) != cudaSuccess) return false;
+    MapKey k;
+    memset(&k, 0, sizeof(k));
+    k.base = base;
+    k.dev_rank = 8LL * dev + rank;
+    for (int i = 0; i < rank; ++i) {
+        k.dims[i] = dims[i];
+        k.box[i] = box[i];
+        // a dimension of one element may come with any stride: give it a valid one
+        if (i > 0) k.strides[i - 1] = dims[i] > 1 ? strides[i - 1] : 16 * ((dims[0] * 2 + 15) / 16);
+    }
+    uint64_t h = 1469598103934665603ull;
+    const uint64_t *words = reinterpret_cast<const uint64_t *>(&k);
+    for (size_t i = 0; i < sizeof(k) / 8; ++i) h = (h ^ words[i]) * 1099511628211ull;
+    AnyMapEntry &e = g_any_maps[(h >> 32) % kAnyMaps];
+    {
+        std::lock_guard<std::mutex> lk(g_any_maps_mu);
+        if (e.used && memcmp(&e.key, &k, sizeof(k)) == 0) {
+            *m = e.map;
+            return true;
+        }
+    }
+    EncodeTiledFn enc = encode_tiled_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
+    if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), k.dims, k.strides,
+            k.box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    std::lock_guard<std::mutex> lk(g_any_maps_mu);
+    e.key = k;
+    e.map = *m;
+    e.used = true;
+    return true;
+}
+
 int *device_error_word() {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -538,6 +596,10 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     const long long per = bf16 ? 8 : 4;
     for (long long s : {q_token_stride, q_head_stride, o_token_stride, o_head_stride})
         if (s < 0 || s % per) return kErrArg;
+    // the tensor maps of the bf16 path take strides below 2^40 bytes, and rows of Q that differ
+    for (long long s : {q_token_stride, q_head_stride, o_token_stride, o_head_stride, cache->page_stride})
+        if (s >= (1LL << 38)) return kErrUnsupported;
+    if ((T > 1 && q_token_stride == 0) || (Hq > 1 && q_head_stride == 0)) return kErrArg;
     if (T == 0 || n == 0) return kOk;
     if (max_q <= 0 || max_q > T) return kErrArg;
     // rows of O must not overlap: one of the strides steps over all of the other's range

@@ -28,6 +28,12 @@ EncodeTiledFn encode_tiled_fn();
 // past N read as zero and are dropped on store.
 bool make_bf16_rows_map(CUtensorMap *m, const void *base, int D, int N, int BH, int box_rows);
 
+// Tensor map of a bf16 tensor of any rank up to 5 (dims innermost first,
+// strides in bytes of dims 1 ..) for 128-byte-swizzled boxes; what lies out of
+// range reads as zero.
+bool make_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box);
+
 // Error-word bit set by the emulation kernel for an out-of-range row id
 // (timed-out waits use the low bits).
 constexpr int kErrWordBadRow = 1 << 24;
@@ -85,6 +91,7 @@ int launch_decode(const void *Q, const void *K, const void *V, void *O, float *L
 // Attention of new tokens over a paged cache (paged_*.cu); the parameters are
 // in paged.cuh.
 constexpr int kPagedMaxCtas = 640;    // CTAs a launch may use (sizes the workspace)
+constexpr int kPagedMaxTcCtas = 160;  // the tensor-core path: one per SM
 struct PagedParams;
 size_t paged_workspace_bytes(int g, int max_q, int d, int bf16);
 int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant);

@@ -180,6 +180,7 @@ int launch_paged_merge(const PagedParams &p, int bf16, int ctas, cudaStream_t st
 
 // The variants (each sets its own unit size, partial layout and grid).
 int launch_paged_simt(PagedParams p, int bf16, void *workspace, cudaStream_t stream);
+int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
 
 // Workspace: headers, m, l, o for `ctas` CTAs and units of `rows` rows.
 inline size_t paged_partial_bytes(int ctas, int rows, int d) {

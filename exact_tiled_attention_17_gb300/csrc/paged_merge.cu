@@ -130,9 +130,21 @@ int launch_paged_merge(const PagedParams &p, int bf16, int ctas, cudaStream_t st
     }
 }
 
-size_t paged_workspace_bytes(int, int, int d, int) { return paged_partial_bytes(kPagedMaxCtas, 64, d); }
+namespace {
+// Whether a call takes the tensor cores: bf16, and more rows to an entry than
+// the kernel for few rows holds.
+bool takes_tc(int g, int max_q, int bf16) { return bf16 && static_cast<long long>(g) * max_q > 16; }
+}  // namespace
+
+size_t paged_workspace_bytes(int g, int max_q, int d, int bf16) {
+    return takes_tc(g, max_q, bf16) ? paged_partial_bytes(kPagedMaxTcCtas, 256, d) : paged_partial_bytes(kPagedMaxCtas, 64, d);
+}
 
 int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant) {
+    if (takes_tc(p.gm.g, p.gm.max_q, bf16)) {
+        if (variant) *variant = p.d <= 64 ? "paged_tc_bf16_d64" : "paged_tc_bf16_d128";
+        return launch_paged_tc(p, workspace, stream);
+    }
     if (variant) *variant = bf16 ? "paged_simt_bf16" : "paged_simt_f32";
     return launch_paged_simt(p, bf16, workspace, stream);
 }

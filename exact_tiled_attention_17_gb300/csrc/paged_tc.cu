@@ -1,0 +1,619 @@
+// Attention of a chunk of new tokens over a paged cache, bf16 in / f32
+// accumulate, on the tcgen05 tensor cores of sm_103a.
+//
+// What it computes: O = softmax(scale Q K^T) V and the row's LSE for the units
+// of paged_index.h: one kv head, a block of new tokens, all g query heads that
+// share the head.  A unit's rows are packed (token, head of the group) into
+// two 128-row query tiles of 128 / g tokens each, so K and V are streamed once
+// for the whole group and short chunks still fill the matrix instructions.
+//
+// Mapping, as in the contiguous forward: one persistent CTA per SM,
+//   warps 0 .. 15  softmax: two warpgroups per query tile, each with half of
+//                  the tile's 64-key halves of S and of O's columns, one
+//                  thread per row; running maximum m (moved only when a tile
+//                  exceeds it by 2^8, so O is rescaled rarely) and float32
+//                  sum l of the unrounded p; P as bf16 over S in tensor memory.
+//   warp 16        TMA producer: Q tiles, then K_j, V_j into a ring of slots.
+//                  A tile is gathered page by page: one box of min(page, 128)
+//                  rows by 64 columns per copy, the table entries of the next
+//                  tile already fetched while the warp waits.
+//   warp 17        MMA issuer: S_q = Q_q K_j^T, O_q += P_q V_j.
+// The work of all units is cut into equal shares, one to a CTA, which may
+// begin and end inside a unit; cut units are joined by the merge kernel.
+//
+// Pages that do not exist, and whole pages past the end, are copied from an
+// out-of-range page coordinate, which fills zeros.  Slots past the end inside
+// the last page may hold anything: the producer waits for that V tile itself
+// and zeroes them before it hands the tile on (a masked p = 0 times NaN would
+// be NaN); masked scores are replaced, never added to.
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace eta {
+namespace {
+
+constexpr float kThresh = 8.0f;   // the reference maximum moves by at least this (log2 units)
+constexpr float kNegInfP = -__builtin_huge_valf();
+
+template <int DP>   // padded head dimension: 64 or 128
+struct PtcShape {
+    static constexpr int NQ = 2, BR = 128, BC = 128;
+    static constexpr int CB = DP / 64;
+    static constexpr int Q_BYTES = BR * DP * 2;
+    static constexpr int SLOT_BYTES = BC * DP * 2;
+    static constexpr int XCH_BYTES = NQ * 2 * 128 * 8;
+    static constexpr int NS_RAW = (222 * 1024 - NQ * Q_BYTES - XCH_BYTES) / SLOT_BYTES;
+    static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
+    static constexpr int SOFTMAX_WARPS = 16, WARP_TMA = 16, WARP_MMA = 17;
+    static constexpr int THREADS = 18 * 32;
+    static constexpr int OFF_RING = NQ * Q_BYTES;
+    static constexpr int OFF_XCH = OFF_RING + NS * SLOT_BYTES;
+    static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
+    static constexpr int BAR_QFULL = 0;
+    static constexpr int BAR_FULL = BAR_QFULL + NQ;
+    static constexpr int BAR_EMPTY = BAR_FULL + NS;
+    static constexpr int BAR_SFULL = BAR_EMPTY + NS;
+    static constexpr int BAR_PFULL = BAR_SFULL + NQ;
+    static constexpr int BAR_OFULL = BAR_PFULL + NQ;
+    static constexpr int BAR_QFREE = BAR_OFULL + NQ;
+    static constexpr int BAR_OFREE = BAR_QFREE + NQ;
+    static constexpr int BAR_DONE = BAR_OFREE + NQ;
+    static constexpr int BAR_TAIL = BAR_DONE + 1;
+    static constexpr int NBARS = BAR_TAIL + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;          // tensor-memory address, abort flag
+    static constexpr int OFF_BADP = OFF_MISC + 16;                // per K tile (mod 8): missing pages, bit per 16 keys
+    static constexpr int OFF_PLAN = OFF_BADP + 32;
+    static constexpr int SMEM_MIN = OFF_PLAN + static_cast<int>(sizeof(PagedPlan)) + 1024;
+    // (all of tensor memory is allocated: a second resident CTA would wait for it)
+    static constexpr int SMEM_BYTES = SMEM_MIN <= 116 * 1024 ? 117 * 1024 : SMEM_MIN;
+    __host__ __device__ static constexpr int s_col(int q) { return q * BC; }
+    __host__ __device__ static constexpr int o_col(int q) { return NQ * BC + q * DP; }
+    static_assert(NS >= 4 && SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(NQ * (BC + DP) <= 512, "tensor memory");
+    static_assert(OFF_PLAN % 8 == 0, "alignment");
+};
+
+template <int DP>
+__global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+    using S = PtcShape<DP>;
+    constexpr int NQ = S::NQ, BC = S::BC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const PagedGeom &gm = p.gm;
+    auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_MISC + 4);
+    volatile uint32_t *bad_pages = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_BADP);
+    PagedPlan *plan = reinterpret_cast<PagedPlan *>(smem + S::OFF_PLAN);
+    const uint32_t sQ = sbase, sRing = sbase + S::OFF_RING;
+
+    if (threadIdx.x == 0) {
+        for (int q = 0; q < NQ; ++q) {
+            mbar_init(bar(S::BAR_QFULL + q), 1);
+            mbar_init(bar(S::BAR_SFULL + q), 1);
+            mbar_init(bar(S::BAR_PFULL + q), 256);
+            mbar_init(bar(S::BAR_OFULL + q), 1);
+            mbar_init(bar(S::BAR_QFREE + q), 1);
+            mbar_init(bar(S::BAR_OFREE + q), 256);
+        }
+        for (int s = 0; s < S::NS; ++s) {
+            mbar_init(bar(S::BAR_FULL + s), 1);
+            mbar_init(bar(S::BAR_EMPTY + s), 1);
+        }
+        mbar_init(bar(S::BAR_DONE), 1);
+        mbar_init(bar(S::BAR_TAIL), 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == S::WARP_MMA) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 2) paged_write_header(p, 2 * cta + threadIdx.x, PagedHdr{0, 0, 0, 0});
+    paged_plan<S::THREADS>(p, plan, cta, gridDim.x);
+
+    const int tpt = 128 / gm.g;   // tokens to a query tile
+    PagedWalk w;
+    w.start(plan);
+    // K/V tiles of the part that query tile q takes part in: the first nkv
+    // (causal tiles of earlier tokens end earlier); 0 when it has no rows.
+    auto tiles_of = [&](int q) -> int {
+        const int t0 = w.tok0(gm) + q * tpt, t1 = min(w.tok0(gm) + w.ntok(gm), t0 + tpt);
+        if (t1 <= t0) return 0;
+        const int keys = paged_visible(gm, w.e, t1 - 1);
+        const int tiles = keys <= BC ? 1 : (keys + BC - 1) / BC;
+        return max(0, min(tiles, w.tile1) - w.tile0);
+    };
+
+    if (warp >= S::SOFTMAX_WARPS) {
+        auto wwait = [&](uint32_t b, uint32_t parity, int site) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
+        };
+        const bool leader = elect_one();
+        if (warp == S::WARP_TMA) {
+            // --------------------------------------------------------------
+            // TMA producer.  Lane b * CB + c copies box b (box_rows keys),
+            // column block c, of a tile.
+            // --------------------------------------------------------------
+            if (leader) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+            }
+            const int box_rows = min(gm.page_size, BC);
+            const int boxes = BC / box_rows;
+            const int my_box = lane / S::CB, my_cb = lane % S::CB;
+            const uint64_t pol_q = l2_policy_evict_first();
+            int t = 0, tails = 0, kt = 0;
+            int uo[NQ] = {0, 0};
+            bool ok = true;
+            while (ok && w.next(gm)) {
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    if (tiles_of(q) == 0) continue;
+                    if (uo[q] > 0 && !wwait(bar(S::BAR_QFREE + q), (uo[q] - 1) & 1, 4)) ok = false;
+                    if (ok && leader) {
+                        mbar_arrive_expect_tx(bar(S::BAR_QFULL + q), S::CB * 128 * gm.g * tpt);
+#pragma unroll
+                        for (int cb = 0; cb < S::CB; ++cb)
+                            tma_load_3d_hint(sQ + q * S::Q_BYTES + cb * (S::BR * 128), &tm_q, bar(S::BAR_QFULL + q), cb * 64,
+                                             w.h * gm.g, w.e.q0 + w.tok0(gm) + q * tpt, pol_q);
+                    }
+                    ++uo[q];
+                }
+                // page of box my_box of tile j: -1 past the end (no keys), -2 missing
+                auto lookup = [&](int j) -> int {
+                    const int key = j * BC + my_box * box_rows;
+                    if (my_box >= boxes || key >= w.e.len) return -1;
+                    const int id = paged_page(gm, w.e.seq, key / gm.page_size);
+                    return id < 0 ? -2 : id;
+                };
+                int next = lookup(w.tile0);
+                for (int j = w.tile0; ok && j < w.tile1; ++j, ++kt) {
+                    const int id = next;
+                    if (j + 1 < w.tile1) next = lookup(j + 1);
+                    const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
+                    const int x = my_cb * 64, slot0 = (j * BC + my_box * box_rows) & (gm.page_size - 1);
+                    const int pg = id < 0 ? gm.pages : id;   // out of range: zeros
+                    const bool mine = my_box < boxes;
+                    const uint32_t dst = my_cb * (BC * 128) + my_box * box_rows * 128;
+                    // rows of V to clear: past the end, in a page that was copied
+                    const int key0 = j * BC;
+                    const int clear0 = w.e.len - key0;
+                    const int clear1 = min(BC, (clear0 + box_rows - 1) / box_rows * box_rows);
+                    const bool tail = clear0 > 0 && clear0 < BC && clear1 > clear0;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++t) {
+                        const int slot = t % S::NS, round = t / S::NS;
+                        if (round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, 1)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t full = bar(kv == 1 && tail ? S::BAR_TAIL : S::BAR_FULL + slot);
+                        if (leader) {
+                            if (kv == 0) {
+                                // one bit for each 16 keys
+                                uint32_t bits = 0;
+                                if (missing) {
+                                    atomicOr(p.err, kErrWordBadRow);
+                                    for (int b = 0; b < boxes; ++b)
+                                        if ((missing >> (b * S::CB)) & 1u)
+                                            bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
+                                }
+                                bad_pages[kt & 7] = bits;
+                            }
+                            mbar_arrive_expect_tx(full, S::SLOT_BYTES);
+                        }
+                        __syncwarp();
+                        if (mine)
+                            tma_load_4d(sRing + slot * S::SLOT_BYTES + dst, kv ? &tm_v : &tm_k, full, x, slot0, w.h, pg);
+                        if (kv == 1 && tail) {
+                            if (!wwait(bar(S::BAR_TAIL), tails & 1, 6)) ok = false;
+                            ++tails;
+                            // 128-byte rows (the swizzle stays inside a row)
+                            for (int i = lane; i < (clear1 - clear0) * 8 * S::CB; i += 32) {
+                                const int c = i / ((clear1 - clear0) * 8), r = i % ((clear1 - clear0) * 8);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 sRing + slot * S::SLOT_BYTES + c * (BC * 128) + clear0 * 128 + r * 16),
+                                             "r"(0u)
+                                             : "memory");
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (leader) mbar_arrive(bar(S::BAR_FULL + slot));
+                        }
+                    }
+                }
+            }
+            // every copy this warp started has landed before the CTA may exit
+            for (int tt = max(0, t - S::NS); tt < t; ++tt) wwait(bar(S::BAR_FULL + tt % S::NS), (tt / S::NS) & 1, 2);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+                if (uo[q] > 0) wwait(bar(S::BAR_QFULL + q), (uo[q] - 1) & 1, 3);
+            __syncwarp();
+        } else {
+            // --------------------------------------------------------------
+            // MMA issuer (one elected lane); the order of the contiguous
+            // forward: P_0 V_j, S_0(j+1), P_1 V_j, S_1(j+1).
+            // --------------------------------------------------------------
+            constexpr uint32_t idesc_s = idesc_bf16_f32(128, BC, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(128, DP, false, true);
+            const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024);
+            const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
+            const uint64_t vdesc0 = sdesc_sw128(sRing, BC * 128, 1024);
+            const int ksteps = p.d / 16;
+            int t_base = 0;
+            int sq[NQ] = {0, 0}, uo[NQ] = {0, 0};
+            auto commit = [&](int b) {
+                if (leader) tc_commit(bar(b));
+            };
+            bool ok = true;
+            while (ok && w.next(gm)) {
+                int nkv[NQ];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) nkv[q] = tiles_of(q);
+                const int nkv_max = w.tile1 - w.tile0;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+                    if (ok && nkv[q] > 0) ok = wwait(bar(S::BAR_QFULL + q), uo[q] & 1, 10);
+                if (!ok) break;
+                auto full_wait = [&](int tt, int site) -> bool {
+                    const int tg = t_base + tt;
+                    if (!wwait(bar(S::BAR_FULL + tg % S::NS), (tg / S::NS) & 1, site)) return false;
+                    tc_fence_after();
+                    return true;
+                };
+                auto slot_of = [&](int tt) { return S::BAR_EMPTY + (t_base + tt) % S::NS; };
+                auto issue_s = [&](int q, int j, int nkvq) {
+                    const uint64_t a0 = qdesc0 + static_cast<uint64_t>((q * S::Q_BYTES) >> 4);
+                    const uint64_t b0 = kdesc0 + static_cast<uint64_t>((((t_base + 2 * j) % S::NS) * S::SLOT_BYTES) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk) {
+                            if (kk >= ksteps) break;
+                            const int cb = kk >> 2, off = (kk & 3) * 32;
+                            mma_bf16_ss(tmem + S::s_col(q), a0 + static_cast<uint64_t>((cb * (S::BR * 128) + off) >> 4),
+                                        b0 + static_cast<uint64_t>((cb * (BC * 128) + off) >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        tc_commit(bar(S::BAR_SFULL + q));
+                    }
+                    if (j == nkvq - 1) commit(S::BAR_QFREE + q);
+                };
+                auto issue_pv = [&](int q, int j) {
+                    const uint64_t b0 = vdesc0 + static_cast<uint64_t>((((t_base + 2 * j + 1) % S::NS) * S::SLOT_BYTES) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < BC / 16; ++kk)
+                            mma_bf16_ts(tmem + S::o_col(q), tmem + S::s_col(q) + (kk / 4) * 64 + (kk % 4) * 8,
+                                        b0 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                    }
+                };
+                auto wait_p = [&](int q, int j) -> bool {
+                    if (j == 0 && uo[q] > 0 && !wwait(bar(S::BAR_OFREE + q), (uo[q] - 1) & 1, 16)) return false;
+                    if (!wwait(bar(S::BAR_PFULL + q), (sq[q] + j) & 1, 13)) return false;
+                    tc_fence_after();
+                    return true;
+                };
+                ok = full_wait(0, 11);
+                if (ok) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+                        if (nkv[q] > 0) issue_s(q, 0, nkv[q]);
+                    commit(slot_of(0));
+                }
+                for (int j = 0; ok && j < nkv_max; ++j) {
+                    if (!full_wait(2 * j + 1, 12)) {
+                        ok = false;
+                        break;
+                    }
+                    bool k_ready = false;
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (!ok || j >= nkv[q]) continue;
+                        if (wait_p(q, j)) issue_pv(q, j);
+                        else ok = false;
+                        if (!ok) continue;
+                        if (j == nkv[q] - 1) commit(S::BAR_OFULL + q);
+                        if (j + 1 < nkv[q]) {
+                            if (!k_ready) {
+                                if (!full_wait(2 * j + 2, 14)) {
+                                    ok = false;
+                                    continue;
+                                }
+                                k_ready = true;
+                            }
+                            issue_s(q, j + 1, nkv[q]);
+                        }
+                    }
+                    commit(slot_of(2 * j + 1));
+                    if (k_ready) commit(slot_of(2 * j + 2));
+                }
+                t_base += 2 * nkv_max;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    sq[q] += nkv[q];
+                    uo[q] += nkv[q] > 0 ? 1 : 0;
+                }
+            }
+            commit(S::BAR_DONE);
+            wwait(bar(S::BAR_DONE), 0, 15);
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------------
+        // Softmax warpgroup h of query tile q.
+        // ------------------------------------------------------------------
+        const int q = warp >> 3, h = (warp >> 2) & 1, wq = warp & 3;
+        const int row_in = wq * 32 + lane;
+        const uint32_t t_lane = static_cast<uint32_t>(wq * 32) << 16;
+        const uint32_t tS = tmem + t_lane + S::s_col(q);
+        const uint32_t tO = tmem + t_lane + S::o_col(q);
+        const float sl2 = p.scale_log2;
+        constexpr int OC = DP / 64;   // 32-column chunks of O of this warpgroup
+        const int tok_in = q * tpt + row_in / gm.g, head_in = row_in % gm.g;
+        const bool slot_ok = row_in < tpt * gm.g;   // g need not divide 128
+        auto xch = [&](int hh) -> uint32_t { return sbase + S::OFF_XCH + ((q * 2 + hh) * 128 + row_in) * 8; };
+        auto pair_sync = [&]() { named_bar_sync(7 + q, 256); };
+        auto exchange = [&](float a, float &ao) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(xch(h)), "f"(a) : "memory");
+            pair_sync();
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ao) : "r"(xch(1 - h)) : "memory");
+        };
+        int sq = 0, uo = 0, kt = 0;
+        bool ok = true;
+        while (w.next(gm)) {
+            const int nkvq = tiles_of(q), ntok = w.ntok(gm);
+            const bool valid = slot_ok && tok_in < ntok;
+            const int vis = valid ? paged_visible(gm, w.e, w.tok0(gm) + tok_in) : 0;
+            // keys that every row of the tile sees
+            const int vis_all = q * tpt < ntok ? paged_visible(gm, w.e, w.tok0(gm) + q * tpt) : 0;
+            float m = kNegInfP, l = 0.f;
+            // (a wait that gives up is recorded and does not end the loop: every
+            // warp still takes part in every named barrier)
+            for (int j = 0; j < nkvq; ++j) {
+                if (!mbar_wait(bar(S::BAR_SFULL + q), (sq + j) & 1, abort_flag, p.err, 20)) ok = false;
+                tc_fence_after();
+                const int key0 = (w.tile0 + j) * BC;
+                const uint32_t bad = bad_pages[(kt + j) & 7];
+                const bool edge = key0 + BC > vis_all || bad != 0u;
+                uint32_t sr[2][32];
+                float mxc[2], mx = kNegInfP;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (edge) tmem_ld32(tS + h * 64 + 32 * c, sr[c]);
+                    else tmem_ld32_max(tS + h * 64 + 32 * c, sr[c], mxc[c]);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    reg_fence32(sr[c]);
+                    if (!edge) {
+                        reg_fence_f32(mxc[c]);
+                        mx = fmaxf(mx, mxc[c]);
+                    } else {
+                        const int first = key0 + h * 64 + 32 * c;
+                        // bits of this chunk's two 16-key groups
+                        const uint32_t b2 = (bad >> (4 * h + 2 * c)) & 3u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float x = __uint_as_float(sr[c][e]) * sl2;
+                            x = (first + e < vis && !((b2 >> (e >> 4)) & 1u)) ? x : kNegInfP;
+                            sr[c][e] = __float_as_uint(x);
+                            mx = fmaxf(mx, x);
+                        }
+                    }
+                }
+                if (!edge) mx *= sl2;
+                if (named_bar_red_or(7 + q, 256, valid && mx > m + kThresh)) {
+                    float mo;
+                    exchange(mx, mo);
+                    mx = fmaxf(mx, mo);
+                } else {
+                    mx = m;
+                }
+                const float m_new = (valid && mx > m + kThresh) ? mx : m;
+                const bool moved = m_new != m;
+                const float a = moved ? ex2(m - m_new) : 1.f;
+                m = m_new;
+                const float m_use = (m == kNegInfP) ? 0.f : m;
+                const uint64_t negm2 = f2_pack(-m_use, -m_use);
+                uint64_t ls2 = f2_pack(0.f, 0.f);
+                auto exps = [&](auto edge_c) {
+                    constexpr bool EDGE = decltype(edge_c)::value;
+                    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t xx = f2_pack(__uint_as_float(sr[c][2 * e]), __uint_as_float(sr[c][2 * e + 1]));
+                            uint64_t y;
+                            if constexpr (EDGE) y = f2_add(xx, negm2);
+                            else y = f2_fma(xx, sl2x2, negm2);
+                            float y0, y1;
+                            f2_unpack(y, y0, y1);
+                            const float p0 = ex2(y0), p1 = ex2(y1);
+                            pk[e] = pack_bf16x2(p0, p1);
+                            ls2 = f2_add(ls2, f2_pack(p0, p1));
+                        }
+                        tmem_st16(tS + h * 64 + 16 * c, pk);
+                    }
+                };
+                if (edge) exps(std::true_type{});
+                else exps(std::false_type{});
+                if (j > 0 && __any_sync(0xffffffffu, moved)) {
+                    const uint64_t a2 = f2_pack(a, a);
+#pragma unroll
+                    for (int c = h * OC; c < (h + 1) * OC; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * c, o);
+                        tmem_ld_wait();
+                        reg_fence32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float v0, v1;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2), v0, v1);
+                            o[e] = __float_as_uint(v0);
+                            o[e + 1] = __float_as_uint(v1);
+                        }
+                        tmem_st32(tO + 32 * c, o);
+                    }
+                }
+                float l0, l1;
+                f2_unpack(ls2, l0, l1);
+                l = l * a + (l0 + l1);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar(S::BAR_PFULL + q));
+            }
+            // ---------------- epilogue ----------------
+            const bool whole = w.whole();
+            float lo;
+            pair_sync();
+            exchange(l, lo);
+            l += lo;
+            pair_sync();
+            if (nkvq > 0 && ok) ok = mbar_wait(bar(S::BAR_OFULL + q), uo & 1, abort_flag, p.err, 21);
+            tc_fence_after();
+            const bool store = valid && !*abort_flag;
+            const bool any = l > 0.f;
+            const float scale_o = whole ? (any ? 1.f / l : 0.f) : 1.f;
+            const uint64_t inv2 = f2_pack(scale_o, scale_o);
+            const int unit_row = q * tpt * gm.g + row_in;
+            const size_t prow = static_cast<size_t>(w.slot(cta)) * p.part_rows + unit_row;
+            const long long tok = w.e.q0 + w.tok0(gm) + tok_in;
+            const int head = w.h * gm.g + head_in;
+            if (nkvq > 0) {
+                const long long at = valid ? tok * p.o_token + static_cast<long long>(head) * p.o_head : 0;
+#pragma unroll
+                for (int c = h * OC; c < (h + 1) * OC; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_ld_wait();
+                    reg_fence32(o);
+                    if (!store || 32 * c >= p.d) continue;
+                    if (whole) {
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + at + 32 * c;
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float v0, v1;
+                            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2), v0, v1);
+                            pk[e] = any ? pack_bf16x2(v0, v1) : 0u;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst + 8 * k), "r"(pk[4 * k]),
+                                         "r"(pk[4 * k + 1]), "r"(pk[4 * k + 2]), "r"(pk[4 * k + 3])
+                                         : "memory");
+                    } else {
+                        float *dst = p.part_o + prow * p.d + 32 * c;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst + 4 * k), "r"(o[4 * k]),
+                                         "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
+                                         : "memory");
+                    }
+                }
+            }
+            if (h == 0 && store) {
+                if (whole) {
+                    if (p.LSE) p.LSE[tok * p.Hq + head] = any ? (m + log2f(l)) * kPagedLn2 : kNegInfP;
+                } else {
+                    p.part_m[prow] = nkvq > 0 && any ? m : kNegInfP;
+                    p.part_l[prow] = l;
+                }
+            }
+            if (!whole && q == 0 && h == 0 && row_in == 0) paged_write_header(p, w.slot(cta), w.header(gm));
+            if (nkvq > 0) {
+                tc_fence_before();
+                mbar_arrive(bar(S::BAR_OFREE + q));
+            }
+            sq += nkvq;
+            uo += nkvq > 0 ? 1 : 0;
+            kt += w.tile1 - w.tile0;
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    if (warp == S::WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+
+template <int DP>
+int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
+    using S = PtcShape<DP>;
+    auto kern = paged_tc_kernel<DP>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return kErrCuda;
+    static std::atomic<int> sms[kMaxDev];   // 0: not set up yet
+    int nsm = sms[dev].load(std::memory_order_acquire);
+    if (nsm == 0) {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES) != cudaSuccess ||
+            cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return kErrCuda;
+        sms[dev].store(nsm, std::memory_order_release);
+    }
+    const PagedGeom &gm = p.gm;
+    const int tpt = 128 / gm.g;
+    CUtensorMap tq, tk, tv;
+    const int box = std::min(gm.page_size, S::BC);
+    const cuuint64_t qd[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(gm.T)};
+    const cuuint64_t qs[2] = {static_cast<cuuint64_t>(p.q_head) * 2, static_cast<cuuint64_t>(p.q_token) * 2};
+    const cuuint32_t qb[3] = {64u, static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tpt)};
+    const cuuint64_t kd[4] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(gm.page_size),
+                              static_cast<cuuint64_t>(gm.heads), static_cast<cuuint64_t>(gm.pages)};
+    const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.slot_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
+                              static_cast<cuuint64_t>(p.page_stride) * 2};
+    const cuuint32_t kb[4] = {64u, static_cast<cuuint32_t>(box), 1u, 1u};
+    if (!make_bf16_map(&tq, p.Q, 3, qd, qs, qb) || !make_bf16_map(&tk, p.K, 4, kd, ks, kb) ||
+        !make_bf16_map(&tv, p.V, 4, kd, ks, kb))
+        return kErrCuda;
+    const int ctas = std::min(nsm, kPagedMaxTcCtas);
+    p.gm.tpu = S::NQ * tpt;
+    p.gm.tk = S::BC;
+    p.gm.unit_cost = 3 * S::BC;
+    p.gm.min_share = 4 * S::BC;
+    paged_carve(p, workspace, ctas, S::NQ * 128);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(S::THREADS);
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
+    return launch_paged_merge(p, 1, ctas, stream);
+}
+
+}  // namespace
+
+int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream) {
+    return p.d <= 64 ? launch_dp<64>(p, workspace, stream) : launch_dp<128>(p, workspace, stream);
+}
+
+}  // namespace eta
