@@ -179,8 +179,14 @@ __device__ __forceinline__ PagedHdr paged_read_header(const PagedParams &p, int 
 int launch_paged_merge(const PagedParams &p, int bf16, int ctas, cudaStream_t stream);
 
 // The variants (each sets its own unit size, partial layout and grid).
-int launch_paged_simt(PagedParams p, int bf16, void *workspace, cudaStream_t stream);
+int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
+int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream);
+
+// Tensor maps of the bf16 kernels: Q in boxes of `tokens` tokens x g heads x 64
+// columns (rows token by token), K and V in boxes of `box` slots x 64 columns of
+// one page and head.
+bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
 
 // Workspace: headers, m, l, o for `ctas` CTAs and units of `rows` rows.
 inline size_t paged_partial_bytes(int ctas, int rows, int d) {

@@ -1,0 +1,474 @@
+// Attention of a few new tokens over a paged cache, bf16 in / f32 accumulate:
+// decoding, and the checking of a few drafted tokens.
+//
+// A unit (paged_index.h) is one kv head with up to 16, 32 or 64 query rows:
+// a few tokens times the g query heads that share the head.  The work is a
+// stream over K and V, a few FLOPs to a byte, so it is bound by HBM and the
+// kernel's job is to keep enough bytes in flight.  With g heads to a stream
+// the CUDA cores would not keep up (g * 2 FMAs to each element read), so both
+// products run on mma.sync with the rows padded to 16: at 16 rows that is
+// 16 * 4 FLOPs to a key's column, a small part of what the instruction can do.
+// tcgen05 would need 128-row tiles, of which these rows fill an eighth or less.
+//
+//   warp 4         TMA producer: gathers tiles of 64 keys, page by page, into a
+//                  ring of stages (K and V of a tile on one barrier), and the
+//                  next unit's Q rows.
+//   warps 0 .. 3   consumers.  S = Q K^T: warp w takes keys 16 w .. 16 w + 15.
+//                  One vote a tile whether some row's maximum exceeds its
+//                  reference by 2^8; only then do the warps exchange maxima and
+//                  rescale.  P goes through shared memory as bf16, and warp w
+//                  forms O += P V for its quarter of the columns.
+// Two barriers a tile among the four warps; with two CTAs on an SM one's
+// arithmetic covers the other's.
+//
+// Missing pages and pages past the end read as zeros (an out-of-range page
+// coordinate); masked scores are replaced by -inf, and V fragments of slots
+// past the end, which may hold NaN, are cleared in registers.
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "paged.cuh"
+
+namespace eta {
+namespace {
+
+constexpr float kThreshD = 8.0f;
+constexpr int kDecKeys = 64;
+
+template <int DP, int MT>   // padded head dimension, 16-row blocks of a unit
+struct PdShape {
+    static constexpr int CB = DP / 64;
+    static constexpr int ROWS = 16 * MT;
+    static constexpr int KV_BYTES = kDecKeys * DP * 2;
+    static constexpr int STAGE = 2 * KV_BYTES;
+    static constexpr int CTAS = MT == 4 ? 1 : 2;                    // per SM
+    static constexpr int QB = MT == 2 ? 1 : 2;                      // Q buffers
+    static constexpr int NS = (MT == 4 ? 5 : 3) * (DP == 64 ? 2 : 1) > 8 ? 8 : (MT == 4 ? 5 : 3) * (DP == 64 ? 2 : 1);
+    static constexpr int Q_BYTES = ROWS * DP * 2;
+    static constexpr int P_BYTES = ROWS * 128;
+    static constexpr int OFF_Q = NS * STAGE;
+    static constexpr int OFF_P = OFF_Q + QB * Q_BYTES;
+    static constexpr int OFF_MX = OFF_P + P_BYTES;                  // [4][ROWS] maxima
+    static constexpr int OFF_L = OFF_MX + 4 * ROWS * 4;             // [4][ROWS] sums
+    static constexpr int OFF_BAR = OFF_L + 4 * ROWS * 4;
+    static constexpr int BAR_FULL = 0, BAR_EMPTY = NS, BAR_QFULL = 2 * NS, BAR_QEMPTY = BAR_QFULL + QB;
+    static constexpr int OFF_MISC = OFF_BAR + (BAR_QEMPTY + QB) * 8;
+    static constexpr int OFF_BADP = OFF_MISC + 16;                  // per stage: missing pages, bit per 16 keys
+    static constexpr int OFF_PLAN = OFF_BADP + ((NS * 4 + 15) / 16) * 16;
+    static constexpr int SMEM_BYTES = OFF_PLAN + static_cast<int>(sizeof(PagedPlan)) + 1024;
+    static_assert(SMEM_BYTES <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int DP, int MT>
+__global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+    using S = PdShape<DP, MT>;
+    constexpr int NS = S::NS, CB = S::CB, ROWS = S::ROWS;
+    constexpr int KS = DP / 16;        // K steps of Q K^T
+    constexpr int NT = DP / 32;        // 8-column blocks of O to a warp
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+    const PagedGeom &gm = p.gm;
+    auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_MISC);
+    volatile uint32_t *bad_pages = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_BADP);
+    PagedPlan *plan = reinterpret_cast<PagedPlan *>(smem + S::OFF_PLAN);
+    float *mx_sh = reinterpret_cast<float *>(smem + S::OFF_MX);
+    float *l_sh = reinterpret_cast<float *>(smem + S::OFF_L);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(bar(S::BAR_FULL + s), 1);
+            mbar_init(bar(S::BAR_EMPTY + s), 4);
+        }
+        for (int b = 0; b < S::QB; ++b) {
+            mbar_init(bar(S::BAR_QFULL + b), 1);
+            mbar_init(bar(S::BAR_QEMPTY + b), 4);
+        }
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 4 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (threadIdx.x < 2) paged_write_header(p, 2 * cta + threadIdx.x, PagedHdr{0, 0, 0, 0});
+    paged_plan<160>(p, plan, cta, gridDim.x);
+    PagedWalk w;
+    w.start(plan);
+
+    if (warp == 4) {
+        // ------------------------------------------------------------------
+        // Producer.  Lane (kv, box, column block) issues that copy of a tile.
+        // ------------------------------------------------------------------
+        auto wwait = [&](uint32_t b, uint32_t parity, int site) -> bool {
+            return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
+        };
+        const int box_rows = min(gm.page_size, kDecKeys);
+        const int boxes = kDecKeys / box_rows;
+        const int my_kv = lane / (boxes * CB), my_box = lane / CB % boxes, my_cb = lane % CB;
+        const bool mine = lane < 2 * boxes * CB;
+        const uint32_t dst = my_kv * S::KV_BYTES + my_cb * (kDecKeys * 128) + my_box * box_rows * 128;
+        int t = 0, u = 0;
+        bool ok = true;
+        while (ok && w.next(gm)) {
+            const int qb = u % S::QB;
+            if (u >= S::QB && !wwait(bar(S::BAR_QEMPTY + qb), (u / S::QB - 1) & 1, 50)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(S::BAR_QFULL + qb), CB * 128 * gm.g * gm.tpu);
+#pragma unroll
+                for (int cb = 0; cb < CB; ++cb)
+                    tma_load_3d(sbase + S::OFF_Q + qb * S::Q_BYTES + cb * (ROWS * 128), &tm_q, bar(S::BAR_QFULL + qb), cb * 64,
+                                w.h * gm.g, w.e.q0 + w.tok0(gm));
+            }
+            ++u;
+            auto lookup = [&](int j) -> int {   // page of this lane's box: -1 past the end, -2 missing
+                const int key = j * kDecKeys + my_box * box_rows;
+                if (!mine || key >= w.e.len) return -1;
+                const int id = paged_page(gm, w.e.seq, key / gm.page_size);
+                return id < 0 ? -2 : id;
+            };
+            // table entries two tiles ahead
+            int next0 = lookup(w.tile0), next1 = w.tile0 + 1 < w.tile1 ? lookup(w.tile0 + 1) : -1;
+            for (int j = w.tile0; j < w.tile1; ++j, ++t) {
+                const int id = next0;
+                next0 = next1;
+                if (j + 2 < w.tile1) next1 = lookup(j + 2);
+                const int st = t % NS;
+                if (t >= NS && !wwait(bar(S::BAR_EMPTY + st), (t / NS - 1) & 1, 51)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_kv == 0 && my_cb == 0);
+                if (lane == 0) {
+                    uint32_t bits = 0;
+                    if (missing) {
+                        atomicOr(p.err, kErrWordBadRow);
+                        for (int b = 0; b < boxes; ++b)
+                            if ((missing >> (b * CB)) & 1u) bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
+                    }
+                    bad_pages[st] = bits;
+                    mbar_arrive_expect_tx(bar(S::BAR_FULL + st), S::STAGE);
+                }
+                __syncwarp();
+                if (mine)
+                    tma_load_4d(sbase + st * S::STAGE + dst, my_kv ? &tm_v : &tm_k, bar(S::BAR_FULL + st), my_cb * 64,
+                                (j * kDecKeys + my_box * box_rows) & (gm.page_size - 1), w.h, id < 0 ? gm.pages : id);
+            }
+        }
+        // every copy has landed before this warp leaves
+        for (int tt = max(0, t - NS); tt < t; ++tt) wwait(bar(S::BAR_FULL + tt % NS), (tt / NS) & 1, 52);
+        for (int uu = max(0, u - S::QB); uu < u; ++uu) wwait(bar(S::BAR_QFULL + uu % S::QB), (uu / S::QB) & 1, 53);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------
+        // Consumers
+        // ------------------------------------------------------------------
+        const float sl2 = p.scale_log2;
+        const int quad = lane >> 2, col2 = (lane & 3) * 2, mat = lane >> 3;
+        const int a_row = lane & 15, a_chunk = lane >> 4;             // ldmatrix lanes of an A fragment
+        const int k_row = warp * 16 + (mat >> 1) * 8 + (lane & 7), k_chunk = mat & 1;
+        const int v_row = (mat & 1) * 8 + (lane & 7), v_chunk = warp * (DP / 32) + (mat >> 1);
+        int t = 0, u = 0;
+        while (w.next(gm)) {
+            const int qb = u % S::QB;
+            mbar_wait(bar(S::BAR_QFULL + qb), (u / S::QB) & 1, abort_flag, p.err, 54);
+            const uint32_t sQ = sbase + S::OFF_Q + qb * S::Q_BYTES;
+            const uint32_t sP = sbase + S::OFF_P;
+            auto q_frag = [&](int mt, int kk, uint32_t (&a)[4]) {
+                const int r = mt * 16 + a_row;
+                ldsm4(sQ + (kk >> 2) * (ROWS * 128) + r * 128 + ((((kk & 3) * 2 + a_chunk) ^ (r & 7)) << 4), a);
+            };
+            uint32_t qf[MT == 1 ? KS : 1][4];
+            if constexpr (MT == 1) {
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) q_frag(0, kk, qf[kk]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));   // the next Q may overwrite it
+            }
+            const int ntok = w.ntok(gm), rows = ntok * gm.g;
+            int vis[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = mt * 16 + quad + 8 * i;
+                    vis[mt][i] = r < rows ? paged_visible(gm, w.e, w.tok0(gm) + r / gm.g) : 0;
+                }
+            const int vis_all = paged_visible(gm, w.e, w.tok0(gm));   // what every row sees
+            float m[MT][2], l[MT][2], o[MT][NT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    m[mt][i] = -INFINITY;
+                    l[mt][i] = 0.f;
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+            }
+            for (int j = w.tile0; j < w.tile1; ++j, ++t) {
+                const int st = t % NS;
+                mbar_wait(bar(S::BAR_FULL + st), (t / NS) & 1, abort_flag, p.err, 55);
+                const uint32_t sK = sbase + st * S::STAGE, sV = sK + S::KV_BYTES;
+                const int key0 = j * kDecKeys;
+                float s[MT][2][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    uint32_t b[4];
+                    ldsm4(sK + (kk >> 2) * (kDecKeys * 128) + k_row * 128 + ((((kk & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), b);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if constexpr (MT == 1) {
+                            mma16816(s[mt][0], qf[kk], b[0], b[1]);
+                            mma16816(s[mt][1], qf[kk], b[2], b[3]);
+                        } else {
+                            uint32_t a[4];
+                            q_frag(mt, kk, a);
+                            mma16816(s[mt][0], a, b[0], b[1]);
+                            mma16816(s[mt][1], a, b[2], b[3]);
+                        }
+                    }
+                }
+                // scaled and masked scores, and whether a maximum moves
+                const uint32_t bad = bad_pages[st];
+                const bool edge = key0 + kDecKeys > vis_all || bad != 0u;
+                const bool gone = (bad >> warp) & 1u;
+                float mx[MT][2];
+                bool move = false;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float x = s[mt][n][2 * i + e] * sl2;
+                                if (edge) x = (!gone && key0 + warp * 16 + n * 8 + col2 + e < vis[mt][i]) ? x : -INFINITY;
+                                s[mt][n][2 * i + e] = x;
+                            }
+                        float v = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                        mx[mt][i] = v;
+                        move = move || (vis[mt][i] > 0 && v > m[mt][i] + kThreshD);
+                    }
+                if (named_bar_red_or(1, 128, move)) {
+                    if ((lane & 3) == 0) {
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) mx_sh[warp * ROWS + mt * 16 + quad + 8 * i] = mx[mt][i];
+                    }
+                    named_bar_sync(1, 128);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float *at = mx_sh + mt * 16 + quad + 8 * i;
+                            const float v = fmaxf(fmaxf(at[0], at[ROWS]), fmaxf(at[2 * ROWS], at[3 * ROWS]));
+                            if (vis[mt][i] > 0 && v > m[mt][i] + kThreshD) {
+                                const float a = m[mt][i] == -INFINITY ? 0.f : ex2(m[mt][i] - v);
+                                m[mt][i] = v;
+                                l[mt][i] *= a;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    o[mt][n][2 * i] *= a;
+                                    o[mt][n][2 * i + 1] *= a;
+                                }
+                            }
+                        }
+                }
+                // P
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float mu = m[mt][i] == -INFINITY ? 0.f : m[mt][i];
+                        const int r = mt * 16 + quad + 8 * i;
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float p0 = ex2(s[mt][n][2 * i] - mu), p1 = ex2(s[mt][n][2 * i + 1] - mu);
+                            l[mt][i] += p0 + p1;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + r * 128 + (((warp * 2 + n) ^ (r & 7)) << 4) + col2 * 2),
+                                         "r"(pack_bf16x2(p0, p1))
+                                         : "memory");
+                        }
+                    }
+                named_bar_sync(1, 128);
+                // O += P V, this warp's columns
+                const int live = w.e.len - key0;   // slots of the tile that hold tokens
+#pragma unroll
+                for (int ks = 0; ks < kDecKeys / 16; ++ks) {
+                    uint32_t vf[NT / 2][4];
+#pragma unroll
+                    for (int n2 = 0; n2 < NT / 2; ++n2) {
+                        const int key = ks * 16 + v_row, chunk = v_chunk + 2 * n2;
+                        ldsm4t(sV + (chunk >> 3) * (kDecKeys * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), vf[n2]);
+                        if (live < kDecKeys) {
+                            // clear what lies past the end
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int k0 = ks * 16 + (e & 1) * 8 + col2;
+                                if (k0 >= live) vf[n2][e] = 0u;
+                                else if (k0 + 1 >= live) vf[n2][e] &= 0xFFFFu;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint32_t a[4];
+                        const int r = mt * 16 + a_row;
+                        ldsm4(sP + r * 128 + (((ks * 2 + a_chunk) ^ (r & 7)) << 4), a);
+#pragma unroll
+                        for (int n2 = 0; n2 < NT / 2; ++n2) {
+                            mma16816(o[mt][2 * n2], a, vf[n2][0], vf[n2][1]);
+                            mma16816(o[mt][2 * n2 + 1], a, vf[n2][2], vf[n2][3]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::BAR_EMPTY + st));
+            }
+            if constexpr (MT > 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));
+            }
+            ++u;
+            // ---------------- the unit's end ----------------
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
+                    l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
+                    if ((lane & 3) == 0) l_sh[warp * ROWS + mt * 16 + quad + 8 * i] = l[mt][i];
+                }
+            named_bar_sync(1, 128);
+            const bool whole = w.whole();
+            const int slot = w.slot(cta);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = mt * 16 + quad + 8 * i;
+                    if (r >= rows || *abort_flag) continue;
+                    const float *at = l_sh + r;
+                    const float L = (at[0] + at[ROWS]) + (at[2 * ROWS] + at[3 * ROWS]);
+                    const long long tok = w.e.q0 + w.tok0(gm) + r / gm.g;
+                    const int head = w.h * gm.g + r % gm.g;
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    const size_t prow = static_cast<size_t>(slot) * p.part_rows + r;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const int c = warp * (DP / 4) + n * 8 + col2;
+                        if (c >= p.d) continue;
+                        if (whole) {
+                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + tok * p.o_token +
+                                                 static_cast<long long>(head) * p.o_head + c;
+                            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(o[mt][n][2 * i] * inv, o[mt][n][2 * i + 1] * inv);
+                        } else {
+                            *reinterpret_cast<float2 *>(p.part_o + prow * p.d + c) = make_float2(o[mt][n][2 * i], o[mt][n][2 * i + 1]);
+                        }
+                    }
+                    if (warp == 0 && (lane & 3) == 0) {
+                        if (!whole) {
+                            p.part_m[prow] = L > 0.f ? m[mt][i] : -INFINITY;
+                            p.part_l[prow] = L;
+                        } else if (p.LSE) {
+                            p.LSE[tok * p.Hq + head] = L > 0.f ? (m[mt][i] + log2f(L)) * kPagedLn2 : -INFINITY;
+                        }
+                    }
+                }
+            if (!whole && threadIdx.x == 0) paged_write_header(p, slot, w.header(gm));
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+constexpr int kMaxDev = 64;
+std::mutex g_mu;
+
+template <int DP, int MT>
+int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
+    using S = PdShape<DP, MT>;
+    auto kern = paged_decode_kernel<DP, MT>;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return kErrCuda;
+    static std::atomic<int> grids[kMaxDev];   // CTAs that are resident at once; 0: not set up yet
+    int grid = grids[dev].load(std::memory_order_acquire);
+    if (grid == 0) {
+        std::lock_guard<std::mutex> lk(g_mu);
+        int nsm = 0, per = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES) != cudaSuccess ||
+            cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, 160, S::SMEM_BYTES) != cudaSuccess)
+            return kErrCuda;
+        grid = std::min(nsm * std::max(per, 1), kPagedMaxCtas);
+        grids[dev].store(grid, std::memory_order_release);
+    }
+    const PagedGeom &gm = p.gm;
+    p.gm.tpu = S::ROWS / gm.g;
+    p.gm.tk = kDecKeys;
+    p.gm.unit_cost = kDecKeys;
+    p.gm.min_share = 2 * kDecKeys;
+    CUtensorMap tq, tk, tv;
+    if (!paged_maps(p, S::ROWS / gm.g, std::min(gm.page_size, kDecKeys), &tq, &tk, &tv)) return kErrCuda;
+    paged_carve(p, workspace, grid, S::ROWS);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(160);
+    cfg.dynamicSmemBytes = S::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
+    return launch_paged_merge(p, 1, grid, stream);
+}
+
+}  // namespace
+
+int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(p.gm.max_q) * p.gm.g;
+    if (rows <= 16) return p.d <= 64 ? launch_one<64, 1>(p, workspace, stream) : launch_one<128, 1>(p, workspace, stream);
+    if (rows <= 32) return p.d <= 64 ? launch_one<64, 2>(p, workspace, stream) : launch_one<128, 2>(p, workspace, stream);
+    return p.d <= 64 ? launch_one<64, 4>(p, workspace, stream) : launch_one<128, 4>(p, workspace, stream);
+}
+
+}  // namespace eta

@@ -130,23 +130,47 @@ int launch_paged_merge(const PagedParams &p, int bf16, int ctas, cudaStream_t st
     }
 }
 
+bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv) {
+    const PagedGeom &gm = p.gm;
+    const cuuint64_t qd[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(gm.T)};
+    const cuuint64_t qs[2] = {static_cast<cuuint64_t>(p.q_head) * 2, static_cast<cuuint64_t>(p.q_token) * 2};
+    const cuuint32_t qb[3] = {64u, static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tokens)};
+    const cuuint64_t kd[4] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(gm.page_size),
+                              static_cast<cuuint64_t>(gm.heads), static_cast<cuuint64_t>(gm.pages)};
+    const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.slot_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
+                              static_cast<cuuint64_t>(p.page_stride) * 2};
+    const cuuint32_t kb[4] = {64u, static_cast<cuuint32_t>(box), 1u, 1u};
+    return make_bf16_map(tq, p.Q, 3, qd, qs, qb) && make_bf16_map(tk, p.K, 4, kd, ks, kb) &&
+           make_bf16_map(tv, p.V, 4, kd, ks, kb);
+}
+
 namespace {
-// Whether a call takes the tensor cores: bf16, and more rows to an entry than
-// the kernel for few rows holds.
-bool takes_tc(int g, int max_q, int bf16) { return bf16 && static_cast<long long>(g) * max_q > 16; }
+// The kernel of a call.  bf16: the stream kernel holds units of up to 64 rows
+// (tokens of an entry x query heads of a group); more rows are matrix work.
+enum class Path { kSimt, kDecode, kTc };
+Path path_of(int g, int max_q, int bf16) {
+    if (!bf16) return Path::kSimt;
+    return static_cast<long long>(g) * max_q <= 64 ? Path::kDecode : Path::kTc;
+}
 }  // namespace
 
 size_t paged_workspace_bytes(int g, int max_q, int d, int bf16) {
-    return takes_tc(g, max_q, bf16) ? paged_partial_bytes(kPagedMaxTcCtas, 256, d) : paged_partial_bytes(kPagedMaxCtas, 64, d);
+    if (path_of(g, max_q, bf16) == Path::kTc) return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
+    return paged_partial_bytes(kPagedMaxCtas, 64, d);
 }
 
 int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant) {
-    if (takes_tc(p.gm.g, p.gm.max_q, bf16)) {
-        if (variant) *variant = p.d <= 64 ? "paged_tc_bf16_d64" : "paged_tc_bf16_d128";
-        return launch_paged_tc(p, workspace, stream);
+    switch (path_of(p.gm.g, p.gm.max_q, bf16)) {
+        case Path::kTc:
+            if (variant) *variant = p.d <= 64 ? "paged_tc_bf16_d64" : "paged_tc_bf16_d128";
+            return launch_paged_tc(p, workspace, stream);
+        case Path::kDecode:
+            if (variant) *variant = p.d <= 64 ? "paged_decode_bf16_d64" : "paged_decode_bf16_d128";
+            return launch_paged_decode(p, workspace, stream);
+        default:
+            if (variant) *variant = "paged_simt_f32";
+            return launch_paged_simt(p, workspace, stream);
     }
-    if (variant) *variant = bf16 ? "paged_simt_bf16" : "paged_simt_f32";
-    return launch_paged_simt(p, bf16, workspace, stream);
 }
 
 }  // namespace eta

@@ -1,5 +1,5 @@
 // Attention of new tokens over a paged cache on the CUDA cores: IEEE float32
-// throughout (no TF32), float32 or bfloat16 storage.
+// throughout (no TF32), float32 storage.
 //
 // O = softmax(scale Q K^T) V of each unit (paged_index.h: one kv head, a block
 // of new tokens, all query heads of the group), key tile by key tile with the
@@ -18,15 +18,7 @@ namespace {
 constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p) {
-    if constexpr (sizeof(T) == 4) {
-        return __ldg(reinterpret_cast<const float4 *>(p));
-    } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-        return make_float4(bf16lo_to_f32(u.x), bf16hi_to_f32(u.x), bf16lo_to_f32(u.y), bf16hi_to_f32(u.y));
-    }
-}
+__device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 __device__ __forceinline__ void fma4(float4 a, float4 b, float &s) {
     s = fmaf(a.x, b.x, s);
     s = fmaf(a.y, b.y, s);
@@ -34,7 +26,7 @@ __device__ __forceinline__ void fma4(float4 a, float4 b, float &s) {
     s = fmaf(a.w, b.w, s);
 }
 
-template <typename T, int E, int RT>   // E = d / 32, RT: query rows of a unit
+template <int E, int RT>   // E = d / 32, RT: query rows of a unit
 struct SimtShape {
     static constexpr int D = 32 * E;
     static constexpr int LD = D + 4;          // padded rows: 16 lanes reading 16 rows meet no bank twice
@@ -43,9 +35,9 @@ struct SimtShape {
     static constexpr int SMEM = FLOATS * 4 + kSimtKeys * 8;
 };
 
-template <typename T, int E, int RT>
+template <int E, int RT>
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedParams p) {
-    using S = SimtShape<T, E, RT>;
+    using S = SimtShape<E, RT>;
     constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = RT / 16;
     extern __shared__ __align__(16) float smem[];
     __shared__ PagedPlan plan;
@@ -57,9 +49,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (tid < 2) paged_write_header(p, 2 * cta + tid, PagedHdr{0, 0, 0, 0});
     paged_plan<kSimtThreads>(p, &plan, cta, gridDim.x);
-    const T *Q = static_cast<const T *>(p.Q);
-    const T *K = static_cast<const T *>(p.K);
-    const T *V = static_cast<const T *>(p.V);
+    const float *Q = static_cast<const float *>(p.Q);
+    const float *K = static_cast<const float *>(p.K);
+    const float *V = static_cast<const float *>(p.V);
     PagedWalk w;
     w.start(&plan);
     while (w.next(gm)) {
@@ -209,12 +201,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
                 v.y *= inv;
                 v.z *= inv;
                 v.w *= inv;
-                T *dst = static_cast<T *>(p.O) + tok * p.o_token + static_cast<long long>(head) * p.o_head + c;
-                if constexpr (sizeof(T) == 4) {
-                    *reinterpret_cast<float4 *>(dst) = v;
-                } else {
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                }
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.O) + tok * p.o_token +
+                                            static_cast<long long>(head) * p.o_head + c) = v;
             }
             if (tx == 0) {
                 if (!whole) {
@@ -230,10 +218,10 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-template <typename T, int E, int RT>
+template <int E, int RT>
 int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
-    using S = SimtShape<T, E, RT>;
-    auto kern = paged_simt_kernel<T, E, RT>;
+    using S = SimtShape<E, RT>;
+    auto kern = paged_simt_kernel<E, RT>;
     int dev = 0, nsm = 0, per_sm = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM) != cudaSuccess ||
@@ -257,27 +245,26 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return kErrCuda;
-    return launch_paged_merge(p, sizeof(T) == 2, ctas, stream);
+    return launch_paged_merge(p, 0, ctas, stream);
 }
 
-template <typename T, int RT>
+template <int RT>
 int launch_d(PagedParams &p, void *workspace, cudaStream_t stream) {
     switch (p.d) {
-        case 32: return launch_one<T, 1, RT>(p, workspace, stream);
-        case 64: return launch_one<T, 2, RT>(p, workspace, stream);
-        case 96: return launch_one<T, 3, RT>(p, workspace, stream);
-        case 128: return launch_one<T, 4, RT>(p, workspace, stream);
+        case 32: return launch_one<1, RT>(p, workspace, stream);
+        case 64: return launch_one<2, RT>(p, workspace, stream);
+        case 96: return launch_one<3, RT>(p, workspace, stream);
+        case 128: return launch_one<4, RT>(p, workspace, stream);
         default: return kErrUnsupported;
     }
 }
 
 }  // namespace
 
-int launch_paged_simt(PagedParams p, int bf16, void *workspace, cudaStream_t stream) {
+int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream) {
     // Units of 16 rows where an entry's rows fit, else of 64.
     const bool small = static_cast<long long>(p.gm.max_q) * p.gm.g <= 16;
-    if (bf16) return small ? launch_d<__nv_bfloat16, 16>(p, workspace, stream) : launch_d<__nv_bfloat16, 64>(p, workspace, stream);
-    return small ? launch_d<float, 16>(p, workspace, stream) : launch_d<float, 64>(p, workspace, stream);
+    return small ? launch_d<16>(p, workspace, stream) : launch_d<64>(p, workspace, stream);
 }
 
 }  // namespace eta

@@ -578,18 +578,7 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     const PagedGeom &gm = p.gm;
     const int tpt = 128 / gm.g;
     CUtensorMap tq, tk, tv;
-    const int box = std::min(gm.page_size, S::BC);
-    const cuuint64_t qd[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(gm.T)};
-    const cuuint64_t qs[2] = {static_cast<cuuint64_t>(p.q_head) * 2, static_cast<cuuint64_t>(p.q_token) * 2};
-    const cuuint32_t qb[3] = {64u, static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tpt)};
-    const cuuint64_t kd[4] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(gm.page_size),
-                              static_cast<cuuint64_t>(gm.heads), static_cast<cuuint64_t>(gm.pages)};
-    const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.slot_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
-                              static_cast<cuuint64_t>(p.page_stride) * 2};
-    const cuuint32_t kb[4] = {64u, static_cast<cuuint32_t>(box), 1u, 1u};
-    if (!make_bf16_map(&tq, p.Q, 3, qd, qs, qb) || !make_bf16_map(&tk, p.K, 4, kd, ks, kb) ||
-        !make_bf16_map(&tv, p.V, 4, kd, ks, kb))
-        return kErrCuda;
+    if (!paged_maps(p, tpt, std::min(gm.page_size, S::BC), &tq, &tk, &tv)) return kErrCuda;
     const int ctas = std::min(nsm, kPagedMaxTcCtas);
     p.gm.tpu = S::NQ * tpt;
     p.gm.tk = S::BC;
