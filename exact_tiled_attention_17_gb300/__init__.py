@@ -22,6 +22,7 @@ import ctypes
 import functools
 import math
 import os
+import threading
 
 import torch
 
@@ -433,7 +434,10 @@ class PagedCache:
         self.device, self.dtype = k.device, k.dtype
         self.layers, self.pages, self.heads, self.page_size, self.d = layers, pages, heads, page_size, d
         self.seqs, self.max_pages = page_table.shape
-        self._index = k.device.index
+        self._index = k.get_device()
+        self._scale = 1.0 / math.sqrt(d)
+        self._code = _DTYPE[k.dtype]
+        self._spaces = {}
         self._c = CacheT(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
                          _DTYPE[k.dtype], layers, pages, heads, page_size, d, self.seqs, self.max_pages, k.stride(0),
                          k.stride(1), k.stride(2), k.stride(3))
@@ -454,8 +458,15 @@ class PagedCache:
         return cls(pool(), pool(), ints(seqs, max_pages) - 1, ints(seqs), ints(pages))
 
 
+# The current device's index, and the raw handle of a device's current stream:
+# torch's own binding functions where they exist (the public ones cost several
+# microseconds a call, which is what a decode step is made of).
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _paged_list(t, cache, name, n=None):
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != cache.device:
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != cache._index:
         raise ValueError(f"{name} must be a contiguous int32 vector on the cache's device")
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} elements")
@@ -475,15 +486,38 @@ def _paged_scope(cache, stream):
                 yield st.cuda_stream
 
 
-def _paged_workspace(workspace, need, cache):
+def _paged_call(cache, stream, body, *args):
+    """body(cache, stream handle, *args) on the cache's device and the stream."""
+    if stream is None and _device_index() == cache._index:
+        return body(cache, _raw_stream(cache._index), *args)
+    with _paged_scope(cache, stream) as st:
+        return body(cache, st, *args)
+
+
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
+
+
+def _paged_workspace(workspace, need, cache, st):
+    """The caller's workspace, or one of the cache object's own: one for each
+    thread and stream, whose calls run in order, so no two calls in flight
+    share it.  A call that is being captured gets memory of its own, which
+    belongs to the graph."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=cache.device)
-    if not workspace.is_cuda or workspace.device != cache.device or workspace.dtype != torch.uint8 or \
-            not workspace.is_contiguous():
+        if _capturing():
+            t = torch.empty(need, dtype=torch.uint8, device=cache.device)
+            return t, need, t.data_ptr()
+        key = (threading.get_ident(), st)
+        ws = cache._spaces.get(key)
+        if ws is None or ws[1] < need:
+            t = torch.empty(need, dtype=torch.uint8, device=cache.device)
+            ws = cache._spaces[key] = (t, need, t.data_ptr())
+        return ws
+    if workspace.get_device() != cache._index or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")
-    return workspace
+    return workspace, workspace.numel(), workspace.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
 def attn_cache_workspace_size(pages: int, n: int) -> int:
     return int(lib.attn_cache_workspace_size(pages, n))
 
@@ -495,18 +529,24 @@ def _granted(granted, cache, n):
     return granted
 
 
+def _reserve(cache, st, a, b, n, granted, workspace):
+    g = _granted(granted, cache, n)
+    ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
+    _check(lib.attn_cache_reserve(cache._p, a, b, n, g.data_ptr(), ws[2], ws[1], st), "attn_cache_reserve")
+    return g
+
+
 def attn_cache_reserve(cache, seqs, n_new, granted=None, workspace=None, stream=None):
     """Room for n_new[i] more tokens in sequence seqs[i] (int32 device
     vectors): free pages, lowest first, in list order; lengths grow.  Returns
     granted, int32 [n]: 1, or 0 for an entry that got nothing."""
     n = seqs.shape[0]
     a, b = _paged_list(seqs, cache, "seqs"), _paged_list(n_new, cache, "n_new", n)
-    with _paged_scope(cache, stream) as st:
-        g = _granted(granted, cache, n)
-        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache)
-        rc = lib.attn_cache_reserve(cache._p, a, b, n, g.data_ptr(), ws.data_ptr(), ws.numel(), st)
-    _check(rc, "attn_cache_reserve")
-    return g
+    return _paged_call(cache, stream, _reserve, a, b, n, granted, workspace)
+
+
+def _free(cache, st, a, b, n):
+    _check(lib.attn_cache_free(cache._p, a, b, n, st), "attn_cache_free")
 
 
 def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
@@ -514,9 +554,14 @@ def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
     n = seqs.shape[0]
     a = _paged_list(seqs, cache, "seqs")
     b = None if keep is None else _paged_list(keep, cache, "keep", n)
-    with _paged_scope(cache, stream) as st:
-        rc = lib.attn_cache_free(cache._p, a, b, n, st)
-    _check(rc, "attn_cache_free")
+    _paged_call(cache, stream, _free, a, b, n)
+
+
+def _fork(cache, st, a, b, n, copy, granted, workspace):
+    g = _granted(granted, cache, n)
+    ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
+    _check(lib.attn_cache_fork(cache._p, a, b, n, copy, g.data_ptr(), ws[2], ws[1], st), "attn_cache_fork")
+    return g
 
 
 def attn_cache_fork(cache, parents, children, copy: bool = False, granted=None, workspace=None, stream=None):
@@ -525,12 +570,17 @@ def attn_cache_fork(cache, parents, children, copy: bool = False, granted=None, 
     copied.  Returns granted, int32 [n]."""
     n = parents.shape[0]
     a, b = _paged_list(parents, cache, "parents"), _paged_list(children, cache, "children", n)
-    with _paged_scope(cache, stream) as st:
-        g = _granted(granted, cache, n)
-        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache)
-        rc = lib.attn_cache_fork(cache._p, a, b, n, int(bool(copy)), g.data_ptr(), ws.data_ptr(), ws.numel(), st)
-    _check(rc, "attn_cache_fork")
-    return g
+    return _paged_call(cache, stream, _fork, a, b, n, int(bool(copy)), granted, workspace)
+
+
+def _compact(cache, st, inplace, workspace):
+    table = cache.page_table if inplace else torch.empty_like(cache.page_table)
+    refs = cache.ref_counts if inplace else torch.empty_like(cache.ref_counts)
+    n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
+    ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, 0), cache, st)
+    _check(lib.attn_cache_compact(cache._p, table.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws[2], ws[1], st),
+           "attn_cache_compact")
+    return table, refs, n_live
 
 
 def attn_cache_compact(cache, inplace: bool = True, workspace=None, stream=None):
@@ -538,15 +588,11 @@ def attn_cache_compact(cache, inplace: bool = True, workspace=None, stream=None)
     ref_counts, n_live): the cache's own tensors, updated, or with
     inplace=False new ones, the cache's staying as they were (and valid, since
     only free pages are written); n_live is an int32 device tensor [1]."""
-    with _paged_scope(cache, stream) as st:
-        table = cache.page_table if inplace else torch.empty_like(cache.page_table)
-        refs = cache.ref_counts if inplace else torch.empty_like(cache.ref_counts)
-        n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
-        ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, 0), cache)
-        rc = lib.attn_cache_compact(cache._p, table.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), st)
-    _check(rc, "attn_cache_compact")
-    return table, refs, n_live
+    return _paged_call(cache, stream, _compact, inplace, workspace)
+
+
+def _append(cache, st, *args):
+    _check(lib.attn_cache_append(cache._p, *args, st), "attn_cache_append")
 
 
 def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None) -> None:
@@ -555,19 +601,17 @@ def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=Non
     dimension (one pair of strides for both).  Entry i: sequence seqs[i]
     (seqs None: sequence i), tokens q_start[i] .. q_start[i+1] - 1, the last
     ones of the sequence (reserved before)."""
-    if (k_new.dim() != 3 or k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or
-            k_new.shape[1:] != (cache.heads, cache.d) or k_new.stride(2) != 1):
+    shape, strides = k_new.shape, k_new.stride()
+    if (len(shape) != 3 or shape != v_new.shape or strides != v_new.stride() or shape[1] != cache.heads or
+            shape[2] != cache.d or strides[2] != 1):
         raise ValueError("k_new and v_new must be [T, heads, d] with one shape and strides, the last dimension contiguous")
-    if k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or k_new.device != cache.device or \
-            v_new.device != cache.device:
+    if (k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or k_new.get_device() != cache._index or
+            v_new.get_device() != cache._index):
         raise ValueError("k_new and v_new must have the cache's dtype and device")
     n = q_start.shape[0] - 1
     a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
     b = _paged_list(q_start, cache, "q_start")
-    with _paged_scope(cache, stream) as st:
-        rc = lib.attn_cache_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0), k_new.stride(1),
-                                   k_new.shape[0], a, b, n, st)
-    _check(rc, "attn_cache_append")
+    _paged_call(cache, stream, _append, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n)
 
 
 @functools.lru_cache(maxsize=256)
@@ -577,6 +621,21 @@ def _paged_workspace_size(Hq, heads, max_q, d, dtype) -> int:
 
 def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) -> int:
     return _paged_workspace_size(Hq, heads, max_q, d, _DTYPE[dtype] if not isinstance(dtype, int) else dtype)
+
+
+def _paged_fwd(cache, st, q, layer, shape, a, b, n, max_q, causal, scale, o, l, want_lse, workspace):
+    T, Hq, d = shape
+    if o is None:
+        o = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+    if l is None and want_lse:
+        l = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
+    # (arguments the library rejects give a size of 0 here; it then says which)
+    ws = _paged_workspace(workspace, _paged_workspace_size(Hq, cache.heads, max(max_q, 1), d, cache._code), cache, st)
+    qs, os_ = q.stride(), o.stride()
+    _check(lib.attn_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(), qs[0], qs[1],
+                              os_[0], os_[1], T, Hq, a, b, n, max_q, causal, scale, ws[2], ws[1], st),
+           "attn_paged_fwd")
+    return o, l
 
 
 def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None, causal: bool = True,
@@ -590,33 +649,22 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     of an entry (default T; a close bound lets short entries take the path for
     few rows).  Returns (o, lse): o like q, lse [T, Hq] float32; rows outside
     the list are left as they were."""
-    if q.dim() != 3 or q.shape[2] != cache.d or (q.shape[2] > 1 and q.stride(2) != 1):
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.d or q.stride(2) != 1:
         raise ValueError("q must be [T, Hq, d] with a contiguous last dimension")
-    if q.dtype != cache.dtype or q.device != cache.device:
+    if q.dtype != cache.dtype or q.get_device() != cache._index:
         raise ValueError("q must have the cache's dtype and device")
-    T, Hq, d = q.shape
     n = q_start.shape[0] - 1
     a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
     b = _paged_list(q_start, cache, "q_start")
-    if max_q is None:
-        max_q = T
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or out.stride(2) != 1):
+    if out is not None and (out.shape != shape or out.dtype != q.dtype or out.get_device() != cache._index or
+                            out.stride(2) != 1):
         raise ValueError("out must be like q, with a contiguous last dimension")
-    if lse is not None and (lse.shape != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            lse.device != q.device):
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            lse.get_device() != cache._index):
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq] on q's device")
-    with _paged_scope(cache, stream) as st:
-        o = out if out is not None else torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
-        l = lse if lse is not None else (torch.empty((T, Hq), dtype=torch.float32, device=q.device) if want_lse else None)
-        # (arguments the library rejects give 0 here; it then says which)
-        ws = _paged_workspace(workspace, _paged_workspace_size(Hq, cache.heads, max(int(max_q), 1), d, cache._c.dtype), cache)
-        rc = lib.attn_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(),
-                                q.stride(0), q.stride(1), o.stride(0), o.stride(1), T, Hq, a, b, n, int(max_q),
-                                int(bool(causal)), float(scale), ws.data_ptr(), ws.numel(), st)
-    _check(rc, "attn_paged_fwd")
-    return o, l
+    return _paged_call(cache, stream, _paged_fwd, q, layer, shape, a, b, n, shape[0] if max_q is None else int(max_q),
+                       1 if causal else 0, cache._scale if scale is None else float(scale), out, lse, want_lse, workspace)
 
 
 def attn_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:

@@ -167,6 +167,16 @@ struct PagedWalk {
     }
 };
 
+// The same for a whole warp, with the state in shared memory (registers are
+// what the matrix kernel lacks): one lane moves on, everyone reads.
+__device__ __forceinline__ bool paged_walk_warp(PagedWalk *w, const PagedGeom &gm) {
+    int more = 0;
+    __syncwarp();   // everyone has read the part before
+    if ((threadIdx.x & 31) == 0) more = w->next(gm) ? 1 : 0;
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, more, 0) != 0;
+}
+
 __device__ __forceinline__ void paged_write_header(const PagedParams &p, int slot, const PagedHdr &h) {
     *reinterpret_cast<int4 *>(p.part_hdr + 4 * slot) = make_int4(h.rows, h.tok0, h.head, h.last);
 }

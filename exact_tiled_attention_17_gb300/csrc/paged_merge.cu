@@ -3,98 +3,132 @@
 //     M = max m_s,  O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
 // the rule by which the tiled forward joins two blocks of keys.
 //
-// Grid (CTA c of the main kernel, row blocks).  Block (c, y) owns the unit
-// that CTA c began but did not end (slot 2c + 1); its other parts lie in the
-// slots 2k of the CTAs after c, up to the one that ends the unit.  One warp
-// per row at a time: lanes read 32 parts' (m, l) in one round trip, then the
-// lanes split d and add the parts in order, so the result does not depend on
-// timing.
+// Grid (CTA c of the main kernel, row blocks), one warp to a row at a time.  The warps of
+// block (c, y) own the unit that CTA c began but did not end (slot 2c + 1); its
+// other parts lie in the slots 2k of the CTAs after c, up to the one that ends
+// the unit.  What bounds this kernel is its chain of dependent reads, so a lane
+// reads the header, m and l of one part at once (32 parts to a round trip,
+// before it is known how many there are), and then up to 8 parts' rows are
+// read before the first is used.  Parts are added in order: the result does
+// not depend on timing.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace eta {
 namespace {
 
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
+constexpr int kMergeRows = 2;      // rows of a warp
+constexpr int kMergeFlight = 8;
+
+template <int E>
+__device__ __forceinline__ void load_row(const float *src, float (&v)[E]) {
+    if constexpr (E == 4) {
+        const float4 f = __ldcg(reinterpret_cast<const float4 *>(src));
+        v[0] = f.x;
+        v[1] = f.y;
+        v[2] = f.z;
+        v[3] = f.w;
+    } else if constexpr (E == 2) {
+        const float2 f = __ldcg(reinterpret_cast<const float2 *>(src));
+        v[0] = f.x;
+        v[1] = f.y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = __ldcg(src + e);
+    }
+}
 
 template <int E, bool BF16>   // E = d / 32 columns per lane
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedParams p, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PagedHdr hd = paged_read_header(p, 2 * c + 1);
-    const int row0 = blockIdx.y * kMergeWarps + warp;
-    if (hd.rows > 0) {
-        // parts after the first: CTAs c + 1 .. last
-        int last = c;
-        for (int k0 = c + 1; k0 < ctas; k0 += 32) {
-            PagedHdr hk{0, 0, 0, 0};
-            if (k0 + lane < ctas) hk = paged_read_header(p, 2 * (k0 + lane));
-            const uint32_t ends = __ballot_sync(0xffffffffu, hk.rows > 0 && hk.last);
-            if (ends) {
-                last = k0 + __ffs(ends) - 1;
-                break;
+    for (int row = blockIdx.y * kMergeWarps + warp; row < p.part_rows; row += gridDim.y * kMergeWarps) {
+        float M = -INFINITY, L = 0.f, acc[E];
+    #pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        PagedHdr own{0, 0, 0, 0};
+        for (int base = 0;; base += 32) {
+            // part s is CTA c + s's (part 0: the one that begins the unit)
+            const int s = base + lane;
+            PagedHdr h{0, 0, 0, 0};
+            float m = -INFINITY, l = 0.f;
+            const int slot = s == 0 ? 2 * c + 1 : 2 * (c + s);
+            if (c + s < ctas) {
+                const size_t at = static_cast<size_t>(slot) * p.part_rows + row;
+                h = paged_read_header(p, slot);
+                m = __ldcg(p.part_m + at);
+                l = __ldcg(p.part_l + at);
             }
-            last = min(k0 + 31, ctas - 1);
-        }
-        const int parts = last - c + 1;
-        // slot of part s (0: the one that begins the unit); -1: that CTA had no share
-        auto slot_of = [&](int s) { return s == 0 ? 2 * c + 1 : 2 * (c + s); };
-        for (int row = row0; row < hd.rows; row += gridDim.y * kMergeWarps) {
-            float M = -INFINITY;
-            for (int s = lane; s < parts; s += 32) {
-                const int sl = slot_of(s);
-                if (s == 0 || paged_read_header(p, sl).rows > 0)
-                    M = fmaxf(M, __ldcg(p.part_m + static_cast<size_t>(sl) * p.part_rows + row));
+            if (base == 0) {
+                own.rows = __shfl_sync(0xffffffffu, h.rows, 0);
+                own.tok0 = __shfl_sync(0xffffffffu, h.tok0, 0);
+                own.head = __shfl_sync(0xffffffffu, h.head, 0);
+                if (row >= own.rows) break;   // nothing begins here, or no more rows
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float mu = M == -INFINITY ? 0.f : M;
-            float L = 0.f, acc[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = 0.f;
-            for (int s0 = 0; s0 < parts; s0 += 32) {
-                float w = 0.f, l = 0.f;
-                const int s = s0 + lane;
-                if (s < parts) {
-                    const int sl = slot_of(s);
-                    if (s == 0 || paged_read_header(p, sl).rows > 0) {
-                        const size_t at = static_cast<size_t>(sl) * p.part_rows + row;
-                        const float m = __ldcg(p.part_m + at);
-                        w = m == -INFINITY ? 0.f : ex2(m - mu);
-                        l = __ldcg(p.part_l + at);
-                    }
-                }
-                float wl = w == 0.f ? 0.f : w * l;
-#pragma unroll
+            const uint32_t ends = __ballot_sync(0xffffffffu, s > 0 && h.rows > 0 && h.last);
+            const int cnt = ends ? __ffs(ends) : min(32, ctas - c - base);
+            const bool in = lane < cnt && h.rows > 0 && m != -INFINITY;   // (a CTA without a share has no part)
+            float Mc = in ? m : -INFINITY;
+    #pragma unroll
+            for (int o = 16; o > 0; o >>= 1) Mc = fmaxf(Mc, __shfl_xor_sync(0xffffffffu, Mc, o));
+            const float Mn = fmaxf(M, Mc);
+            if (Mn != -INFINITY) {
+                const float a = M == -INFINITY ? 0.f : ex2(M - Mn);
+                const float w = in ? ex2(m - Mn) : 0.f;
+                float wl = in ? w * l : 0.f;
+    #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
-                L += wl;
-                const int cnt = min(32, parts - s0);
-                for (int q0 = 0; q0 < cnt; q0 += 8) {
-                    float v[8][E], ws[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
+                L = L * a + wl;
+    #pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= a;
+                for (int q0 = 0; q0 < cnt; q0 += kMergeFlight) {
+                    float v[kMergeFlight][E], ws[kMergeFlight];
+    #pragma unroll
+                    for (int q = 0; q < kMergeFlight; ++q) {
                         ws[q] = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
+                        const int sl = __shfl_sync(0xffffffffu, slot, (q0 + q) & 31);
                         if (q0 + q >= cnt) ws[q] = 0.f;
-                        const float *src = p.part_o +
-                                           (static_cast<size_t>(slot_of(s0 + min(q0 + q, cnt - 1))) * p.part_rows + row) * p.d +
-                                           E * lane;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) v[q][e] = ws[q] != 0.f ? __ldcg(src + e) : 0.f;
+    #pragma unroll
+                        for (int e = 0; e < E; ++e) v[q][e] = 0.f;
+                        if (ws[q] != 0.f) load_row<E>(p.part_o + (static_cast<size_t>(sl) * p.part_rows + row) * p.d + E * lane, v[q]);
                     }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-#pragma unroll
+    #pragma unroll
+                    for (int q = 0; q < kMergeFlight; ++q)
+    #pragma unroll
                         for (int e = 0; e < E; ++e) acc[e] = fmaf(ws[q], v[q][e], acc[e]);
                 }
+                M = Mn;
             }
+            if (ends || base + 32 >= ctas - c) break;
+        }
+        if (row >= own.rows) break;
+        {
             const float inv = L > 0.f ? 1.f / L : 0.f;
-            const long long tok = hd.tok0 + row / p.gm.g;
-            const int head = hd.head * p.gm.g + row % p.gm.g;
+            const long long tok = own.tok0 + row / p.gm.g;
+            const int head = own.head * p.gm.g + row % p.gm.g;
             const long long at = tok * p.o_token + static_cast<long long>(head) * p.o_head + E * lane;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if constexpr (BF16) static_cast<__nv_bfloat16 *>(p.O)[at + e] = __float2bfloat16_rn(acc[e] * inv);
-                else static_cast<float *>(p.O)[at + e] = acc[e] * inv;
+            if constexpr (BF16) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + at;
+                if constexpr (E == 4) {
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
+                } else if constexpr (E == 2) {
+                    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+                } else {
+    #pragma unroll
+                    for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
+                }
+            } else {
+                float *dst = static_cast<float *>(p.O) + at;
+                if constexpr (E == 4) {
+                    *reinterpret_cast<float4 *>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+                } else {
+    #pragma unroll
+                    for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
+                }
             }
             if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + head] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
         }
@@ -105,9 +139,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
 template <int E, bool BF16>
 int launch_one(const PagedParams &p, int ctas, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    // up to 16 rows to a block: few blocks leave at once when nothing was cut
-    const int rows_y = (p.part_rows + 4 * kMergeWarps - 1) / (4 * kMergeWarps);
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows_y));
+    // a unit has at most as many rows as an entry
+    const int rows = static_cast<int>(std::min<long long>(p.part_rows, static_cast<long long>(p.gm.max_q) * p.gm.g));
+    const int per = kMergeWarps * kMergeRows;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((rows + per - 1) / per));
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -150,7 +185,7 @@ namespace {
 enum class Path { kSimt, kDecode, kTc };
 Path path_of(int g, int max_q, int bf16) {
     if (!bf16) return Path::kSimt;
-    return static_cast<long long>(g) * max_q <= 64 ? Path::kDecode : Path::kTc;
+    return static_cast<long long>(g) * max_q <= 32 ? Path::kDecode : Path::kTc;
 }
 }  // namespace
 

@@ -67,7 +67,8 @@ struct PtcShape {
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;          // tensor-memory address, abort flag
     static constexpr int OFF_BADP = OFF_MISC + 16;                // per K tile (mod 8): missing pages, bit per 16 keys
     static constexpr int OFF_PLAN = OFF_BADP + 32;
-    static constexpr int SMEM_MIN = OFF_PLAN + static_cast<int>(sizeof(PagedPlan)) + 1024;
+    static constexpr int OFF_WALK = OFF_PLAN + (static_cast<int>(sizeof(PagedPlan)) + 15) / 16 * 16;   // one per warp
+    static constexpr int SMEM_MIN = OFF_WALK + 18 * static_cast<int>(sizeof(PagedWalk)) + 1024;
     // (all of tensor memory is allocated: a second resident CTA would wait for it)
     static constexpr int SMEM_BYTES = SMEM_MIN <= 116 * 1024 ? 117 * 1024 : SMEM_MIN;
     __host__ __device__ static constexpr int s_col(int q) { return q * BC; }
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
     paged_plan<S::THREADS>(p, plan, cta, gridDim.x);
 
     const int tpt = 128 / gm.g;   // tokens to a query tile
-    PagedWalk w;
-    w.start(plan);
+    PagedWalk &w = reinterpret_cast<PagedWalk *>(smem + S::OFF_WALK)[warp];
+    if (lane == 0) w.start(plan);
     // K/V tiles of the part that query tile q takes part in: the first nkv
     // (causal tiles of earlier tokens end earlier); 0 when it has no rows.
     auto tiles_of = [&](int q) -> int {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             int t = 0, tails = 0, kt = 0;
             int uo[NQ] = {0, 0};
             bool ok = true;
-            while (ok && w.next(gm)) {
+            while (ok && paged_walk_warp(&w, gm)) {
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
                     if (tiles_of(q) == 0) continue;
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 if (leader) tc_commit(bar(b));
             };
             bool ok = true;
-            while (ok && w.next(gm)) {
+            while (ok && paged_walk_warp(&w, gm)) {
                 int nkv[NQ];
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) nkv[q] = tiles_of(q);
@@ -375,19 +376,20 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         };
         int sq = 0, uo = 0, kt = 0;
         bool ok = true;
-        while (w.next(gm)) {
+        while (paged_walk_warp(&w, gm)) {
             const int nkvq = tiles_of(q), ntok = w.ntok(gm);
             const bool valid = slot_ok && tok_in < ntok;
             const int vis = valid ? paged_visible(gm, w.e, w.tok0(gm) + tok_in) : 0;
             // keys that every row of the tile sees
             const int vis_all = q * tpt < ntok ? paged_visible(gm, w.e, w.tok0(gm) + q * tpt) : 0;
+            const int tile0 = w.tile0;
             float m = kNegInfP, l = 0.f;
             // (a wait that gives up is recorded and does not end the loop: every
             // warp still takes part in every named barrier)
             for (int j = 0; j < nkvq; ++j) {
                 if (!mbar_wait(bar(S::BAR_SFULL + q), (sq + j) & 1, abort_flag, p.err, 20)) ok = false;
                 tc_fence_after();
-                const int key0 = (w.tile0 + j) * BC;
+                const int key0 = (tile0 + j) * BC;
                 const uint32_t bad = bad_pages[(kt + j) & 7];
                 const bool edge = key0 + BC > vis_all || bad != 0u;
                 uint32_t sr[2][32];
