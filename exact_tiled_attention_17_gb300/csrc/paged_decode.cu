@@ -1,7 +1,7 @@
 // Attention of a few new tokens over a paged cache, bf16 in / f32 accumulate:
 // decoding, and the checking of a few drafted tokens.
 //
-// A unit (paged_index.h) is one kv head with up to 16, 32 or 64 query rows:
+// A unit (paged_index.h) is one kv head with up to 16 or 32 query rows:
 // a few tokens times the g query heads that share the head.  The work is a
 // stream over K and V, a few FLOPs to a byte, so it is bound by HBM and the
 // kernel's job is to keep enough bytes in flight.  With g heads to a stream
@@ -42,9 +42,9 @@ struct PdShape {
     static constexpr int ROWS = 16 * MT;
     static constexpr int KV_BYTES = kDecKeys * DP * 2;
     static constexpr int STAGE = 2 * KV_BYTES;
-    static constexpr int CTAS = MT == 4 ? 1 : 2;                    // per SM
-    static constexpr int QB = MT == 2 ? 1 : 2;                      // Q buffers
-    static constexpr int NS = (MT == 4 ? 5 : 3) * (DP == 64 ? 2 : 1) > 8 ? 8 : (MT == 4 ? 5 : 3) * (DP == 64 ? 2 : 1);
+    static constexpr int CTAS = 2;                                  // per SM
+    static constexpr int QB = MT == 1 ? 2 : 1;                      // Q buffers
+    static constexpr int NS = DP == 64 ? 6 : 3;                     // stages: 96 KB in flight to a CTA
     static constexpr int Q_BYTES = ROWS * DP * 2;
     static constexpr int P_BYTES = ROWS * 128;
     static constexpr int OFF_Q = NS * STAGE;
@@ -52,12 +52,13 @@ struct PdShape {
     static constexpr int OFF_MX = OFF_P + P_BYTES;                  // [4][ROWS] maxima
     static constexpr int OFF_L = OFF_MX + 4 * ROWS * 4;             // [4][ROWS] sums
     static constexpr int OFF_BAR = OFF_L + 4 * ROWS * 4;
+    // a unit's words and its Q arrive on one barrier; QEMPTY: both have been read
     static constexpr int BAR_FULL = 0, BAR_EMPTY = NS, BAR_QFULL = 2 * NS, BAR_QEMPTY = BAR_QFULL + QB;
-    static constexpr int OFF_MISC = OFF_BAR + (BAR_QEMPTY + QB) * 8;
+    static constexpr int OFF_MISC = OFF_BAR + ((BAR_QEMPTY + QB) * 8 + 15) / 16 * 16;
     static constexpr int OFF_BADP = OFF_MISC + 16;                  // per stage: missing pages, bit per 16 keys
-    static constexpr int OFF_PLAN = OFF_BADP + ((NS * 4 + 15) / 16) * 16;
-    static constexpr int SMEM_BYTES = OFF_PLAN + static_cast<int>(sizeof(PagedPlan)) + 1024;
-    static_assert(SMEM_BYTES <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+    static constexpr int OFF_UNIT = OFF_BADP + ((NS * 4 + 15) / 16) * 16;   // [QB]
+    static constexpr int SMEM_BYTES = OFF_UNIT + QB * static_cast<int>(sizeof(PagedUnit)) + 1024;
+    static_assert(SMEM_BYTES <= 113 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
     auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_MISC);
     volatile uint32_t *bad_pages = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_BADP);
-    PagedPlan *plan = reinterpret_cast<PagedPlan *>(smem + S::OFF_PLAN);
+    PagedUnit *units = reinterpret_cast<PagedUnit *>(smem + S::OFF_UNIT);
     float *mx_sh = reinterpret_cast<float *>(smem + S::OFF_MX);
     float *l_sh = reinterpret_cast<float *>(smem + S::OFF_L);
     if (threadIdx.x == 0) {
@@ -115,11 +116,9 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
+    __syncthreads();
+    paged_touch(p);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (threadIdx.x < 2) paged_write_header(p, 2 * cta + threadIdx.x, PagedHdr{0, 0, 0, 0});
-    paged_plan<160>(p, plan, cta, gridDim.x);
-    PagedWalk w;
-    w.start(plan);
 
     if (warp == 4) {
         // ------------------------------------------------------------------
@@ -135,29 +134,41 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
         const uint32_t dst = my_kv * S::KV_BYTES + my_cb * (kDecKeys * 128) + my_box * box_rows * 128;
         int t = 0, u = 0;
         bool ok = true;
-        while (ok && w.next(gm)) {
+        PagedFeed feed;
+        feed.start(p, cta, gridDim.x);
+        for (;; ++u) {
+            PagedUnit w;
+            feed.next(p, cta, w);
             const int qb = u % S::QB;
-            if (u >= S::QB && !wwait(bar(S::BAR_QEMPTY + qb), (u / S::QB - 1) & 1, 50)) break;
+            if (u >= S::QB && !wwait(bar(S::BAR_QEMPTY + qb), (u / S::QB - 1) & 1, 50)) ok = false;
+            if (!ok) break;   // (the others' waits run out too)
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar(S::BAR_QFULL + qb), CB * 128 * gm.g * gm.tpu);
+                units[qb] = w;
+                if (w.tiles == 0) {
+                    mbar_arrive(bar(S::BAR_QFULL + qb));
+                } else {
+                    mbar_arrive_expect_tx(bar(S::BAR_QFULL + qb), CB * 128 * gm.g * gm.tpu);
 #pragma unroll
-                for (int cb = 0; cb < CB; ++cb)
-                    tma_load_3d(sbase + S::OFF_Q + qb * S::Q_BYTES + cb * (ROWS * 128), &tm_q, bar(S::BAR_QFULL + qb), cb * 64,
-                                w.h * gm.g, w.e.q0 + w.tok0(gm));
+                    for (int cb = 0; cb < CB; ++cb)
+                        tma_load_3d(sbase + S::OFF_Q + qb * S::Q_BYTES + cb * (ROWS * 128), &tm_q, bar(S::BAR_QFULL + qb),
+                                    cb * 64, w.head * gm.g, w.tok0);
+                }
             }
-            ++u;
+            if (w.tiles == 0) break;
+            feed.report(p, w);
+            const int j1 = w.tile0 + w.tiles;
             auto lookup = [&](int j) -> int {   // page of this lane's box: -1 past the end, -2 missing
                 const int key = j * kDecKeys + my_box * box_rows;
-                if (!mine || key >= w.e.len) return -1;
-                const int id = paged_page(gm, w.e.seq, key / gm.page_size);
+                if (!mine || key >= w.len) return -1;
+                const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                 return id < 0 ? -2 : id;
             };
             // table entries two tiles ahead
-            int next0 = lookup(w.tile0), next1 = w.tile0 + 1 < w.tile1 ? lookup(w.tile0 + 1) : -1;
-            for (int j = w.tile0; j < w.tile1; ++j, ++t) {
+            int next0 = lookup(w.tile0), next1 = w.tiles > 1 ? lookup(w.tile0 + 1) : -1;
+            for (int j = w.tile0; j < j1; ++j, ++t) {
                 const int id = next0;
                 next0 = next1;
-                if (j + 2 < w.tile1) next1 = lookup(j + 2);
+                if (j + 2 < j1) next1 = lookup(j + 2);
                 const int st = t % NS;
                 if (t >= NS && !wwait(bar(S::BAR_EMPTY + st), (t / NS - 1) & 1, 51)) {
                     ok = false;
@@ -177,12 +188,14 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 __syncwarp();
                 if (mine)
                     tma_load_4d(sbase + st * S::STAGE + dst, my_kv ? &tm_v : &tm_k, bar(S::BAR_FULL + st), my_cb * 64,
-                                (j * kDecKeys + my_box * box_rows) & (gm.page_size - 1), w.h, id < 0 ? gm.pages : id);
+                                (j * kDecKeys + my_box * box_rows) & (gm.page_size - 1), w.head, id < 0 ? gm.pages : id);
             }
         }
+        feed.finish(p, cta);
         // every copy has landed before this warp leaves
         for (int tt = max(0, t - NS); tt < t; ++tt) wwait(bar(S::BAR_FULL + tt % NS), (tt / NS) & 1, 52);
-        for (int uu = max(0, u - S::QB); uu < u; ++uu) wwait(bar(S::BAR_QFULL + uu % S::QB), (uu / S::QB) & 1, 53);
+        // (the buffer that the last words went to was free: its Q had been read)
+        for (int uu = max(0, u - S::QB + 1); uu < u; ++uu) wwait(bar(S::BAR_QFULL + uu % S::QB), (uu / S::QB) & 1, 53);
         __syncwarp();
     } else {
         // ------------------------------------------------------------------
@@ -193,10 +206,15 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
         const int a_row = lane & 15, a_chunk = lane >> 4;             // ldmatrix lanes of an A fragment
         const int k_row = warp * 16 + (mat >> 1) * 8 + (lane & 7), k_chunk = mat & 1;
         const int v_row = (mat & 1) * 8 + (lane & 7), v_chunk = warp * (DP / 32) + (mat >> 1);
-        int t = 0, u = 0;
-        while (w.next(gm)) {
+        int t = 0;
+        for (int u = 0;; ++u) {
             const int qb = u % S::QB;
-            mbar_wait(bar(S::BAR_QFULL + qb), (u / S::QB) & 1, abort_flag, p.err, 54);
+            // (all four warps leave together: what one reads of a unit that never
+            // came, the others read too)
+            const bool came = mbar_wait(bar(S::BAR_QFULL + qb), (u / S::QB) & 1, abort_flag, p.err, 54);
+            if (named_bar_red_or(1, 128, !came)) break;
+            const PagedUnit w = units[qb];
+            if (w.tiles == 0) break;
             const uint32_t sQ = sbase + S::OFF_Q + qb * S::Q_BYTES;
             const uint32_t sP = sbase + S::OFF_P;
             auto q_frag = [&](int mt, int kk, uint32_t (&a)[4]) {
@@ -210,16 +228,16 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));   // the next Q may overwrite it
             }
-            const int ntok = w.ntok(gm), rows = ntok * gm.g;
+            const int rows = w.ntok * gm.g, j1 = w.tile0 + w.tiles;
             int vis[MT][2];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int r = mt * 16 + quad + 8 * i;
-                    vis[mt][i] = r < rows ? paged_visible(gm, w.e, w.tok0(gm) + r / gm.g) : 0;
+                    vis[mt][i] = r < rows ? paged_unit_visible(gm, w, paged_token(gm, r)) : 0;
                 }
-            const int vis_all = paged_visible(gm, w.e, w.tok0(gm));   // what every row sees
+            const int vis_all = paged_unit_visible(gm, w, 0);   // what every row sees
             float m[MT][2], l[MT][2], o[MT][NT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
             }
-            for (int j = w.tile0; j < w.tile1; ++j, ++t) {
+            for (int j = w.tile0; j < j1; ++j, ++t) {
                 const int st = t % NS;
                 mbar_wait(bar(S::BAR_FULL + st), (t / NS) & 1, abort_flag, p.err, 55);
                 const uint32_t sK = sbase + st * S::STAGE, sV = sK + S::KV_BYTES;
@@ -330,7 +348,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     }
                 named_bar_sync(1, 128);
                 // O += P V, this warp's columns
-                const int live = w.e.len - key0;   // slots of the tile that hold tokens
+                const int live = w.len - key0;   // slots of the tile that hold tokens
 #pragma unroll
                 for (int ks = 0; ks < kDecKeys / 16; ++ks) {
                     uint32_t vf[NT / 2][4];
@@ -367,7 +385,6 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));
             }
-            ++u;
             // ---------------- the unit's end ----------------
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -378,8 +395,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     if ((lane & 3) == 0) l_sh[warp * ROWS + mt * 16 + quad + 8 * i] = l[mt][i];
                 }
             named_bar_sync(1, 128);
-            const bool whole = w.whole();
-            const int slot = w.slot(cta);
+            const bool whole = w.slot < 0;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -388,10 +404,11 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     if (r >= rows || *abort_flag) continue;
                     const float *at = l_sh + r;
                     const float L = (at[0] + at[ROWS]) + (at[2 * ROWS] + at[3 * ROWS]);
-                    const long long tok = w.e.q0 + w.tok0(gm) + r / gm.g;
-                    const int head = w.h * gm.g + r % gm.g;
+                    const int tr = paged_token(gm, r);
+                    const long long tok = w.tok0 + tr;
+                    const int head = w.head * gm.g + r - tr * gm.g;
                     const float inv = L > 0.f ? 1.f / L : 0.f;
-                    const size_t prow = static_cast<size_t>(slot) * p.part_rows + r;
+                    const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * p.part_rows + r;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const int c = warp * (DP / 4) + n * 8 + col2;
@@ -413,7 +430,6 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                         }
                     }
                 }
-            if (!whole && threadIdx.x == 0) paged_write_header(p, slot, w.header(gm));
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -445,6 +461,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.tk = kDecKeys;
     p.gm.unit_cost = kDecKeys;
     p.gm.min_share = 2 * kDecKeys;
+    paged_derive(p.gm);
     CUtensorMap tq, tk, tv;
     if (!paged_maps(p, S::ROWS / gm.g, std::min(gm.page_size, kDecKeys), &tq, &tk, &tv)) return kErrCuda;
     paged_carve(p, workspace, grid, S::ROWS);
@@ -459,7 +476,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
-    return launch_paged_merge(p, 1, grid, stream);
+    return launch_paged_merge(p, 1, grid, grid / S::CTAS, stream);
 }
 
 }  // namespace
@@ -467,8 +484,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.gm.max_q) * p.gm.g;
     if (rows <= 16) return p.d <= 64 ? launch_one<64, 1>(p, workspace, stream) : launch_one<128, 1>(p, workspace, stream);
-    if (rows <= 32) return p.d <= 64 ? launch_one<64, 2>(p, workspace, stream) : launch_one<128, 2>(p, workspace, stream);
-    return p.d <= 64 ? launch_one<64, 4>(p, workspace, stream) : launch_one<128, 4>(p, workspace, stream);
+    return p.d <= 64 ? launch_one<64, 2>(p, workspace, stream) : launch_one<128, 2>(p, workspace, stream);
 }
 
 }  // namespace eta

@@ -34,7 +34,27 @@ struct PagedGeom {
     int tpu, tk;             // tokens per unit, keys per tile
     int unit_cost;           // a unit's fixed cost, in keys
     int min_share;           // the least work worth a CTA, in keys
+    // derived (paged_derive): divisions are slow where a call takes microseconds
+    int page_shift, tk_shift;   // page_size and tk are powers of two
+    unsigned g_mul;             // r / g = r * g_mul >> 16 for r < 256
 };
+
+ETA_HD void paged_derive(PagedGeom &gm) {
+    gm.page_shift = 0;
+    while ((1 << gm.page_shift) < gm.page_size) ++gm.page_shift;
+    gm.tk_shift = 0;
+    while ((1 << gm.tk_shift) < gm.tk) ++gm.tk_shift;
+    gm.g_mul = (65536u + static_cast<unsigned>(gm.g) - 1) / static_cast<unsigned>(gm.g);
+}
+
+// Row r < 256 of a unit: its token within the unit (r / g; the head is the rest).
+ETA_HD int paged_token(const PagedGeom &gm, int r) { return static_cast<int>(static_cast<unsigned>(r) * gm.g_mul >> 16); }
+
+// a / b, by the short division where both fit into 32 bits.
+ETA_HD long long paged_div(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+    return a / b;
+}
 
 // One entry of the list.  nq = 0: nothing to do (or a bad entry).
 struct PagedEntry {
@@ -69,13 +89,15 @@ ETA_HD int paged_visible(const PagedGeom &gm, const PagedEntry &e, int t) {
     return v < 0 ? 0 : v > e.len ? e.len : v;
 }
 
-ETA_HD int paged_units(const PagedGeom &gm, const PagedEntry &e) { return (e.nq + gm.tpu - 1) / gm.tpu; }
+ETA_HD int paged_units(const PagedGeom &gm, const PagedEntry &e) {
+    return e.nq <= gm.tpu ? (e.nq > 0 ? 1 : 0) : (e.nq + gm.tpu - 1) / gm.tpu;
+}
 
 // Tiles of unit u: at least one, so that rows without any key are written.
 ETA_HD int paged_tiles(const PagedGeom &gm, const PagedEntry &e, int u) {
     const int last = (u + 1) * gm.tpu < e.nq ? (u + 1) * gm.tpu : e.nq;
     const int keys = paged_visible(gm, e, last - 1);
-    return keys <= gm.tk ? 1 : (keys + gm.tk - 1) / gm.tk;
+    return keys <= gm.tk ? 1 : ((keys - 1) >> gm.tk_shift) + 1;
 }
 
 // Work of units [0, u) of one head, in keys (every unit before the last has
@@ -120,7 +142,7 @@ ETA_HD PagedPos paged_locate(const PagedGeom &gm, const PagedEntry &e, int i, lo
     const long long hw = paged_head_work(gm, e);
     PagedPos p;
     p.i = i;
-    p.h = static_cast<int>(x / hw);
+    p.h = static_cast<int>(paged_div(x, hw));
     x -= p.h * hw;
     int lo = 0, hi = paged_units(gm, e) - 1;   // the last unit that begins at or before x
     while (lo < hi) {
@@ -130,7 +152,7 @@ ETA_HD PagedPos paged_locate(const PagedGeom &gm, const PagedEntry &e, int i, lo
     }
     p.u = lo;
     x -= paged_before(gm, e, lo);
-    const long long t = (x + gm.tk / 2) / gm.tk;
+    const long long t = (x + gm.tk / 2) >> gm.tk_shift;
     const int tiles = paged_tiles(gm, e, lo);
     p.tile = t < tiles ? static_cast<int>(t) : tiles;
     if (p.tile == tiles) paged_next_unit(gm, e, p);
@@ -139,13 +161,14 @@ ETA_HD PagedPos paged_locate(const PagedGeom &gm, const PagedEntry &e, int i, lo
 
 // CTAs that get a share of W, and where share c begins.
 ETA_HD int paged_shares(const PagedGeom &gm, long long W, int ctas) {
-    const long long most = (W + gm.min_share - 1) / gm.min_share;
+    const long long most = paged_div(W + gm.min_share - 1, gm.min_share);
     return most < 1 ? 1 : most < ctas ? static_cast<int>(most) : ctas;
 }
 ETA_HD long long paged_share_begin(long long W, int c, int shares) {
     if (c >= shares) return W;
     // W c / shares without overflow: W < 2^62, shares <= 4096
-    return W / shares * c + W % shares * c / shares;
+    const long long each = paged_div(W, shares);
+    return each * c + paged_div((W - each * shares) * c, shares);
 }
 
 // The page of tile-relative page k of a tile that starts at key `key0` (a

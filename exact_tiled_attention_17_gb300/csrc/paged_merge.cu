@@ -3,14 +3,19 @@
 //     M = max m_s,  O = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s,
 // the rule by which the tiled forward joins two blocks of keys.
 //
-// Grid (CTA c of the main kernel, row blocks), one warp to a row at a time.  The warps of
-// block (c, y) own the unit that CTA c began but did not end (slot 2c + 1); its
-// other parts lie in the slots 2k of the CTAs after c, up to the one that ends
-// the unit.  What bounds this kernel is its chain of dependent reads, so a lane
-// reads the header, m and l of one part at once (32 parts to a round trip,
-// before it is known how many there are), and then up to 8 parts' rows are
-// read before the first is used.  Parts are added in order: the result does
-// not depend on timing.
+// The unit that CTA c began but did not end has its first part in slot 2c + 1
+// and the others in the slots 2k of the CTAs after c, up to the one that ends
+// it; each CTA left one word that says which of its slots are in use.  A warp
+// takes a row: a lane to a part reads m and l, then up to 8 parts' rows are
+// read before the first is used.  What bounds it is this chain of dependent
+// reads.  Parts are added in order: the result does not depend on timing.
+//
+// Units of few rows (decoding): block c looks at CTA c's unit, and all lanes
+// read words, m and l at once before it is known how many parts there are.
+// Units of many rows: every block reads all words and finds the cut units in
+// them, so rows are dealt out evenly however few units were cut (8 units of
+// 256 rows and 19 parts each: 20 us when their blocks stayed on 64 SMs); with
+// two parts, as nearly always in a large batch, a warp takes four rows at once.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -19,7 +24,7 @@ namespace eta {
 namespace {
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeRows = 2;      // rows of a warp
+constexpr int kMergeThreads = 32 * kMergeWarps;
 constexpr int kMergeFlight = 8;
 
 template <int E>
@@ -40,127 +45,254 @@ __device__ __forceinline__ void load_row(const float *src, float (&v)[E]) {
     }
 }
 
-template <int E, bool BF16>   // E = d / 32 columns per lane
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedParams p, int ctas) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int row = blockIdx.y * kMergeWarps + warp; row < p.part_rows; row += gridDim.y * kMergeWarps) {
-        float M = -INFINITY, L = 0.f, acc[E];
-    #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        PagedHdr own{0, 0, 0, 0};
-        for (int base = 0;; base += 32) {
-            // part s is CTA c + s's (part 0: the one that begins the unit)
-            const int s = base + lane;
-            PagedHdr h{0, 0, 0, 0};
-            float m = -INFINITY, l = 0.f;
-            const int slot = s == 0 ? 2 * c + 1 : 2 * (c + s);
-            if (c + s < ctas) {
-                const size_t at = static_cast<size_t>(slot) * p.part_rows + row;
-                h = paged_read_header(p, slot);
-                m = __ldcg(p.part_m + at);
-                l = __ldcg(p.part_l + at);
-            }
-            if (base == 0) {
-                own.rows = __shfl_sync(0xffffffffu, h.rows, 0);
-                own.tok0 = __shfl_sync(0xffffffffu, h.tok0, 0);
-                own.head = __shfl_sync(0xffffffffu, h.head, 0);
-                if (row >= own.rows) break;   // nothing begins here, or no more rows
-            }
-            const uint32_t ends = __ballot_sync(0xffffffffu, s > 0 && h.rows > 0 && h.last);
-            const int cnt = ends ? __ffs(ends) : min(32, ctas - c - base);
-            const bool in = lane < cnt && h.rows > 0 && m != -INFINITY;   // (a CTA without a share has no part)
-            float Mc = in ? m : -INFINITY;
-    #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) Mc = fmaxf(Mc, __shfl_xor_sync(0xffffffffu, Mc, o));
-            const float Mn = fmaxf(M, Mc);
-            if (Mn != -INFINITY) {
-                const float a = M == -INFINITY ? 0.f : ex2(M - Mn);
-                const float w = in ? ex2(m - Mn) : 0.f;
-                float wl = in ? w * l : 0.f;
-    #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
-                L = L * a + wl;
-    #pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] *= a;
-                for (int q0 = 0; q0 < cnt; q0 += kMergeFlight) {
-                    float v[kMergeFlight][E], ws[kMergeFlight];
-    #pragma unroll
-                    for (int q = 0; q < kMergeFlight; ++q) {
-                        ws[q] = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
-                        const int sl = __shfl_sync(0xffffffffu, slot, (q0 + q) & 31);
-                        if (q0 + q >= cnt) ws[q] = 0.f;
-    #pragma unroll
-                        for (int e = 0; e < E; ++e) v[q][e] = 0.f;
-                        if (ws[q] != 0.f) load_row<E>(p.part_o + (static_cast<size_t>(sl) * p.part_rows + row) * p.d + E * lane, v[q]);
-                    }
-    #pragma unroll
-                    for (int q = 0; q < kMergeFlight; ++q)
-    #pragma unroll
-                        for (int e = 0; e < E; ++e) acc[e] = fmaf(ws[q], v[q][e], acc[e]);
-                }
-                M = Mn;
-            }
-            if (ends || base + 32 >= ctas - c) break;
+template <int E, bool BF16>
+__device__ __forceinline__ void store_row(void *base, long long at, const float (&v)[E], float inv) {
+    if constexpr (BF16) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(base) + at;
+        if constexpr (E == 4) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+        } else if constexpr (E == 2) {
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(v[0] * inv, v[1] * inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(v[e] * inv);
         }
-        if (row >= own.rows) break;
-        {
-            const float inv = L > 0.f ? 1.f / L : 0.f;
-            const long long tok = own.tok0 + row / p.gm.g;
-            const int head = own.head * p.gm.g + row % p.gm.g;
-            const long long at = tok * p.o_token + static_cast<long long>(head) * p.o_head + E * lane;
-            if constexpr (BF16) {
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + at;
-                if constexpr (E == 4) {
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                                 pack_bf16x2(acc[2] * inv, acc[3] * inv));
-                } else if constexpr (E == 2) {
-                    *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-                } else {
-    #pragma unroll
-                    for (int e = 0; e < E; ++e) dst[e] = __float2bfloat16_rn(acc[e] * inv);
-                }
-            } else {
-                float *dst = static_cast<float *>(p.O) + at;
-                if constexpr (E == 4) {
-                    *reinterpret_cast<float4 *>(dst) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-                } else {
-    #pragma unroll
-                    for (int e = 0; e < E; ++e) dst[e] = acc[e] * inv;
-                }
+    } else {
+        float *dst = static_cast<float *>(base) + at;
+        if constexpr (E == 4) {
+            *reinterpret_cast<float4 *>(dst) = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) dst[e] = v[e] * inv;
+        }
+    }
+}
+
+// One row of the unit that CTA c began.  word(k): CTA k's word.  FEW: words and
+// statistics are read together, whatever the words then say.
+template <int E, bool BF16, bool FEW, typename Word>
+__device__ __forceinline__ void merge_row(const PagedParams &p, int ctas, int c, int row, const Word &word) {
+    const int lane = threadIdx.x & 31;
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    PagedHdr own{0, 0, 0, 0};
+    if constexpr (!FEW) own = paged_read_header(p, 2 * c + 1);
+    for (int base = 0; base < ctas - c; base += 32) {
+        // part s is CTA c + s's (part 0: the one that begins the unit)
+        const int s = base + lane;
+        const int slot = s == 0 ? 2 * c + 1 : 2 * (c + s);
+        const size_t x = static_cast<size_t>(slot) * p.part_rows + row;
+        float m = -INFINITY, l = 0.f;
+        int wd = 0;
+        if constexpr (FEW) {
+            if (c + s < ctas) {
+                wd = word(c + s);
+                m = __ldcg(p.part_m + x);
+                l = __ldcg(p.part_l + x);
+                if (base == 0 && lane == 0) own = paged_read_header(p, 2 * c + 1);
             }
-            if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + head] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+            if (base == 0 && row >= __shfl_sync(0xffffffffu, wd, 0) >> 2) return;   // nothing begins here, or no such row
+        } else {
+            if (c + s < ctas) wd = word(c + s);
+        }
+        const uint32_t ends = __ballot_sync(0xffffffffu, s > 0 && (wd & 3) == 3);
+        const int cnt = ends ? __ffs(ends) : min(32, ctas - c - base);
+        const bool in = lane < cnt && (s == 0 || (wd & 1));   // (a CTA without a share has no part)
+        if constexpr (FEW) {
+            if (!in) m = -INFINITY;
+        } else if (in) {
+            m = __ldcg(p.part_m + x);
+            l = __ldcg(p.part_l + x);
+        }
+        float Mc = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) Mc = fmaxf(Mc, __shfl_xor_sync(0xffffffffu, Mc, o));
+        const float Mn = fmaxf(M, Mc);
+        if (Mn != -INFINITY) {
+            const float a = M == -INFINITY ? 0.f : ex2(M - Mn);
+            // (a weight of 0 also stands for an o that was not written)
+            const float w = m == -INFINITY ? 0.f : ex2(m - Mn);
+            float wl = w == 0.f ? 0.f : w * l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
+            L = L * a + wl;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= a;
+            auto add = [&](int q0) {
+                constexpr int F = kMergeFlight;
+                float v[F][E], ws[F];
+#pragma unroll
+                for (int q = 0; q < F; ++q) {
+                    ws[q] = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
+                    if (q0 + q >= cnt) ws[q] = 0.f;
+                    const int part = base + q0 + q;
+                    const size_t sl = static_cast<size_t>(part == 0 ? 2 * c + 1 : 2 * (c + part));
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[q][e] = 0.f;
+                    if (ws[q] != 0.f) load_row<E>(p.part_o + (sl * p.part_rows + row) * p.d + E * lane, v[q]);
+                }
+#pragma unroll
+                for (int q = 0; q < F; ++q)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(ws[q], v[q][e], acc[e]);
+            };
+            for (int q0 = 0; q0 < cnt; q0 += kMergeFlight) add(q0);
+            M = Mn;
+        }
+        if (ends) break;
+    }
+    if constexpr (FEW) {
+        own.tok0 = __shfl_sync(0xffffffffu, own.tok0, 0);
+        own.head = __shfl_sync(0xffffffffu, own.head, 0);
+    }
+    const int t = paged_token(p.gm, row);
+    const long long tok = own.tok0 + t;
+    const int hq = own.head * p.gm.g + row - t * p.gm.g;
+    store_row<E, BF16>(p.O, tok * p.o_token + static_cast<long long>(hq) * p.o_head + E * lane, acc, L > 0.f ? 1.f / L : 0.f);
+    if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+}
+
+// Four rows (row, row + kMergeWarps, ...) of a unit of two parts: lane 2 q + s reads m and l of row q's part s.
+template <int E, bool BF16>
+__device__ __forceinline__ void merge_rows4(const PagedParams &p, int c, int row, int rows) {
+    const int lane = threadIdx.x & 31;
+    const PagedHdr own = paged_read_header(p, 2 * c + 1);
+    const int s = lane & 1, mine = row + (lane >> 1) * kMergeWarps;
+    float m = -INFINITY, l = 0.f;
+    if (lane < 8 && mine < rows) {
+        const size_t x = static_cast<size_t>(s == 0 ? 2 * c + 1 : 2 * (c + 1)) * p.part_rows + mine;
+        m = __ldcg(p.part_m + x);
+        l = __ldcg(p.part_l + x);
+    }
+    const float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    // (a weight of 0 also stands for an o that was not written)
+    const float w = m == -INFINITY ? 0.f : ex2(m - M);
+    float L = w == 0.f ? 0.f : w * l;
+    L += __shfl_xor_sync(0xffffffffu, L, 1);
+    float v[2][4][E], ws[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const size_t at = static_cast<size_t>(t == 0 ? 2 * c + 1 : 2 * (c + 1)) * p.part_rows + row;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            ws[t][q] = __shfl_sync(0xffffffffu, w, 2 * q + t);
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[t][q][e] = 0.f;
+            if (ws[t][q] != 0.f) load_row<E>(p.part_o + (at + q * kMergeWarps) * p.d + E * lane, v[t][q]);
+        }
+    }
+    float acc[4][E];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[q][e] = fmaf(ws[1][q], v[1][q][e], ws[0][q] * v[0][q][e]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int r = row + q * kMergeWarps;
+        const float Lq = __shfl_sync(0xffffffffu, L, 2 * q), Mq = __shfl_sync(0xffffffffu, M, 2 * q);
+        if (r >= rows) continue;
+        const int t = paged_token(p.gm, r);
+        const long long tok = own.tok0 + t;
+        const int hq = own.head * p.gm.g + r - t * p.gm.g;
+        store_row<E, BF16>(p.O, tok * p.o_token + static_cast<long long>(hq) * p.o_head + E * lane, acc[q],
+                           Lq > 0.f ? 1.f / Lq : 0.f);
+        if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = Lq > 0.f ? (Mq + log2f(Lq)) * kPagedLn2 : -INFINITY;
+    }
+}
+
+template <int E, bool BF16, bool FEW>   // E = d / 32 columns per lane
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p, int ctas) {
+    paged_touch(p);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (FEW) {
+        const int row = blockIdx.y * kMergeWarps + warp;
+        if (row < p.part_rows)
+            merge_row<E, BF16, true>(p, ctas, blockIdx.x, row, [&](int k) { return __ldcg(p.part_sum + k); });
+    } else {
+        // before: row blocks of earlier CTAs' units
+        __shared__ int words[kPagedMaxTcCtas + 1], before[kPagedMaxTcCtas];
+        __shared__ int wsum[kMergeWarps];
+        static_assert(kPagedMaxTcCtas < kMergeThreads, "a thread to a CTA's word");
+        const int wd = threadIdx.x < ctas ? __ldcg(p.part_sum + threadIdx.x) : 0;
+        if (threadIdx.x <= kPagedMaxTcCtas) words[threadIdx.x] = wd;
+        __syncthreads();
+        // a unit whose next part is its last has two (in a large batch nearly all)
+        auto two = [&](int k) { return (words[k + 1] & 3) == 3; };
+        int blocks = 0;
+        if (wd >> 2) {
+            const int per = two(threadIdx.x) ? 4 * kMergeWarps : kMergeWarps;   // rows of a block
+            blocks = ((wd >> 2) + per - 1) / per;
+        }
+        int inc = blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int at = inc - blocks, total = 0;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            if (w < warp) at += wsum[w];
+            total += wsum[w];
+        }
+        if (threadIdx.x < ctas) before[threadIdx.x] = at;
+        __syncthreads();
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            int lo = 0, hi = ctas - 1;   // the last CTA with before <= item (the last of equal ones has the rows)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (before[mid] <= item) lo = mid;
+                else hi = mid - 1;
+            }
+            const int rows = words[lo] >> 2, block = item - before[lo];
+            if (two(lo)) {
+                const int row = block * 4 * kMergeWarps + warp;
+                if (row < rows) merge_rows4<E, BF16>(p, lo, row, rows);
+            } else {
+                const int row = block * kMergeWarps + warp;
+                if (row < rows) merge_row<E, BF16, false>(p, ctas, lo, row, [&](int k) { return words[k]; });
+            }
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-template <int E, bool BF16>
-int launch_one(const PagedParams &p, int ctas, cudaStream_t stream) {
+template <int E, bool BF16, bool FEW>
+int launch_one(const PagedParams &p, int ctas, int sms, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    // a unit has at most as many rows as an entry
-    const int rows = static_cast<int>(std::min<long long>(p.part_rows, static_cast<long long>(p.gm.max_q) * p.gm.g));
-    const int per = kMergeWarps * kMergeRows;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((rows + per - 1) / per));
-    cfg.blockDim = dim3(32 * kMergeWarps);
+    // at most ctas units are cut, of at most as many rows as an entry has
+    const long long rows = std::min<long long>(p.part_rows, static_cast<long long>(p.gm.max_q) * p.gm.g);
+    const long long per = (rows + kMergeWarps - 1) / kMergeWarps;
+    if (FEW) cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(per));
+    else cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(ctas * per, 4LL * sms)));
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<E, BF16>, p, ctas) == cudaSuccess ? kOk : kErrCuda;
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<E, BF16, FEW>, p, ctas) == cudaSuccess ? kOk : kErrCuda;
+}
+
+template <int E>
+int launch_e(const PagedParams &p, int bf16, int ctas, int sms, cudaStream_t stream) {
+    if (!bf16) return launch_one<E, false, true>(p, ctas, sms, stream);
+    return p.part_rows <= 64 ? launch_one<E, true, true>(p, ctas, sms, stream) : launch_one<E, true, false>(p, ctas, sms, stream);
 }
 
 }  // namespace
 
-int launch_paged_merge(const PagedParams &p, int bf16, int ctas, cudaStream_t stream) {
+int launch_paged_merge(const PagedParams &p, int bf16, int ctas, int sms, cudaStream_t stream) {
     switch (p.d) {
-        case 32: return bf16 ? launch_one<1, true>(p, ctas, stream) : launch_one<1, false>(p, ctas, stream);
-        case 64: return bf16 ? launch_one<2, true>(p, ctas, stream) : launch_one<2, false>(p, ctas, stream);
-        case 96: return bf16 ? launch_one<3, true>(p, ctas, stream) : launch_one<3, false>(p, ctas, stream);
-        case 128: return bf16 ? launch_one<4, true>(p, ctas, stream) : launch_one<4, false>(p, ctas, stream);
+        case 32: return launch_e<1>(p, bf16, ctas, sms, stream);
+        case 64: return launch_e<2>(p, bf16, ctas, sms, stream);
+        case 96: return launch_e<3>(p, bf16, ctas, sms, stream);
+        case 128: return launch_e<4>(p, bf16, ctas, sms, stream);
         default: return kErrUnsupported;
     }
 }
@@ -180,8 +312,8 @@ bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUte
 }
 
 namespace {
-// The kernel of a call.  bf16: the stream kernel holds units of up to 64 rows
-// (tokens of an entry x query heads of a group); more rows are matrix work.
+// The kernel of a call.  bf16: the stream kernel takes units of up to 32 rows
+// (tokens of an entry x query heads of a group), the matrix kernel more.
 enum class Path { kSimt, kDecode, kTc };
 Path path_of(int g, int max_q, int bf16) {
     if (!bf16) return Path::kSimt;

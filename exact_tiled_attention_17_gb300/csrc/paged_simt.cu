@@ -40,28 +40,36 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
     using S = SimtShape<E, RT>;
     constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = RT / 16;
     extern __shared__ __align__(16) float smem[];
-    __shared__ PagedPlan plan;
+    __shared__ PagedUnit unit;
     float *qs = smem, *ks = qs + RT * LD, *vs = ks + kSimtKeys * LD, *ps = vs + kSimtKeys * LD;
     long long *key_at = reinterpret_cast<long long *>(ps + RT * LP);   // offset of each key's row, or -1
     const PagedGeom &gm = p.gm;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cta = blockIdx.x;
+    paged_touch(p);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tid < 2) paged_write_header(p, 2 * cta + tid, PagedHdr{0, 0, 0, 0});
-    paged_plan<kSimtThreads>(p, &plan, cta, gridDim.x);
     const float *Q = static_cast<const float *>(p.Q);
     const float *K = static_cast<const float *>(p.K);
     const float *V = static_cast<const float *>(p.V);
-    PagedWalk w;
-    w.start(&plan);
-    while (w.next(gm)) {
-        const int rows = w.ntok(gm) * gm.g, tok0 = w.e.q0 + w.tok0(gm);
+    PagedFeed feed;   // (warp 0)
+    if (tid < 32) feed.start(p, cta, gridDim.x);
+    for (;;) {
+        __syncthreads();   // the unit before is done with
+        if (tid < 32) {
+            PagedUnit w;
+            feed.next(p, cta, w);
+            if (w.tiles > 0) feed.report(p, w);
+            if (tid == 0) unit = w;
+        }
         __syncthreads();
+        const PagedUnit w = unit;
+        if (w.tiles == 0) break;
+        const int rows = w.ntok * gm.g, tok0 = w.tok0;
         for (int i = tid; i < RT * (D / 4); i += kSimtThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                v = load4(Q + (tok0 + r / gm.g) * p.q_token + static_cast<long long>(w.h * gm.g + r % gm.g) * p.q_head + c);
+                v = load4(Q + (tok0 + paged_token(gm, r)) * p.q_token + static_cast<long long>(w.head * gm.g + (r - paged_token(gm, r) * gm.g)) * p.q_head + c);
             *reinterpret_cast<float4 *>(qs + r * LD + c) = v;
         }
         int vis[RR];   // keys that this thread's rows see
@@ -71,21 +79,21 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
 #pragma unroll
         for (int a = 0; a < RR; ++a) {
             const int r = ty * RR + a;
-            vis[a] = r < rows ? paged_visible(gm, w.e, w.tok0(gm) + r / gm.g) : 0;
+            vis[a] = r < rows ? paged_unit_visible(gm, w, paged_token(gm, r)) : 0;
             m[a] = -INFINITY;
             l[a] = 0.f;
 #pragma unroll
             for (int b = 0; b < (E + 1) / 2; ++b) o[a][b] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        for (int t = w.tile0; t < w.tile1; ++t) {
+        for (int t = w.tile0; t < w.tile0 + w.tiles; ++t) {
             const int key0 = t * kSimtKeys;
             __syncthreads();   // the previous tile has been read
             if (tid < kSimtKeys) {
                 const int key = key0 + tid;
                 long long at = -1;
-                if (key < w.e.len) {
-                    const int id = paged_page(gm, w.e.seq, key / gm.page_size);
-                    if (id >= 0) at = id * p.page_stride + (key % gm.page_size) * p.slot_stride + w.h * p.head_stride;
+                if (key < w.len) {
+                    const int id = paged_page(gm, w.seq, key >> gm.page_shift);
+                    if (id >= 0) at = id * p.page_stride + (key & (gm.page_size - 1)) * p.slot_stride + w.head * p.head_stride;
                     else atomicOr(p.err, kErrWordBadRow);
                 }
                 key_at[tid] = at;
@@ -179,14 +187,14 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
             }
         }
         // the unit's rows, or this share's part of them
-        const bool whole = w.whole();
-        const int slot = w.slot(cta);
+        const bool whole = w.slot < 0;
+        const int slot = whole ? 0 : w.slot;
 #pragma unroll
         for (int a = 0; a < RR; ++a) {
             const int r = ty * RR + a;
             if (r >= rows) continue;
-            const long long tok = tok0 + r / gm.g;
-            const int head = w.h * gm.g + r % gm.g;
+            const long long tok = tok0 + paged_token(gm, r);
+            const int head = w.head * gm.g + (r - paged_token(gm, r) * gm.g);
             const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
 #pragma unroll
             for (int b = 0; b < (E + 1) / 2; ++b) {
@@ -213,8 +221,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
                 }
             }
         }
-        if (!whole && tid == 0) paged_write_header(p, slot, w.header(gm));
     }
+    if (tid < 32) feed.finish(p, cta);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -233,6 +241,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.tk = kSimtKeys;
     p.gm.unit_cost = kSimtKeys;
     p.gm.min_share = 2 * kSimtKeys;
+    paged_derive(p.gm);
     paged_carve(p, workspace, ctas, RT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -245,7 +254,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return kErrCuda;
-    return launch_paged_merge(p, 0, ctas, stream);
+    return launch_paged_merge(p, 0, ctas, nsm, stream);
 }
 
 template <int RT>

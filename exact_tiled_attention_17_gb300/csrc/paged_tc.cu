@@ -63,19 +63,21 @@ struct PtcShape {
     static constexpr int BAR_OFREE = BAR_QFREE + NQ;
     static constexpr int BAR_DONE = BAR_OFREE + NQ;
     static constexpr int BAR_TAIL = BAR_DONE + 1;
-    static constexpr int NBARS = BAR_TAIL + 1;
+    static constexpr int UB = 4;                                  // units announced ahead
+    static constexpr int BAR_UFULL = BAR_TAIL + 1;
+    static constexpr int BAR_UEMPTY = BAR_UFULL + UB;
+    static constexpr int NBARS = (BAR_UEMPTY + UB + 1) / 2 * 2;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;          // tensor-memory address, abort flag
     static constexpr int OFF_BADP = OFF_MISC + 16;                // per K tile (mod 8): missing pages, bit per 16 keys
-    static constexpr int OFF_PLAN = OFF_BADP + 32;
-    static constexpr int OFF_WALK = OFF_PLAN + (static_cast<int>(sizeof(PagedPlan)) + 15) / 16 * 16;   // one per warp
-    static constexpr int SMEM_MIN = OFF_WALK + 18 * static_cast<int>(sizeof(PagedWalk)) + 1024;
+    static constexpr int OFF_UNIT = OFF_BADP + 32;                // [UB]; spare[q]: key tiles of query tile q
+    static constexpr int SMEM_MIN = OFF_UNIT + UB * static_cast<int>(sizeof(PagedUnit)) + 1024;
     // (all of tensor memory is allocated: a second resident CTA would wait for it)
     static constexpr int SMEM_BYTES = SMEM_MIN <= 116 * 1024 ? 117 * 1024 : SMEM_MIN;
     __host__ __device__ static constexpr int s_col(int q) { return q * BC; }
     __host__ __device__ static constexpr int o_col(int q) { return NQ * BC + q * DP; }
     static_assert(NS >= 4 && SMEM_BYTES <= 227 * 1024, "shared memory");
     static_assert(NQ * (BC + DP) <= 512, "tensor memory");
-    static_assert(OFF_PLAN % 8 == 0, "alignment");
+    static_assert(OFF_UNIT % 16 == 0, "alignment");
 };
 
 template <int DP>
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::OFF_MISC);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_MISC + 4);
     volatile uint32_t *bad_pages = reinterpret_cast<volatile uint32_t *>(smem + S::OFF_BADP);
-    PagedPlan *plan = reinterpret_cast<PagedPlan *>(smem + S::OFF_PLAN);
+    PagedUnit *units = reinterpret_cast<PagedUnit *>(smem + S::OFF_UNIT);
     const uint32_t sQ = sbase, sRing = sbase + S::OFF_RING;
 
     if (threadIdx.x == 0) {
@@ -112,6 +114,10 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         }
         mbar_init(bar(S::BAR_DONE), 1);
         mbar_init(bar(S::BAR_TAIL), 1);
+        for (int u = 0; u < S::UB; ++u) {
+            mbar_init(bar(S::BAR_UFULL + u), 1);
+            mbar_init(bar(S::BAR_UEMPTY + u), S::SOFTMAX_WARPS + 1);
+        }
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -123,21 +129,17 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    paged_touch(p);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (threadIdx.x < 2) paged_write_header(p, 2 * cta + threadIdx.x, PagedHdr{0, 0, 0, 0});
-    paged_plan<S::THREADS>(p, plan, cta, gridDim.x);
 
     const int tpt = 128 / gm.g;   // tokens to a query tile
-    PagedWalk &w = reinterpret_cast<PagedWalk *>(smem + S::OFF_WALK)[warp];
-    if (lane == 0) w.start(plan);
-    // K/V tiles of the part that query tile q takes part in: the first nkv
-    // (causal tiles of earlier tokens end earlier); 0 when it has no rows.
-    auto tiles_of = [&](int q) -> int {
-        const int t0 = w.tok0(gm) + q * tpt, t1 = min(w.tok0(gm) + w.ntok(gm), t0 + tpt);
-        if (t1 <= t0) return 0;
-        const int keys = paged_visible(gm, w.e, t1 - 1);
-        const int tiles = keys <= BC ? 1 : (keys + BC - 1) / BC;
-        return max(0, min(tiles, w.tile1) - w.tile0);
+    // Unit u has been announced by the producer.
+    auto unit_wait = [&](int u, int site) -> bool {
+        return mbar_wait(bar(S::BAR_UFULL + u % S::UB), (u / S::UB) & 1, abort_flag, p.err, site);
+    };
+    auto unit_done = [&](int u) {   // one lane of each warp, when the warp has read the last of it
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::BAR_UEMPTY + u % S::UB));
     };
 
     if (warp >= S::SOFTMAX_WARPS) {
@@ -162,31 +164,59 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             int t = 0, tails = 0, kt = 0;
             int uo[NQ] = {0, 0};
             bool ok = true;
-            while (ok && paged_walk_warp(&w, gm)) {
+            PagedFeed feed;
+            feed.start(p, cta, gridDim.x);
+            for (int u = 0; ok; ++u) {
+                PagedUnit w;
+                feed.next(p, cta, w);
+                // K/V tiles of the part that query tile q takes part in: the first
+                // ones (causal tiles of earlier tokens end earlier); 0 without rows
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    if (tiles_of(q) == 0) continue;
+                    const int t1 = min(w.ntok, (q + 1) * tpt);
+                    const int keys = paged_unit_visible(gm, w, t1 - 1);
+                    const int tiles = keys <= BC ? 1 : (keys - 1) / BC + 1;
+                    w.spare[q] = t1 > q * tpt ? max(0, min(tiles - w.tile0, w.tiles)) : 0;
+                }
+                if (u >= S::UB && !wwait(bar(S::BAR_UEMPTY + u % S::UB), (u / S::UB - 1) & 1, 7)) break;
+                if (lane == 0) {
+                    units[u % S::UB] = w;
+                    mbar_arrive(bar(S::BAR_UFULL + u % S::UB));
+                }
+                if (w.tiles == 0) break;
+                feed.report(p, w);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    if (w.spare[q] == 0) continue;
                     if (uo[q] > 0 && !wwait(bar(S::BAR_QFREE + q), (uo[q] - 1) & 1, 4)) ok = false;
                     if (ok && leader) {
                         mbar_arrive_expect_tx(bar(S::BAR_QFULL + q), S::CB * 128 * gm.g * tpt);
 #pragma unroll
                         for (int cb = 0; cb < S::CB; ++cb)
                             tma_load_3d_hint(sQ + q * S::Q_BYTES + cb * (S::BR * 128), &tm_q, bar(S::BAR_QFULL + q), cb * 64,
-                                             w.h * gm.g, w.e.q0 + w.tok0(gm) + q * tpt, pol_q);
+                                             w.head * gm.g, w.tok0 + q * tpt, pol_q);
                     }
                     ++uo[q];
                 }
                 // page of box my_box of tile j: -1 past the end (no keys), -2 missing
                 auto lookup = [&](int j) -> int {
                     const int key = j * BC + my_box * box_rows;
-                    if (my_box >= boxes || key >= w.e.len) return -1;
-                    const int id = paged_page(gm, w.e.seq, key / gm.page_size);
+                    if (my_box >= boxes || key >= w.len) return -1;
+                    const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                     return id < 0 ? -2 : id;
                 };
-                int next = lookup(w.tile0);
-                for (int j = w.tile0; ok && j < w.tile1; ++j, ++kt) {
-                    const int id = next;
-                    if (j + 1 < w.tile1) next = lookup(j + 1);
+                // table entries four tiles ahead: a read takes about as long as a
+                // tile's matrix products (one ahead, tiles of 16-token pages came
+                // in at 2.0 us each instead of 1.5)
+                const int j0 = w.tile0, j1 = w.tile0 + w.tiles;
+                auto ahead = [&](int j) { return j < j1 ? lookup(j) : -1; };
+                int n0 = ahead(j0), n1 = ahead(j0 + 1), n2 = ahead(j0 + 2), n3 = ahead(j0 + 3);
+                for (int j = j0; ok && j < j1; ++j, ++kt) {
+                    const int id = n0;
+                    n0 = n1;
+                    n1 = n2;
+                    n2 = n3;
+                    n3 = ahead(j + 4);
                     const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
                     const int x = my_cb * 64, slot0 = (j * BC + my_box * box_rows) & (gm.page_size - 1);
                     const int pg = id < 0 ? gm.pages : id;   // out of range: zeros
@@ -194,7 +224,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     const uint32_t dst = my_cb * (BC * 128) + my_box * box_rows * 128;
                     // rows of V to clear: past the end, in a page that was copied
                     const int key0 = j * BC;
-                    const int clear0 = w.e.len - key0;
+                    const int clear0 = w.len - key0;
                     const int clear1 = min(BC, (clear0 + box_rows - 1) / box_rows * box_rows);
                     const bool tail = clear0 > 0 && clear0 < BC && clear1 > clear0;
 #pragma unroll
@@ -221,7 +251,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                         }
                         __syncwarp();
                         if (mine)
-                            tma_load_4d(sRing + slot * S::SLOT_BYTES + dst, kv ? &tm_v : &tm_k, full, x, slot0, w.h, pg);
+                            tma_load_4d(sRing + slot * S::SLOT_BYTES + dst, kv ? &tm_v : &tm_k, full, x, slot0, w.head, pg);
                         if (kv == 1 && tail) {
                             if (!wwait(bar(S::BAR_TAIL), tails & 1, 6)) ok = false;
                             ++tails;
@@ -240,6 +270,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     }
                 }
             }
+            feed.finish(p, cta);
             // every copy this warp started has landed before the CTA may exit
             for (int tt = max(0, t - S::NS); tt < t; ++tt) wwait(bar(S::BAR_FULL + tt % S::NS), (tt / S::NS) & 1, 2);
 #pragma unroll
@@ -263,11 +294,15 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 if (leader) tc_commit(bar(b));
             };
             bool ok = true;
-            while (ok && paged_walk_warp(&w, gm)) {
+            for (int u = 0; ok; ++u) {
+                if (!__all_sync(0xffffffffu, unit_wait(u, 8))) break;
+                const PagedUnit *w = units + u % S::UB;
+                if (w->tiles == 0) break;
                 int nkv[NQ];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) nkv[q] = tiles_of(q);
-                const int nkv_max = w.tile1 - w.tile0;
+                for (int q = 0; q < NQ; ++q) nkv[q] = w->spare[q];
+                const int nkv_max = w->tiles;
+                unit_done(u);
 #pragma unroll
                 for (int q = 0; q < NQ; ++q)
                     if (ok && nkv[q] > 0) ok = wwait(bar(S::BAR_QFULL + q), uo[q] & 1, 10);
@@ -365,7 +400,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         const uint32_t tO = tmem + t_lane + S::o_col(q);
         const float sl2 = p.scale_log2;
         constexpr int OC = DP / 64;   // 32-column chunks of O of this warpgroup
-        const int tok_in = q * tpt + row_in / gm.g, head_in = row_in % gm.g;
+        const int tok_in = q * tpt + paged_token(gm, row_in), head_in = row_in - paged_token(gm, row_in) * gm.g;
         const bool slot_ok = row_in < tpt * gm.g;   // g need not divide 128
         auto xch = [&](int hh) -> uint32_t { return sbase + S::OFF_XCH + ((q * 2 + hh) * 128 + row_in) * 8; };
         auto pair_sync = [&]() { named_bar_sync(7 + q, 256); };
@@ -376,13 +411,17 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         };
         int sq = 0, uo = 0, kt = 0;
         bool ok = true;
-        while (paged_walk_warp(&w, gm)) {
-            const int nkvq = tiles_of(q), ntok = w.ntok(gm);
+        for (int u = 0;; ++u) {
+            // (the tile's two warpgroups leave together, whichever wait gave up)
+            if (named_bar_red_or(7 + q, 256, !unit_wait(u, 9))) break;
+            const PagedUnit *w = units + u % S::UB;
+            if (w->tiles == 0) break;
+            const int nkvq = w->spare[q], ntok = w->ntok;
             const bool valid = slot_ok && tok_in < ntok;
-            const int vis = valid ? paged_visible(gm, w.e, w.tok0(gm) + tok_in) : 0;
+            const int vis = valid ? paged_unit_visible(gm, *w, tok_in) : 0;
             // keys that every row of the tile sees
-            const int vis_all = q * tpt < ntok ? paged_visible(gm, w.e, w.tok0(gm) + q * tpt) : 0;
-            const int tile0 = w.tile0;
+            const int vis_all = q * tpt < ntok ? paged_unit_visible(gm, *w, q * tpt) : 0;
+            const int tile0 = w->tile0;
             float m = kNegInfP, l = 0.f;
             // (a wait that gives up is recorded and does not end the loop: every
             // warp still takes part in every named barrier)
@@ -483,7 +522,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 mbar_arrive(bar(S::BAR_PFULL + q));
             }
             // ---------------- epilogue ----------------
-            const bool whole = w.whole();
+            const bool whole = w->slot < 0;
             float lo;
             pair_sync();
             exchange(l, lo);
@@ -496,9 +535,11 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             const float scale_o = whole ? (any ? 1.f / l : 0.f) : 1.f;
             const uint64_t inv2 = f2_pack(scale_o, scale_o);
             const int unit_row = q * tpt * gm.g + row_in;
-            const size_t prow = static_cast<size_t>(w.slot(cta)) * p.part_rows + unit_row;
-            const long long tok = w.e.q0 + w.tok0(gm) + tok_in;
-            const int head = w.h * gm.g + head_in;
+            const size_t prow = static_cast<size_t>(whole ? 0 : w->slot) * p.part_rows + unit_row;
+            const long long tok = w->tok0 + tok_in;
+            const int head = w->head * gm.g + head_in;
+            kt += w->tiles;
+            unit_done(u);
             if (nkvq > 0) {
                 const long long at = valid ? tok * p.o_token + static_cast<long long>(head) * p.o_head : 0;
 #pragma unroll
@@ -540,14 +581,12 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     p.part_l[prow] = l;
                 }
             }
-            if (!whole && q == 0 && h == 0 && row_in == 0) paged_write_header(p, w.slot(cta), w.header(gm));
             if (nkvq > 0) {
                 tc_fence_before();
                 mbar_arrive(bar(S::BAR_OFREE + q));
             }
             sq += nkvq;
             uo += nkvq > 0 ? 1 : 0;
-            kt += w.tile1 - w.tile0;
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -586,6 +625,7 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.tk = S::BC;
     p.gm.unit_cost = 3 * S::BC;
     p.gm.min_share = 4 * S::BC;
+    paged_derive(p.gm);
     paged_carve(p, workspace, ctas, S::NQ * 128);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
@@ -598,7 +638,7 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
-    return launch_paged_merge(p, 1, ctas, stream);
+    return launch_paged_merge(p, 1, ctas, nsm, stream);
 }
 
 }  // namespace

@@ -160,6 +160,7 @@ static PagedGeom geom(const G *g) {
     const int *v = g->v;
     m.n = v[0]; m.rows = v[1]; m.max_pages = v[2]; m.pages = v[3]; m.page_size = v[4]; m.T = v[5]; m.max_q = v[6];
     m.heads = v[7]; m.g = v[8]; m.causal = v[9]; m.tpu = v[10]; m.tk = v[11]; m.unit_cost = v[12]; m.min_share = v[13];
+    paged_derive(m);
     return m;
 }
 int entry(const G *g, int i, int *out) {
@@ -206,6 +207,7 @@ int units(const G *g, int *out, int cap) {
     }
     return k;
 }
+int token(const G *g, int r) { return paged_token(geom(g), r); }
 int visible(const G *g, int i, int t) { PagedEntry e; paged_entry(geom(g), i, e); return paged_visible(geom(g), e, t); }
 }
 """
@@ -283,6 +285,12 @@ def test_visible_keys(shim, causal):
             for t in range(nq):
                 want = sum(1 for j in range(n) if j <= n - nq + t) if causal else n
                 assert shim.visible(ctypes.byref(a), 0, t) == want
+
+
+def test_rows_to_tokens(shim):
+    for g in range(1, 65):
+        a = geom([1], [0], [0, 1], 1, 1, g=g)
+        assert [shim.token(ctypes.byref(a), r) for r in range(256)] == [r // g for r in range(256)]
 
 
 def test_bad_entries_are_left_out(shim):
