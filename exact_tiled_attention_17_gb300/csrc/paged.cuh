@@ -67,9 +67,12 @@ struct PagedUnit {
     int vis0, len;       // keys that token 0 sees (before clamping); keys of the sequence
     int slot;            // partial slot, or -1: the whole unit
     int seq;             // table row
+    // the matrix kernel, per query tile: key tiles of this part that it takes
+    // part in (the first ones), and how many of them every row sees whole
+    int own[2], inner[2];
     int spare[3];
 };
-static_assert(sizeof(PagedUnit) == 48, "units are copied 16 bytes at a time");
+static_assert(sizeof(PagedUnit) == 64, "units are copied 16 bytes at a time");
 
 __device__ __forceinline__ int paged_unit_visible(const PagedGeom &gm, const PagedUnit &u, int t) {
     return gm.causal ? max(0, min(u.vis0 + t, u.len)) : u.len;

@@ -69,7 +69,7 @@ struct PtcShape {
     static constexpr int NBARS = (BAR_UEMPTY + UB + 1) / 2 * 2;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;          // tensor-memory address, abort flag
     static constexpr int OFF_BADP = OFF_MISC + 16;                // per K tile (mod 8): missing pages, bit per 16 keys
-    static constexpr int OFF_UNIT = OFF_BADP + 32;                // [UB]; spare[q]: key tiles of query tile q
+    static constexpr int OFF_UNIT = OFF_BADP + 32;                // [UB]
     static constexpr int SMEM_MIN = OFF_UNIT + UB * static_cast<int>(sizeof(PagedUnit)) + 1024;
     // (all of tensor memory is allocated: a second resident CTA would wait for it)
     static constexpr int SMEM_BYTES = SMEM_MIN <= 116 * 1024 ? 117 * 1024 : SMEM_MIN;
@@ -176,7 +176,8 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     const int t1 = min(w.ntok, (q + 1) * tpt);
                     const int keys = paged_unit_visible(gm, w, t1 - 1);
                     const int tiles = keys <= BC ? 1 : (keys - 1) / BC + 1;
-                    w.spare[q] = t1 > q * tpt ? max(0, min(tiles - w.tile0, w.tiles)) : 0;
+                    w.own[q] = t1 > q * tpt ? max(0, min(tiles - w.tile0, w.tiles)) : 0;
+                    w.inner[q] = paged_unit_visible(gm, w, q * tpt) / BC - w.tile0;
                 }
                 if (u >= S::UB && !wwait(bar(S::BAR_UEMPTY + u % S::UB), (u / S::UB - 1) & 1, 7)) break;
                 if (lane == 0) {
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 feed.report(p, w);
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    if (w.spare[q] == 0) continue;
+                    if (w.own[q] == 0) continue;
                     if (uo[q] > 0 && !wwait(bar(S::BAR_QFREE + q), (uo[q] - 1) & 1, 4)) ok = false;
                     if (ok && leader) {
                         mbar_arrive_expect_tx(bar(S::BAR_QFULL + q), S::CB * 128 * gm.g * tpt);
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 if (w->tiles == 0) break;
                 int nkv[NQ];
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) nkv[q] = w->spare[q];
+                for (int q = 0; q < NQ; ++q) nkv[q] = w->own[q];
                 const int nkv_max = w->tiles;
                 unit_done(u);
 #pragma unroll
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     }
                 };
                 auto wait_p = [&](int q, int j) -> bool {
-                    if (j == 0 && uo[q] > 0 && !wwait(bar(S::BAR_OFREE + q), (uo[q] - 1) & 1, 16)) return false;
+                    if (j == 0 && u > 0 && !wwait(bar(S::BAR_OFREE + q), (u - 1) & 1, 16)) return false;
                     if (!wwait(bar(S::BAR_PFULL + q), (sq[q] + j) & 1, 13)) return false;
                     tc_fence_after();
                     return true;
@@ -381,6 +382,11 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 t_base += 2 * nkv_max;
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
+                    if (ok && nkv[q] == 0) {
+                        // nothing for this tile: O is free and "full" at once
+                        if (u > 0) ok = wwait(bar(S::BAR_OFREE + q), (u - 1) & 1, 17);
+                        if (ok) commit(S::BAR_OFULL + q);
+                    }
                     sq[q] += nkv[q];
                     uo[q] += nkv[q] > 0 ? 1 : 0;
                 }
@@ -400,8 +406,8 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         const uint32_t tO = tmem + t_lane + S::o_col(q);
         const float sl2 = p.scale_log2;
         constexpr int OC = DP / 64;   // 32-column chunks of O of this warpgroup
-        const int tok_in = q * tpt + paged_token(gm, row_in), head_in = row_in - paged_token(gm, row_in) * gm.g;
-        const bool slot_ok = row_in < tpt * gm.g;   // g need not divide 128
+        // this row's token within the unit, or one that no unit has (g need not divide 128)
+        auto token_in = [&]() { return row_in < tpt * gm.g ? q * tpt + paged_token(gm, row_in) : 256; };
         auto xch = [&](int hh) -> uint32_t { return sbase + S::OFF_XCH + ((q * 2 + hh) * 128 + row_in) * 8; };
         auto pair_sync = [&]() { named_bar_sync(7 + q, 256); };
         auto exchange = [&](float a, float &ao) {
@@ -409,28 +415,22 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             pair_sync();
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ao) : "r"(xch(1 - h)) : "memory");
         };
-        int sq = 0, uo = 0, kt = 0;
+        int sq = 0, kt = 0;
         bool ok = true;
         for (int u = 0;; ++u) {
             // (the tile's two warpgroups leave together, whichever wait gave up)
             if (named_bar_red_or(7 + q, 256, !unit_wait(u, 9))) break;
             const PagedUnit *w = units + u % S::UB;
             if (w->tiles == 0) break;
-            const int nkvq = w->spare[q], ntok = w->ntok;
-            const bool valid = slot_ok && tok_in < ntok;
-            const int vis = valid ? paged_unit_visible(gm, *w, tok_in) : 0;
-            // keys that every row of the tile sees
-            const int vis_all = q * tpt < ntok ? paged_unit_visible(gm, *w, q * tpt) : 0;
-            const int tile0 = w->tile0;
-            float m = kNegInfP, l = 0.f;
+            const int nkvq = w->own[q], inner = w->inner[q];
+            // (a row that is none has a reference that no maximum exceeds)
+            float m = token_in() < w->ntok ? kNegInfP : -kNegInfP, l = 0.f;
             // (a wait that gives up is recorded and does not end the loop: every
             // warp still takes part in every named barrier)
             for (int j = 0; j < nkvq; ++j) {
                 if (!mbar_wait(bar(S::BAR_SFULL + q), (sq + j) & 1, abort_flag, p.err, 20)) ok = false;
                 tc_fence_after();
-                const int key0 = (tile0 + j) * BC;
-                const uint32_t bad = bad_pages[(kt + j) & 7];
-                const bool edge = key0 + BC > vis_all || bad != 0u;
+                const bool edge = j >= inner || bad_pages[(kt + j) & 7] != 0u;
                 uint32_t sr[2][32];
                 float mxc[2], mx = kNegInfP;
 #pragma unroll
@@ -446,27 +446,29 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                         reg_fence_f32(mxc[c]);
                         mx = fmaxf(mx, mxc[c]);
                     } else {
-                        const int first = key0 + h * 64 + 32 * c;
+                        // (read again rather than kept: edge tiles are few, registers fewer)
+                        const PagedUnit *w = units + u % S::UB;
+                        const int vis = paged_unit_visible(gm, *w, token_in()) - (w->tile0 + j) * BC - h * 64 - 32 * c;
                         // bits of this chunk's two 16-key groups
-                        const uint32_t b2 = (bad >> (4 * h + 2 * c)) & 3u;
+                        const uint32_t b2 = (bad_pages[(kt + j) & 7] >> (4 * h + 2 * c)) & 3u;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             float x = __uint_as_float(sr[c][e]) * sl2;
-                            x = (first + e < vis && !((b2 >> (e >> 4)) & 1u)) ? x : kNegInfP;
+                            x = (e < vis && !((b2 >> (e >> 4)) & 1u)) ? x : kNegInfP;
                             sr[c][e] = __float_as_uint(x);
                             mx = fmaxf(mx, x);
                         }
                     }
                 }
                 if (!edge) mx *= sl2;
-                if (named_bar_red_or(7 + q, 256, valid && mx > m + kThresh)) {
+                if (named_bar_red_or(7 + q, 256, mx > m + kThresh)) {
                     float mo;
                     exchange(mx, mo);
                     mx = fmaxf(mx, mo);
                 } else {
                     mx = m;
                 }
-                const float m_new = (valid && mx > m + kThresh) ? mx : m;
+                const float m_new = mx > m + kThresh ? mx : m;
                 const bool moved = m_new != m;
                 const float a = moved ? ex2(m - m_new) : 1.f;
                 m = m_new;
@@ -522,14 +524,15 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 mbar_arrive(bar(S::BAR_PFULL + q));
             }
             // ---------------- epilogue ----------------
-            const bool whole = w->slot < 0;
             float lo;
             pair_sync();
             exchange(l, lo);
             l += lo;
             pair_sync();
-            if (nkvq > 0 && ok) ok = mbar_wait(bar(S::BAR_OFULL + q), uo & 1, abort_flag, p.err, 21);
+            if (ok) ok = mbar_wait(bar(S::BAR_OFULL + q), u & 1, abort_flag, p.err, 21);
             tc_fence_after();
+            const int tok_in = token_in(), head_in = row_in - paged_token(gm, row_in) * gm.g;
+            const bool whole = w->slot < 0, valid = tok_in < w->ntok;
             const bool store = valid && !*abort_flag;
             const bool any = l > 0.f;
             const float scale_o = whole ? (any ? 1.f / l : 0.f) : 1.f;
@@ -581,12 +584,9 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     p.part_l[prow] = l;
                 }
             }
-            if (nkvq > 0) {
-                tc_fence_before();
-                mbar_arrive(bar(S::BAR_OFREE + q));
-            }
+            tc_fence_before();
+            mbar_arrive(bar(S::BAR_OFREE + q));
             sq += nkvq;
-            uo += nkvq > 0 ? 1 : 0;
         }
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
