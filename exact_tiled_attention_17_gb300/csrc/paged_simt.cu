@@ -5,44 +5,56 @@
 // of new tokens, all query heads of the group), key tile by key tile with the
 // running maximum m and sum l of the online softmax.
 //
-// A CTA of 256 threads walks its share of the units.  Q rows, a tile of 64
-// keys and its values are staged in shared memory as float32; S is a register
-// tile of RT/16 rows x 4 keys per thread, P goes through shared memory and O
-// is a register tile of RT/16 rows x d/16 columns.  Keys of pages that do not
-// exist, and keys a row does not see, have score -inf and value 0.
+// A CTA of 128 threads walks its share of the units.  Q, a tile of 64 keys and
+// its values are staged in shared memory; S is a register tile of RT/8 rows x
+// 4 keys per thread, O one of RT/8 rows x d/16 columns.  What bounds it is
+// the multiply-add rate (1.07 GFLOP of the 200-token case below are 14 us), so
+// both products run on packed pairs (fma.rn.f32x2): S pairs up along d, O
+// along its columns, with each p stored twice so that no pair is put
+// together in the loop.  Tiles are fetched with cp.async while the other
+// product runs: K of the next tile during softmax and P V, V during Q K^T.
+// Keys of pages that do not exist, and keys a row does not see, have score
+// -inf; what is not a token of the sequence is fetched as zero.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace eta {
 namespace {
 
-constexpr int kSimtThreads = 256;
+constexpr int kSimtThreads = 128;
 constexpr int kSimtKeys = 64;
-
-__device__ __forceinline__ float4 load4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
-__device__ __forceinline__ void fma4(float4 a, float4 b, float &s) {
-    s = fmaf(a.x, b.x, s);
-    s = fmaf(a.y, b.y, s);
-    s = fmaf(a.z, b.z, s);
-    s = fmaf(a.w, b.w, s);
-}
 
 template <int E, int RT>   // E = d / 32, RT: query rows of a unit
 struct SimtShape {
     static constexpr int D = 32 * E;
-    static constexpr int LD = D + 4;          // padded rows: 16 lanes reading 16 rows meet no bank twice
-    static constexpr int LP = kSimtKeys + 4;
+    static constexpr int LD = D + 4;               // padded rows: 16 lanes reading 16 rows spread over the banks
+    static constexpr int LP = 2 * kSimtKeys + 4;   // each p twice
+    static constexpr int RR = RT / 8;              // rows of a thread
+    static constexpr int NC = (D + 63) / 64;       // 4-column pieces of a thread
     static constexpr int FLOATS = RT * LD + 2 * kSimtKeys * LD + RT * LP;
-    static constexpr int SMEM = FLOATS * 4 + kSimtKeys * 8;
+    static constexpr int SMEM = FLOATS * 4 + 2 * kSimtKeys * 8;
+    static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;   // at least, on an SM
 };
 
+// 16 bytes from global to shared memory; zeros if !in.
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ ulonglong2 load2(const float *p) { return *reinterpret_cast<const ulonglong2 *>(p); }
+
 template <int E, int RT>
-__global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_simt_kernel(const PagedParams p) {
     using S = SimtShape<E, RT>;
-    constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = RT / 16;
+    constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = S::RR, NC = S::NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ PagedUnit unit;
     float *qs = smem, *ks = qs + RT * LD, *vs = ks + kSimtKeys * LD, *ps = vs + kSimtKeys * LD;
-    long long *key_at = reinterpret_cast<long long *>(ps + RT * LP);   // offset of each key's row, or -1
+    long long *key_at = reinterpret_cast<long long *>(ps + RT * LP);   // [2]: offset of each key's row, or -1
     const PagedGeom &gm = p.gm;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cta = blockIdx.x;
@@ -64,18 +76,47 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
         __syncthreads();
         const PagedUnit w = unit;
         if (w.tiles == 0) break;
-        const int rows = w.ntok * gm.g, tok0 = w.tok0;
+        const int rows = w.ntok * gm.g, tok0 = w.tok0, t1 = w.tile0 + w.tiles;
+        // where the keys of tile t lie
+        auto places = [&](int t) {
+            if (tid < kSimtKeys && t < t1) {
+                const int key = t * kSimtKeys + tid;
+                long long at = -1;
+                if (key < w.len) {
+                    const int id = paged_page(gm, w.seq, key >> gm.page_shift);
+                    if (id >= 0) at = id * p.page_stride + (key & (gm.page_size - 1)) * p.slot_stride + w.head * p.head_stride;
+                    else atomicOr(p.err, kErrWordBadRow);
+                }
+                key_at[(t & 1) * kSimtKeys + tid] = at;
+            }
+        };
+        auto fetch = [&](float *dst, const float *src, int t) {
+            if (t < t1) {
+                for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
+                    const int r = i / (D / 4), c = 4 * (i % (D / 4));
+                    const long long at = key_at[(t & 1) * kSimtKeys + r];
+                    copy16(dst + r * LD + c, at >= 0 ? src + at + c : src, at >= 0);
+                }
+            }
+            copy_commit();   // (a group every time, so that the counts below hold)
+        };
+        places(w.tile0);
+        __syncthreads();
+        fetch(ks, K, w.tile0);
+        fetch(vs, V, w.tile0);
         for (int i = tid; i < RT * (D / 4); i += kSimtThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows)
-                v = load4(Q + (tok0 + paged_token(gm, r)) * p.q_token + static_cast<long long>(w.head * gm.g + (r - paged_token(gm, r) * gm.g)) * p.q_head + c);
+            if (r < rows) {
+                const int tr = paged_token(gm, r);
+                v = __ldg(reinterpret_cast<const float4 *>(
+                    Q + (tok0 + tr) * p.q_token + static_cast<long long>(w.head * gm.g + r - tr * gm.g) * p.q_head + c));
+            }
             *reinterpret_cast<float4 *>(qs + r * LD + c) = v;
         }
         int vis[RR];   // keys that this thread's rows see
         float m[RR], l[RR];
-        float4 o[RR][E == 1 ? 1 : (E + 1) / 2];
-        static_assert(D / 64 <= 2, "columns per thread");
+        uint64_t o[RR][NC][2];
 #pragma unroll
         for (int a = 0; a < RR; ++a) {
             const int r = ty * RR + a;
@@ -83,55 +124,50 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
             m[a] = -INFINITY;
             l[a] = 0.f;
 #pragma unroll
-            for (int b = 0; b < (E + 1) / 2; ++b) o[a][b] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int b = 0; b < NC; ++b) o[a][b][0] = o[a][b][1] = 0ull;
         }
-        for (int t = w.tile0; t < w.tile0 + w.tiles; ++t) {
+        for (int t = w.tile0; t < t1; ++t) {
             const int key0 = t * kSimtKeys;
-            __syncthreads();   // the previous tile has been read
-            if (tid < kSimtKeys) {
-                const int key = key0 + tid;
-                long long at = -1;
-                if (key < w.len) {
-                    const int id = paged_page(gm, w.seq, key >> gm.page_shift);
-                    if (id >= 0) at = id * p.page_stride + (key & (gm.page_size - 1)) * p.slot_stride + w.head * p.head_stride;
-                    else atomicOr(p.err, kErrWordBadRow);
-                }
-                key_at[tid] = at;
-            }
-            __syncthreads();
-            for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
-                const int r = i / (D / 4), c = 4 * (i % (D / 4));
-                const long long at = key_at[r];
-                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-                if (at >= 0) {
-                    kv = load4(K + at + c);
-                    vv = load4(V + at + c);
-                }
-                *reinterpret_cast<float4 *>(ks + r * LD + c) = kv;
-                *reinterpret_cast<float4 *>(vs + r * LD + c) = vv;
-            }
+            places(t + 1);
+            copy_wait<1>();    // K has landed (V may be on its way)
             __syncthreads();
             // S: rows ty * RR + a, keys tx + 16 b
             float s[RR][4];
+            {
+                uint64_t acc[RR][4];
 #pragma unroll
-            for (int a = 0; a < RR; ++a)
+                for (int a = 0; a < RR; ++a)
 #pragma unroll
-                for (int b = 0; b < 4; ++b) s[a][b] = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
-                float4 kf[4];
+                    for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
+#pragma unroll 2
+                for (int c = 0; c < D; c += 4) {
+                    ulonglong2 kf[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) kf[b] = *reinterpret_cast<const float4 *>(ks + (tx + 16 * b) * LD + c);
+                    for (int b = 0; b < 4; ++b) kf[b] = load2(ks + (tx + 16 * b) * LD + c);
 #pragma unroll
-                for (int a = 0; a < RR; ++a) {
-                    const float4 qf = *reinterpret_cast<const float4 *>(qs + (ty * RR + a) * LD + c);
+                    for (int a = 0; a < RR; ++a) {
+                        const ulonglong2 qf = load2(qs + (ty * RR + a) * LD + c);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) fma4(qf, kf[b], s[a][b]);
+                        for (int b = 0; b < 4; ++b) {
+                            acc[a][b] = f2_fma(qf.x, kf[b].x, acc[a][b]);
+                            acc[a][b] = f2_fma(qf.y, kf[b].y, acc[a][b]);
+                        }
+                    }
                 }
+#pragma unroll
+                for (int a = 0; a < RR; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float x, y;
+                        f2_unpack(acc[a][b], x, y);
+                        s[a][b] = x + y;
+                    }
             }
             bool here[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) here[b] = key_at[tx + 16 * b] >= 0;
+            for (int b = 0; b < 4; ++b) here[b] = key_at[(t & 1) * kSimtKeys + tx + 16 * b] >= 0;
+            __syncthreads();   // K has been read
+            fetch(ks, K, t + 1);
 #pragma unroll
             for (int a = 0; a < RR; ++a) {
                 float mx = -INFINITY;
@@ -143,81 +179,90 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedPar
 #pragma unroll
                 for (int q = 1; q < 16; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
                 const float mn = fmaxf(m[a], mx), mu = mn == -INFINITY ? 0.f : mn;
-                const float al = m[a] == -INFINITY ? 0.f : exp2f(m[a] - mu);
+                const float al = m[a] == -INFINITY ? 0.f : ex2(m[a] - mu);
                 m[a] = mn;
                 float sum = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const float e = exp2f(s[a][b] - mu);
+                    const float e = ex2(s[a][b] - mu);
                     sum += e;
-                    ps[(ty * RR + a) * LP + tx + 16 * b] = e;
+                    *reinterpret_cast<uint64_t *>(ps + (ty * RR + a) * LP + 2 * (tx + 16 * b)) = f2_pack(e, e);
                 }
+                l[a] = l[a] * al + sum;   // (this thread's keys; joined at the end)
+                if (al != 1.f) {
+                    const uint64_t a2 = f2_pack(al, al);
 #pragma unroll
-                for (int q = 1; q < 16; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
-                l[a] = l[a] * al + sum;
-#pragma unroll
-                for (int b = 0; b < (E + 1) / 2; ++b) {
-                    o[a][b].x *= al;
-                    o[a][b].y *= al;
-                    o[a][b].z *= al;
-                    o[a][b].w *= al;
-                }
-            }
-            __syncwarp();   // a row's P is written and read by the same half-warp
-            // O: rows ty * RR + a, columns 4 tx + 64 b
-#pragma unroll 4
-            for (int k = 0; k < kSimtKeys; ++k) {
-                float4 vf[(E + 1) / 2];
-#pragma unroll
-                for (int b = 0; b < (E + 1) / 2; ++b) {
-                    const int c = 4 * tx + 64 * b;
-                    vf[b] = c < D ? *reinterpret_cast<const float4 *>(vs + k * LD + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-#pragma unroll
-                for (int a = 0; a < RR; ++a) {
-                    const float e = ps[(ty * RR + a) * LP + k];
-#pragma unroll
-                    for (int b = 0; b < (E + 1) / 2; ++b) {
-                        o[a][b].x = fmaf(e, vf[b].x, o[a][b].x);
-                        o[a][b].y = fmaf(e, vf[b].y, o[a][b].y);
-                        o[a][b].z = fmaf(e, vf[b].z, o[a][b].z);
-                        o[a][b].w = fmaf(e, vf[b].w, o[a][b].w);
+                    for (int b = 0; b < NC; ++b) {
+                        o[a][b][0] = f2_mul(o[a][b][0], a2);
+                        o[a][b][1] = f2_mul(o[a][b][1], a2);
                     }
                 }
             }
+            copy_wait<1>();    // V has landed (the next K may be on its way)
+            __syncthreads();
+            // O: rows ty * RR + a, columns 4 tx + 64 b
+#pragma unroll 2
+            for (int k = 0; k < kSimtKeys; k += 2) {
+                ulonglong2 vf[2][NC];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int b = 0; b < NC; ++b) {
+                        const int c = 4 * tx + 64 * b;
+                        vf[h][b] = (D % 64 == 0 || c < D) ? load2(vs + (k + h) * LD + c) : ulonglong2{0ull, 0ull};
+                    }
+#pragma unroll
+                for (int a = 0; a < RR; ++a) {
+                    const ulonglong2 pp = load2(ps + (ty * RR + a) * LP + 2 * k);   // (p, p) of two keys
+#pragma unroll
+                    for (int b = 0; b < NC; ++b) {
+                        o[a][b][0] = f2_fma(pp.x, vf[0][b].x, o[a][b][0]);
+                        o[a][b][1] = f2_fma(pp.x, vf[0][b].y, o[a][b][1]);
+                        o[a][b][0] = f2_fma(pp.y, vf[1][b].x, o[a][b][0]);
+                        o[a][b][1] = f2_fma(pp.y, vf[1][b].y, o[a][b][1]);
+                    }
+                }
+            }
+            __syncthreads();   // V has been read
+            fetch(vs, V, t + 1);
         }
+        copy_wait<0>();
         // the unit's rows, or this share's part of them
         const bool whole = w.slot < 0;
         const int slot = whole ? 0 : w.slot;
 #pragma unroll
         for (int a = 0; a < RR; ++a) {
+            float sum = l[a];
+#pragma unroll
+            for (int q = 1; q < 16; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
             const int r = ty * RR + a;
             if (r >= rows) continue;
-            const long long tok = tok0 + paged_token(gm, r);
-            const int head = w.head * gm.g + (r - paged_token(gm, r) * gm.g);
-            const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
+            const int tr = paged_token(gm, r);
+            const long long tok = tok0 + tr;
+            const int head = w.head * gm.g + r - tr * gm.g;
+            const size_t prow = static_cast<size_t>(slot) * p.part_rows + r;
+            const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+            float *dst = whole ? static_cast<float *>(p.O) + tok * p.o_token + static_cast<long long>(head) * p.o_head
+                               : p.part_o + prow * D;
 #pragma unroll
-            for (int b = 0; b < (E + 1) / 2; ++b) {
+            for (int b = 0; b < NC; ++b) {
                 const int c = 4 * tx + 64 * b;
                 if (c >= D) continue;
-                float4 v = o[a][b];
-                if (!whole) {
-                    *reinterpret_cast<float4 *>(p.part_o + (static_cast<size_t>(slot) * p.part_rows + r) * D + c) = v;
-                    continue;
-                }
+                float4 v;
+                f2_unpack(o[a][b][0], v.x, v.y);
+                f2_unpack(o[a][b][1], v.z, v.w);
                 v.x *= inv;
                 v.y *= inv;
                 v.z *= inv;
                 v.w *= inv;
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.O) + tok * p.o_token +
-                                            static_cast<long long>(head) * p.o_head + c) = v;
+                *reinterpret_cast<float4 *>(dst + c) = v;
             }
             if (tx == 0) {
                 if (!whole) {
-                    p.part_m[static_cast<size_t>(slot) * p.part_rows + r] = m[a];
-                    p.part_l[static_cast<size_t>(slot) * p.part_rows + r] = l[a];
+                    p.part_m[prow] = m[a];
+                    p.part_l[prow] = sum;
                 } else if (p.LSE) {
-                    p.LSE[tok * p.Hq + head] = l[a] > 0.f ? (m[a] + log2f(l[a])) * kPagedLn2 : -INFINITY;
+                    p.LSE[tok * p.Hq + head] = sum > 0.f ? (m[a] + log2f(sum)) * kPagedLn2 : -INFINITY;
                 }
             }
         }
@@ -236,7 +281,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kSimtThreads, S::SMEM) != cudaSuccess)
         return kErrCuda;
-    const int ctas = min(max(per_sm, 1) * max(nsm, 1), kPagedMaxCtas);
+    const int ctas = std::min(std::max(per_sm, 1) * std::max(nsm, 1), kPagedMaxCtas);
     p.gm.tpu = RT / p.gm.g;
     p.gm.tk = kSimtKeys;
     p.gm.unit_cost = kSimtKeys;
@@ -257,23 +302,25 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     return launch_paged_merge(p, 0, ctas, nsm, stream);
 }
 
-template <int RT>
-int launch_d(PagedParams &p, void *workspace, cudaStream_t stream) {
-    switch (p.d) {
-        case 32: return launch_one<1, RT>(p, workspace, stream);
-        case 64: return launch_one<2, RT>(p, workspace, stream);
-        case 96: return launch_one<3, RT>(p, workspace, stream);
-        case 128: return launch_one<4, RT>(p, workspace, stream);
-        default: return kErrUnsupported;
-    }
-}
-
 }  // namespace
 
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream) {
-    // Units of 16 rows where an entry's rows fit, else of 64.
-    const bool small = static_cast<long long>(p.gm.max_q) * p.gm.g <= 16;
-    return small ? launch_d<16>(p, workspace, stream) : launch_d<64>(p, workspace, stream);
+    // Units of 16 rows where an entry's rows fit; else of 32 at d > 64, where two
+    // CTAs then fit an SM, and of 64 below (and where a group alone has more than 32).
+    const bool few = static_cast<long long>(p.gm.max_q) * p.gm.g <= 16, mid = p.gm.g <= 32;
+    switch (p.d) {
+        case 32: return few ? launch_one<1, 16>(p, workspace, stream) : launch_one<1, 64>(p, workspace, stream);
+        case 64: return few ? launch_one<2, 16>(p, workspace, stream) : launch_one<2, 64>(p, workspace, stream);
+        case 96:
+            return few   ? launch_one<3, 16>(p, workspace, stream)
+                   : mid ? launch_one<3, 32>(p, workspace, stream)
+                         : launch_one<3, 64>(p, workspace, stream);
+        case 128:
+            return few   ? launch_one<4, 16>(p, workspace, stream)
+                   : mid ? launch_one<4, 32>(p, workspace, stream)
+                         : launch_one<4, 64>(p, workspace, stream);
+        default: return kErrUnsupported;
+    }
 }
 
 }  // namespace eta
