@@ -139,20 +139,23 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                 for (int a = 0; a < RR; ++a)
 #pragma unroll
                     for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
-#pragma unroll 2
+#pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
                     ulonglong2 kf[4];
 #pragma unroll
                     for (int b = 0; b < 4; ++b) kf[b] = load2(ks + (tx + 16 * b) * LD + c);
+                    // (no product next to one that it depends on)
+                    ulonglong2 qf[RR];
 #pragma unroll
-                    for (int a = 0; a < RR; ++a) {
-                        const ulonglong2 qf = load2(qs + (ty * RR + a) * LD + c);
+                    for (int a = 0; a < RR; ++a) qf[a] = load2(qs + (ty * RR + a) * LD + c);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            acc[a][b] = f2_fma(qf.x, kf[b].x, acc[a][b]);
-                            acc[a][b] = f2_fma(qf.y, kf[b].y, acc[a][b]);
-                        }
-                    }
+                    for (int a = 0; a < RR; ++a)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) acc[a][b] = f2_fma(qf[a].x, kf[b].x, acc[a][b]);
+#pragma unroll
+                    for (int a = 0; a < RR; ++a)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) acc[a][b] = f2_fma(qf[a].y, kf[b].y, acc[a][b]);
                 }
 #pragma unroll
                 for (int a = 0; a < RR; ++a)
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             copy_wait<1>();    // V has landed (the next K may be on its way)
             __syncthreads();
             // O: rows ty * RR + a, columns 4 tx + 64 b
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < kSimtKeys; k += 2) {
                 ulonglong2 vf[2][NC];
 #pragma unroll
@@ -211,17 +214,23 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                         const int c = 4 * tx + 64 * b;
                         vf[h][b] = (D % 64 == 0 || c < D) ? load2(vs + (k + h) * LD + c) : ulonglong2{0ull, 0ull};
                     }
+                ulonglong2 pp[RR];   // (p, p) of two keys
 #pragma unroll
-                for (int a = 0; a < RR; ++a) {
-                    const ulonglong2 pp = load2(ps + (ty * RR + a) * LP + 2 * k);   // (p, p) of two keys
+                for (int a = 0; a < RR; ++a) pp[a] = load2(ps + (ty * RR + a) * LP + 2 * k);
+#pragma unroll
+                for (int a = 0; a < RR; ++a)
 #pragma unroll
                     for (int b = 0; b < NC; ++b) {
-                        o[a][b][0] = f2_fma(pp.x, vf[0][b].x, o[a][b][0]);
-                        o[a][b][1] = f2_fma(pp.x, vf[0][b].y, o[a][b][1]);
-                        o[a][b][0] = f2_fma(pp.y, vf[1][b].x, o[a][b][0]);
-                        o[a][b][1] = f2_fma(pp.y, vf[1][b].y, o[a][b][1]);
+                        o[a][b][0] = f2_fma(pp[a].x, vf[0][b].x, o[a][b][0]);
+                        o[a][b][1] = f2_fma(pp[a].x, vf[0][b].y, o[a][b][1]);
                     }
-                }
+#pragma unroll
+                for (int a = 0; a < RR; ++a)
+#pragma unroll
+                    for (int b = 0; b < NC; ++b) {
+                        o[a][b][0] = f2_fma(pp[a].y, vf[1][b].x, o[a][b][0]);
+                        o[a][b][1] = f2_fma(pp[a].y, vf[1][b].y, o[a][b][1]);
+                    }
             }
             __syncthreads();   // V has been read
             fetch(vs, V, t + 1);
