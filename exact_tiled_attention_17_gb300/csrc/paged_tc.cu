@@ -13,11 +13,13 @@
 //                  thread per row; running maximum m (moved only when a tile
 //                  exceeds it by 2^8, so O is rescaled rarely) and float32
 //                  sum l of the unrounded p; P as bf16 over S in tensor memory.
-//   warp 16        TMA producer: Q tiles, then K_j, V_j into a ring of slots.
-//                  A tile is gathered page by page: one box of min(page, 128)
-//                  rows by 64 columns per copy, the table entries of the next
-//                  tile already fetched while the warp waits.
+//   warp 16        finds the CTA's work and announces it unit by unit; TMA
+//                  producer of the Q tiles and of K_j.
 //   warp 17        MMA issuer: S_q = Q_q K_j^T, O_q += P_q V_j.
+//   warp 18        TMA producer of V_j.  (K_j and V_j share a ring of slots.  A
+//                  tile is gathered page by page, one box of min(page, 128) rows
+//                  by 64 columns per copy; at 16 tokens a page that is 32 copies
+//                  a tile, which one warp issues too slowly.)
 // The work of all units is cut into equal shares, one to a CTA, which may
 // begin and end inside a unit; cut units are joined by the merge kernel.
 //
@@ -48,8 +50,8 @@ struct PtcShape {
     static constexpr int XCH_BYTES = NQ * 2 * 128 * 8;
     static constexpr int NS_RAW = (222 * 1024 - NQ * Q_BYTES - XCH_BYTES) / SLOT_BYTES;
     static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
-    static constexpr int SOFTMAX_WARPS = 16, WARP_TMA = 16, WARP_MMA = 17;
-    static constexpr int THREADS = 18 * 32;
+    static constexpr int SOFTMAX_WARPS = 16, WARP_MMA = 17, WARP_TMV = 18;   // (warp 16: Q, K and the work)
+    static constexpr int THREADS = 19 * 32;
     static constexpr int OFF_RING = NQ * Q_BYTES;
     static constexpr int OFF_XCH = OFF_RING + NS * SLOT_BYTES;
     static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         mbar_init(bar(S::BAR_TAIL), 1);
         for (int u = 0; u < S::UB; ++u) {
             mbar_init(bar(S::BAR_UFULL + u), 1);
-            mbar_init(bar(S::BAR_UEMPTY + u), S::SOFTMAX_WARPS + 1);
+            mbar_init(bar(S::BAR_UEMPTY + u), S::SOFTMAX_WARPS + 2);
         }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -147,136 +149,143 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
         const bool leader = elect_one();
-        if (warp == S::WARP_TMA) {
+        if (warp != S::WARP_MMA) {
             // --------------------------------------------------------------
-            // TMA producer.  Lane b * CB + c copies box b (box_rows keys),
-            // column block c, of a tile.
+            // TMA producers.  Lane b * CB + c copies box b (box_rows keys),
+            // column block c, of a tile; tile i of K is the ring's tile 2 i, of V
+            // 2 i + 1.
             // --------------------------------------------------------------
+            const bool is_v = warp == S::WARP_TMV;
+            const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
             if (leader) {
-                tma_prefetch_desc(&tm_q);
-                tma_prefetch_desc(&tm_k);
-                tma_prefetch_desc(&tm_v);
+                if (!is_v) tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(tm);
             }
             const int box_rows = min(gm.page_size, BC);
             const int boxes = BC / box_rows;
             const int my_box = lane / S::CB, my_cb = lane % S::CB;
+            const bool mine = my_box < boxes;
+            const uint32_t dst = my_cb * (BC * 128) + my_box * box_rows * 128;
             const uint64_t pol_q = l2_policy_evict_first();
-            int t = 0, tails = 0, kt = 0;
+            int kt = 0, tails = 0;       // K (or V) tiles issued so far
             int uo[NQ] = {0, 0};
             bool ok = true;
             PagedFeed feed;
-            feed.start(p, cta, gridDim.x);
+            if (!is_v) feed.start(p, cta, gridDim.x);
             for (int u = 0; ok; ++u) {
                 PagedUnit w;
-                feed.next(p, cta, w);
-                // K/V tiles of the part that query tile q takes part in: the first
-                // ones (causal tiles of earlier tokens end earlier); 0 without rows
+                if (is_v) {
+                    if (!__all_sync(0xffffffffu, unit_wait(u, 18))) break;
+                    w = units[u % S::UB];
+                    unit_done(u);
+                    if (w.tiles == 0) break;
+                } else {
+                    feed.next(p, cta, w);
 #pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    const int t1 = min(w.ntok, (q + 1) * tpt);
-                    const int keys = paged_unit_visible(gm, w, t1 - 1);
-                    const int tiles = keys <= BC ? 1 : (keys - 1) / BC + 1;
-                    w.own[q] = t1 > q * tpt ? max(0, min(tiles - w.tile0, w.tiles)) : 0;
-                    w.inner[q] = paged_unit_visible(gm, w, q * tpt) / BC - w.tile0;
-                }
-                if (u >= S::UB && !wwait(bar(S::BAR_UEMPTY + u % S::UB), (u / S::UB - 1) & 1, 7)) break;
-                if (lane == 0) {
-                    units[u % S::UB] = w;
-                    mbar_arrive(bar(S::BAR_UFULL + u % S::UB));
-                }
-                if (w.tiles == 0) break;
-                feed.report(p, w);
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    if (w.own[q] == 0) continue;
-                    if (uo[q] > 0 && !wwait(bar(S::BAR_QFREE + q), (uo[q] - 1) & 1, 4)) ok = false;
-                    if (ok && leader) {
-                        mbar_arrive_expect_tx(bar(S::BAR_QFULL + q), S::CB * 128 * gm.g * tpt);
-#pragma unroll
-                        for (int cb = 0; cb < S::CB; ++cb)
-                            tma_load_3d_hint(sQ + q * S::Q_BYTES + cb * (S::BR * 128), &tm_q, bar(S::BAR_QFULL + q), cb * 64,
-                                             w.head * gm.g, w.tok0 + q * tpt, pol_q);
+                    for (int q = 0; q < NQ; ++q) {
+                        const int t1 = min(w.ntok, (q + 1) * tpt);
+                        const int keys = paged_unit_visible(gm, w, t1 - 1);
+                        const int tiles = keys <= BC ? 1 : (keys - 1) / BC + 1;
+                        w.own[q] = t1 > q * tpt ? max(0, min(tiles - w.tile0, w.tiles)) : 0;
+                        w.inner[q] = paged_unit_visible(gm, w, q * tpt) / BC - w.tile0;
                     }
-                    ++uo[q];
+                    if (u >= S::UB && !wwait(bar(S::BAR_UEMPTY + u % S::UB), (u / S::UB - 1) & 1, 7)) break;
+                    if (lane == 0) {
+                        units[u % S::UB] = w;
+                        mbar_arrive(bar(S::BAR_UFULL + u % S::UB));
+                    }
+                    if (w.tiles == 0) break;
+                    feed.report(p, w);
                 }
-                // page of box my_box of tile j: -1 past the end (no keys), -2 missing
+                // page of box my_box of tile j: -1 past the end (no keys), -2 missing;
+                // looked up four tiles ahead, since a read takes about as long as a
+                // tile's matrix products
+                const int j0 = w.tile0, j1 = w.tile0 + w.tiles;
                 auto lookup = [&](int j) -> int {
                     const int key = j * BC + my_box * box_rows;
-                    if (my_box >= boxes || key >= w.len) return -1;
+                    if (j >= j1 || !mine || key >= w.len) return -1;
                     const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                     return id < 0 ? -2 : id;
                 };
-                // table entries four tiles ahead: a read takes about as long as a
-                // tile's matrix products (one ahead, tiles of 16-token pages came
-                // in at 2.0 us each instead of 1.5)
-                const int j0 = w.tile0, j1 = w.tile0 + w.tiles;
-                auto ahead = [&](int j) { return j < j1 ? lookup(j) : -1; };
-                int n0 = ahead(j0), n1 = ahead(j0 + 1), n2 = ahead(j0 + 2), n3 = ahead(j0 + 3);
+                int n0 = lookup(j0), n1 = lookup(j0 + 1), n2 = lookup(j0 + 2), n3 = lookup(j0 + 3);
+                if (!is_v) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (w.own[q] == 0) continue;
+                        if (uo[q] > 0 && !wwait(bar(S::BAR_QFREE + q), (uo[q] - 1) & 1, 4)) ok = false;
+                        if (ok && leader) {
+                            mbar_arrive_expect_tx(bar(S::BAR_QFULL + q), S::CB * 128 * gm.g * tpt);
+#pragma unroll
+                            for (int cb = 0; cb < S::CB; ++cb)
+                                tma_load_3d_hint(sQ + q * S::Q_BYTES + cb * (S::BR * 128), &tm_q, bar(S::BAR_QFULL + q),
+                                                 cb * 64, w.head * gm.g, w.tok0 + q * tpt, pol_q);
+                        }
+                        ++uo[q];
+                    }
+                }
                 for (int j = j0; ok && j < j1; ++j, ++kt) {
                     const int id = n0;
                     n0 = n1;
                     n1 = n2;
                     n2 = n3;
-                    n3 = ahead(j + 4);
-                    const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
-                    const int x = my_cb * 64, slot0 = (j * BC + my_box * box_rows) & (gm.page_size - 1);
-                    const int pg = id < 0 ? gm.pages : id;   // out of range: zeros
-                    const bool mine = my_box < boxes;
-                    const uint32_t dst = my_cb * (BC * 128) + my_box * box_rows * 128;
+                    n3 = lookup(j + 4);
+                    const int t = 2 * kt + (is_v ? 1 : 0), slot = t % S::NS, round = t / S::NS;
+                    if (round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, is_v ? 19 : 1)) {
+                        ok = false;
+                        break;
+                    }
                     // rows of V to clear: past the end, in a page that was copied
-                    const int key0 = j * BC;
-                    const int clear0 = w.len - key0;
+                    const int clear0 = w.len - j * BC;
                     const int clear1 = min(BC, (clear0 + box_rows - 1) / box_rows * box_rows);
-                    const bool tail = clear0 > 0 && clear0 < BC && clear1 > clear0;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++t) {
-                        const int slot = t % S::NS, round = t / S::NS;
-                        if (round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, 1)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t full = bar(kv == 1 && tail ? S::BAR_TAIL : S::BAR_FULL + slot);
-                        if (leader) {
-                            if (kv == 0) {
-                                // one bit for each 16 keys
-                                uint32_t bits = 0;
-                                if (missing) {
-                                    atomicOr(p.err, kErrWordBadRow);
-                                    for (int b = 0; b < boxes; ++b)
-                                        if ((missing >> (b * S::CB)) & 1u)
-                                            bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
-                                }
-                                bad_pages[kt & 7] = bits;
+                    const bool tail = is_v && clear0 > 0 && clear0 < BC && clear1 > clear0;
+                    const uint32_t full = bar(tail ? S::BAR_TAIL : S::BAR_FULL + slot);
+                    const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
+                    if (leader) {
+                        if (!is_v) {
+                            // one bit for each 16 keys
+                            uint32_t bits = 0;
+                            if (missing) {
+                                atomicOr(p.err, kErrWordBadRow);
+                                for (int b = 0; b < boxes; ++b)
+                                    if ((missing >> (b * S::CB)) & 1u)
+                                        bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
                             }
-                            mbar_arrive_expect_tx(full, S::SLOT_BYTES);
+                            bad_pages[kt & 7] = bits;
                         }
+                        mbar_arrive_expect_tx(full, S::SLOT_BYTES);
+                    }
+                    __syncwarp();
+                    if (mine)   // (an out-of-range page: zeros)
+                        tma_load_4d(sRing + slot * S::SLOT_BYTES + dst, tm, full, my_cb * 64,
+                                    (j * BC + my_box * box_rows) & (gm.page_size - 1), w.head, id < 0 ? gm.pages : id);
+                    if (tail) {
+                        if (!wwait(bar(S::BAR_TAIL), tails & 1, 6)) ok = false;
+                        ++tails;
+                        // 128-byte rows (the swizzle stays inside a row)
+                        for (int i = lane; i < (clear1 - clear0) * 8 * S::CB; i += 32) {
+                            const int c = i / ((clear1 - clear0) * 8), r = i % ((clear1 - clear0) * 8);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             sRing + slot * S::SLOT_BYTES + c * (BC * 128) + clear0 * 128 + r * 16),
+                                         "r"(0u)
+                                         : "memory");
+                        }
+                        fence_proxy_async_smem();
                         __syncwarp();
-                        if (mine)
-                            tma_load_4d(sRing + slot * S::SLOT_BYTES + dst, kv ? &tm_v : &tm_k, full, x, slot0, w.head, pg);
-                        if (kv == 1 && tail) {
-                            if (!wwait(bar(S::BAR_TAIL), tails & 1, 6)) ok = false;
-                            ++tails;
-                            // 128-byte rows (the swizzle stays inside a row)
-                            for (int i = lane; i < (clear1 - clear0) * 8 * S::CB; i += 32) {
-                                const int c = i / ((clear1 - clear0) * 8), r = i % ((clear1 - clear0) * 8);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 sRing + slot * S::SLOT_BYTES + c * (BC * 128) + clear0 * 128 + r * 16),
-                                             "r"(0u)
-                                             : "memory");
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (leader) mbar_arrive(bar(S::BAR_FULL + slot));
-                        }
+                        if (leader) mbar_arrive(bar(S::BAR_FULL + slot));
                     }
                 }
             }
-            feed.finish(p, cta);
+            if (!is_v) feed.finish(p, cta);
             // every copy this warp started has landed before the CTA may exit
-            for (int tt = max(0, t - S::NS); tt < t; ++tt) wwait(bar(S::BAR_FULL + tt % S::NS), (tt / S::NS) & 1, 2);
+            for (int i = max(0, kt - (S::NS + 1) / 2); i < kt; ++i) {
+                const int t = 2 * i + (is_v ? 1 : 0);
+                if (t + S::NS >= 2 * kt) wwait(bar(S::BAR_FULL + t % S::NS), (t / S::NS) & 1, 2);
+            }
+            if (!is_v) {
 #pragma unroll
-            for (int q = 0; q < NQ; ++q)
-                if (uo[q] > 0) wwait(bar(S::BAR_QFULL + q), (uo[q] - 1) & 1, 3);
+                for (int q = 0; q < NQ; ++q)
+                    if (uo[q] > 0) wwait(bar(S::BAR_QFULL + q), (uo[q] - 1) & 1, 3);
+            }
             __syncwarp();
         } else {
             // --------------------------------------------------------------
