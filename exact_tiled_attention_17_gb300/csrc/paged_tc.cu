@@ -82,6 +82,25 @@ struct PtcShape {
     static_assert(OFF_UNIT % 16 == 0, "alignment");
 };
 
+// N words to 16-byte aligned memory, 32 bytes at a time where that is aligned.
+template <int N>
+__device__ __forceinline__ void store_words(void *dst, const uint32_t *r) {
+    if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+        for (int k = 0; k < N; k += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<uint32_t *>(dst) + k),
+                         "r"(r[k]), "r"(r[k + 1]), "r"(r[k + 2]), "r"(r[k + 3]), "r"(r[k + 4]), "r"(r[k + 5]), "r"(r[k + 6]),
+                         "r"(r[k + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; k += 4)
+            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(static_cast<uint32_t *>(dst) + k), "r"(r[k]),
+                         "r"(r[k + 1]), "r"(r[k + 2]), "r"(r[k + 3])
+                         : "memory");
+    }
+}
+
 template <int DP>
 __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -561,27 +580,18 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     tmem_ld_wait();
                     reg_fence32(o);
                     if (!store || 32 * c >= p.d) continue;
+                    // whole 32-byte sectors where alignment allows
                     if (whole) {
                         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + at + 32 * c;
-                        uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float v0, v1;
                             f2_unpack(f2_mul(f2_pack(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2), v0, v1);
-                            pk[e] = any ? pack_bf16x2(v0, v1) : 0u;
+                            o[e] = any ? pack_bf16x2(v0, v1) : 0u;
                         }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst + 8 * k), "r"(pk[4 * k]),
-                                         "r"(pk[4 * k + 1]), "r"(pk[4 * k + 2]), "r"(pk[4 * k + 3])
-                                         : "memory");
+                        store_words<16>(dst, o);
                     } else {
-                        float *dst = p.part_o + prow * p.d + 32 * c;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(dst + 4 * k), "r"(o[4 * k]),
-                                         "r"(o[4 * k + 1]), "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
-                                         : "memory");
+                        store_words<32>(p.part_o + prow * p.d + 32 * c, o);
                     }
                 }
             }
@@ -632,7 +642,7 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     const int ctas = std::min(nsm, kPagedMaxTcCtas);
     p.gm.tpu = S::NQ * tpt;
     p.gm.tk = S::BC;
-    p.gm.unit_cost = 3 * S::BC;
+    p.gm.unit_cost = 5 * S::BC;   // (1, 3 and 8 tiles: 161, 133 and 135 us for a 4096-token prompt, 5: 131)
     p.gm.min_share = 4 * S::BC;
     paged_derive(p.gm);
     paged_carve(p, workspace, ctas, S::NQ * 128);
