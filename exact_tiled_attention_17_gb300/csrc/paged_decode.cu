@@ -10,10 +10,11 @@
 // 16 * 4 FLOPs to a key's column, a small part of what the instruction can do.
 // tcgen05 would need 128-row tiles, of which these rows fill an eighth or less.
 //
-//   warp 4         TMA producer: gathers tiles of 64 keys, page by page, into a
-//                  ring of stages (K and V of a tile on one barrier), and the
+//   warp 4         finds the CTA's work; TMA producer: gathers tiles of 64 keys
+//                  (128 at d <= 64: the same bytes), page by page, into a ring
+//                  of three stages (K and V of a tile on one barrier), and the
 //                  next unit's Q rows.
-//   warps 0 .. 3   consumers.  S = Q K^T: warp w takes keys 16 w .. 16 w + 15.
+//   warps 0 .. 3   consumers.  S = Q K^T: warp w takes a quarter of the keys.
 //                  One vote a tile whether some row's maximum exceeds its
 //                  reference by 2^8; only then do the warps exchange maxima and
 //                  rescale.  P goes through shared memory as bf16, and warp w
@@ -34,19 +35,19 @@ namespace eta {
 namespace {
 
 constexpr float kThreshD = 8.0f;
-constexpr int kDecKeys = 64;
 
 template <int DP, int MT>   // padded head dimension, 16-row blocks of a unit
 struct PdShape {
     static constexpr int CB = DP / 64;
     static constexpr int ROWS = 16 * MT;
-    static constexpr int KV_BYTES = kDecKeys * DP * 2;
+    static constexpr int KEYS = DP == 64 ? 128 : 64;                // of a tile
+    static constexpr int KV_BYTES = KEYS * DP * 2;
     static constexpr int STAGE = 2 * KV_BYTES;
     static constexpr int CTAS = 2;                                  // per SM
     static constexpr int QB = MT == 1 ? 2 : 1;                      // Q buffers
-    static constexpr int NS = DP == 64 ? 6 : 3;                     // stages: 96 KB in flight to a CTA
+    static constexpr int NS = 3;                                    // stages: 96 KB in flight to a CTA
     static constexpr int Q_BYTES = ROWS * DP * 2;
-    static constexpr int P_BYTES = ROWS * 128;
+    static constexpr int P_BYTES = ROWS * KEYS * 2;                 // [KEYS / 64][ROWS][128 bytes]
     static constexpr int OFF_Q = NS * STAGE;
     static constexpr int OFF_P = OFF_Q + QB * Q_BYTES;
     static constexpr int OFF_MX = OFF_P + P_BYTES;                  // [4][ROWS] maxima
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
     constexpr int NS = S::NS, CB = S::CB, ROWS = S::ROWS;
     constexpr int KS = DP / 16;        // K steps of Q K^T
     constexpr int NT = DP / 32;        // 8-column blocks of O to a warp
+    constexpr int KEYS = S::KEYS, KW = KEYS / 4, NK = KW / 8;   // keys of a tile, of a warp, 8-key blocks of a warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
@@ -127,11 +129,11 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
         auto wwait = [&](uint32_t b, uint32_t parity, int site) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
-        const int box_rows = min(gm.page_size, kDecKeys);
-        const int boxes = kDecKeys / box_rows;
+        const int box_rows = min(gm.page_size, KEYS);
+        const int boxes = KEYS / box_rows;
         const int my_kv = lane / (boxes * CB), my_box = lane / CB % boxes, my_cb = lane % CB;
         const bool mine = lane < 2 * boxes * CB;
-        const uint32_t dst = my_kv * S::KV_BYTES + my_cb * (kDecKeys * 128) + my_box * box_rows * 128;
+        const uint32_t dst = my_kv * S::KV_BYTES + my_cb * (KEYS * 128) + my_box * box_rows * 128;
         int t = 0, u = 0;
         bool ok = true;
         PagedFeed feed;
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
             feed.report(p, w);
             const int j1 = w.tile0 + w.tiles;
             auto lookup = [&](int j) -> int {   // page of this lane's box: -1 past the end, -2 missing
-                const int key = j * kDecKeys + my_box * box_rows;
+                const int key = j * KEYS + my_box * box_rows;
                 if (!mine || key >= w.len) return -1;
                 const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                 return id < 0 ? -2 : id;
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 __syncwarp();
                 if (mine)
                     tma_load_4d(sbase + st * S::STAGE + dst, my_kv ? &tm_v : &tm_k, bar(S::BAR_FULL + st), my_cb * 64,
-                                (j * kDecKeys + my_box * box_rows) & (gm.page_size - 1), w.head, id < 0 ? gm.pages : id);
+                                (j * KEYS + my_box * box_rows) & (gm.page_size - 1), w.head, id < 0 ? gm.pages : id);
             }
         }
         feed.finish(p, cta);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
         const float sl2 = p.scale_log2;
         const int quad = lane >> 2, col2 = (lane & 3) * 2, mat = lane >> 3;
         const int a_row = lane & 15, a_chunk = lane >> 4;             // ldmatrix lanes of an A fragment
-        const int k_row = warp * 16 + (mat >> 1) * 8 + (lane & 7), k_chunk = mat & 1;
+        const int k_row = warp * KW + (mat >> 1) * 8 + (lane & 7), k_chunk = mat & 1;
         const int v_row = (mat & 1) * 8 + (lane & 7), v_chunk = warp * (DP / 32) + (mat >> 1);
         int t = 0;
         for (int u = 0;; ++u) {
@@ -255,50 +257,59 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 const int st = t % NS;
                 mbar_wait(bar(S::BAR_FULL + st), (t / NS) & 1, abort_flag, p.err, 55);
                 const uint32_t sK = sbase + st * S::STAGE, sV = sK + S::KV_BYTES;
-                const int key0 = j * kDecKeys;
-                float s[MT][2][4];
+                const int key0 = j * KEYS;
+                float s[MT][NK][4];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int n = 0; n < NK; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) {
-                    uint32_t b[4];
-                    ldsm4(sK + (kk >> 2) * (kDecKeys * 128) + k_row * 128 + ((((kk & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), b);
+                    uint32_t b[NK / 2][4];
+#pragma unroll
+                    for (int n2 = 0; n2 < NK / 2; ++n2)
+                        ldsm4(sK + (kk >> 2) * (KEYS * 128) + (k_row + 16 * n2) * 128 +
+                                  ((((kk & 3) * 2 + k_chunk) ^ (k_row & 7)) << 4), b[n2]);
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        if constexpr (MT == 1) {
-                            mma16816(s[mt][0], qf[kk], b[0], b[1]);
-                            mma16816(s[mt][1], qf[kk], b[2], b[3]);
-                        } else {
-                            uint32_t a[4];
-                            q_frag(mt, kk, a);
-                            mma16816(s[mt][0], a, b[0], b[1]);
-                            mma16816(s[mt][1], a, b[2], b[3]);
+                        uint32_t a[4];
+                        if constexpr (MT > 1) q_frag(mt, kk, a);
+#pragma unroll
+                        for (int n2 = 0; n2 < NK / 2; ++n2) {
+                            if constexpr (MT == 1) {
+                                mma16816(s[mt][2 * n2], qf[kk], b[n2][0], b[n2][1]);
+                                mma16816(s[mt][2 * n2 + 1], qf[kk], b[n2][2], b[n2][3]);
+                            } else {
+                                mma16816(s[mt][2 * n2], a, b[n2][0], b[n2][1]);
+                                mma16816(s[mt][2 * n2 + 1], a, b[n2][2], b[n2][3]);
+                            }
                         }
                     }
                 }
                 // scaled and masked scores, and whether a maximum moves
                 const uint32_t bad = bad_pages[st];
-                const bool edge = key0 + kDecKeys > vis_all || bad != 0u;
-                const bool gone = (bad >> warp) & 1u;
+                const bool edge = key0 + KEYS > vis_all || bad != 0u;
                 float mx[MT][2];
                 bool move = false;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
+                        float v = -INFINITY;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < NK; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 float x = s[mt][n][2 * i + e] * sl2;
-                                if (edge) x = (!gone && key0 + warp * 16 + n * 8 + col2 + e < vis[mt][i]) ? x : -INFINITY;
+                                if (edge) {
+                                    const int key = warp * KW + n * 8 + col2 + e;
+                                    x = (!((bad >> (key >> 4)) & 1u) && key0 + key < vis[mt][i]) ? x : -INFINITY;
+                                }
                                 s[mt][n][2 * i + e] = x;
+                                v = fmaxf(v, x);
                             }
-                        float v = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                         mx[mt][i] = v;
@@ -338,10 +349,12 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                         const float mu = m[mt][i] == -INFINITY ? 0.f : m[mt][i];
                         const int r = mt * 16 + quad + 8 * i;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
+                        for (int n = 0; n < NK; ++n) {
                             const float p0 = ex2(s[mt][n][2 * i] - mu), p1 = ex2(s[mt][n][2 * i + 1] - mu);
                             l[mt][i] += p0 + p1;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + r * 128 + (((warp * 2 + n) ^ (r & 7)) << 4) + col2 * 2),
+                            const int chunk = warp * NK + n;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + (chunk >> 3) * (ROWS * 128) + r * 128 +
+                                                                          (((chunk & 7) ^ (r & 7)) << 4) + col2 * 2),
                                          "r"(pack_bf16x2(p0, p1))
                                          : "memory");
                         }
@@ -350,13 +363,13 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                 // O += P V, this warp's columns
                 const int live = w.len - key0;   // slots of the tile that hold tokens
 #pragma unroll
-                for (int ks = 0; ks < kDecKeys / 16; ++ks) {
+                for (int ks = 0; ks < KEYS / 16; ++ks) {
                     uint32_t vf[NT / 2][4];
 #pragma unroll
                     for (int n2 = 0; n2 < NT / 2; ++n2) {
                         const int key = ks * 16 + v_row, chunk = v_chunk + 2 * n2;
-                        ldsm4t(sV + (chunk >> 3) * (kDecKeys * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), vf[n2]);
-                        if (live < kDecKeys) {
+                        ldsm4t(sV + (chunk >> 3) * (KEYS * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4), vf[n2]);
+                        if (live < KEYS) {
                             // clear what lies past the end
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t a[4];
                         const int r = mt * 16 + a_row;
-                        ldsm4(sP + r * 128 + (((ks * 2 + a_chunk) ^ (r & 7)) << 4), a);
+                        ldsm4(sP + (ks >> 2) * (ROWS * 128) + r * 128 + ((((ks & 3) * 2 + a_chunk) ^ (r & 7)) << 4), a);
 #pragma unroll
                         for (int n2 = 0; n2 < NT / 2; ++n2) {
                             mma16816(o[mt][2 * n2], a, vf[n2][0], vf[n2][1]);
@@ -458,12 +471,12 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     }
     const PagedGeom &gm = p.gm;
     p.gm.tpu = S::ROWS / gm.g;
-    p.gm.tk = kDecKeys;
-    p.gm.unit_cost = kDecKeys;
-    p.gm.min_share = 2 * kDecKeys;
+    p.gm.tk = S::KEYS;
+    p.gm.unit_cost = S::KEYS;
+    p.gm.min_share = 128;
     paged_derive(p.gm);
     CUtensorMap tq, tk, tv;
-    if (!paged_maps(p, S::ROWS / gm.g, std::min(gm.page_size, kDecKeys), &tq, &tk, &tv)) return kErrCuda;
+    if (!paged_maps(p, S::ROWS / gm.g, std::min(gm.page_size, S::KEYS), &tq, &tk, &tv)) return kErrCuda;
     paged_carve(p, workspace, grid, S::ROWS);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
