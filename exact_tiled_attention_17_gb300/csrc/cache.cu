@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace eta {
@@ -558,17 +559,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
 }
 
 template <typename K, typename... A>
-int launch(K kern, unsigned grid, int threads, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? kOk : kErrCuda;
+int launch(K kern, unsigned grid, int threads, cudaStream_t stream, const A &...args) {
+    return launch_dependent(kern, dim3(grid), static_cast<unsigned>(threads), 0, stream, args...);
 }
 
 int copy_grid() {

@@ -48,6 +48,12 @@ __device__ __forceinline__ int paged_sum(int tail_rows, bool part, bool last) {
     return tail_rows << 2 | (last ? 2 : 0) | (part ? 1 : 0);
 }
 
+// The maximum that goes with a part's sum: -inf for a part without keys, and
+// something finite where the sum is NaN, so that the merge passes the NaN on.
+__device__ __forceinline__ float paged_part_max(float m, float l) {
+    return l == 0.f ? -INFINITY : m == -INFINITY ? 0.f : m;
+}
+
 // Reads the parameters once, while the kernel waits for the one before it: a
 // first touch of a line of the parameter bank takes about half a microsecond,
 // and a short call touches all of them one after the other.

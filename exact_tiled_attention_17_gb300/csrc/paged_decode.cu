@@ -29,6 +29,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace eta {
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     const int tr = paged_token(gm, r);
                     const long long tok = w.tok0 + tr;
                     const int head = w.head * gm.g + r - tr * gm.g;
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    const float inv = L != 0.f ? 1.f / L : 0.f;   // (a NaN goes on)
                     const size_t prow = static_cast<size_t>(whole ? 0 : w.slot) * p.part_rows + r;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
@@ -436,10 +437,10 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     }
                     if (warp == 0 && (lane & 3) == 0) {
                         if (!whole) {
-                            p.part_m[prow] = L > 0.f ? m[mt][i] : -INFINITY;
+                            p.part_m[prow] = paged_part_max(m[mt][i], L);
                             p.part_l[prow] = L;
                         } else if (p.LSE) {
-                            p.LSE[tok * p.Hq + head] = L > 0.f ? (m[mt][i] + log2f(L)) * kPagedLn2 : -INFINITY;
+                            p.LSE[tok * p.Hq + head] = L != 0.f ? (m[mt][i] + log2f(L)) * kPagedLn2 : -INFINITY;
                         }
                     }
                 }
@@ -478,17 +479,8 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     CUtensorMap tq, tk, tv;
     if (!paged_maps(p, S::ROWS / gm.g, std::min(gm.page_size, S::KEYS), &tq, &tk, &tv)) return kErrCuda;
     paged_carve(p, workspace, grid, S::ROWS);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(160);
-    cfg.dynamicSmemBytes = S::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
+    const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), 160, S::SMEM_BYTES, stream, tq, tk, tv, p);
+    if (rc != kOk) return rc;
     return launch_paged_merge(p, 1, grid, grid / S::CTAS, stream);
 }
 

@@ -18,6 +18,7 @@
 // two parts, as nearly always in a large batch, a warp takes four rows at once.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace eta {
@@ -149,8 +150,8 @@ __device__ __forceinline__ void merge_row(const PagedParams &p, int ctas, int c,
     const int t = paged_token(p.gm, row);
     const long long tok = own.tok0 + t;
     const int hq = own.head * p.gm.g + row - t * p.gm.g;
-    store_row<E, BF16>(p.O, tok * p.o_token + static_cast<long long>(hq) * p.o_head + E * lane, acc, L > 0.f ? 1.f / L : 0.f);
-    if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = L > 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+    store_row<E, BF16>(p.O, tok * p.o_token + static_cast<long long>(hq) * p.o_head + E * lane, acc, L != 0.f ? 1.f / L : 0.f);
+    if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = L != 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
 }
 
 // Four rows (row, row + kMergeWarps, ...) of a unit of two parts: lane 2 q + s reads m and l of row q's part s.
@@ -196,8 +197,8 @@ __device__ __forceinline__ void merge_rows4(const PagedParams &p, int c, int row
         const long long tok = own.tok0 + t;
         const int hq = own.head * p.gm.g + r - t * p.gm.g;
         store_row<E, BF16>(p.O, tok * p.o_token + static_cast<long long>(hq) * p.o_head + E * lane, acc[q],
-                           Lq > 0.f ? 1.f / Lq : 0.f);
-        if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = Lq > 0.f ? (Mq + log2f(Lq)) * kPagedLn2 : -INFINITY;
+                           Lq != 0.f ? 1.f / Lq : 0.f);
+        if (lane == 0 && p.LSE) p.LSE[tok * p.Hq + hq] = Lq != 0.f ? (Mq + log2f(Lq)) * kPagedLn2 : -INFINITY;
     }
 }
 
@@ -263,20 +264,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
 
 template <int E, bool BF16, bool FEW>
 int launch_one(const PagedParams &p, int ctas, int sms, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
     // at most ctas units are cut, of at most as many rows as an entry has
     const long long rows = std::min<long long>(p.part_rows, static_cast<long long>(p.gm.max_q) * p.gm.g);
-    const long long per = (rows + kMergeWarps - 1) / kMergeWarps;
-    if (FEW) cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(per));
-    else cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(ctas * per, 4LL * sms)));
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<E, BF16, FEW>, p, ctas) == cudaSuccess ? kOk : kErrCuda;
+    const unsigned per = static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps);
+    const dim3 grid = FEW ? dim3(static_cast<unsigned>(ctas), per)
+                          : dim3(std::min(static_cast<unsigned>(ctas) * per, 4u * static_cast<unsigned>(sms)));
+    return launch_dependent(paged_merge_kernel<E, BF16, FEW>, grid, kMergeThreads, 0, stream, p, ctas);
 }
 
 template <int E>

@@ -17,6 +17,7 @@
 // -inf; what is not a token of the sequence is fetched as zero.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace eta {
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             const long long tok = tok0 + tr;
             const int head = w.head * gm.g + r - tr * gm.g;
             const size_t prow = static_cast<size_t>(slot) * p.part_rows + r;
-            const float inv = !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = !whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;   // (a NaN goes on)
             float *dst = whole ? static_cast<float *>(p.O) + tok * p.o_token + static_cast<long long>(head) * p.o_head
                                : p.part_o + prow * D;
 #pragma unroll
@@ -268,10 +269,10 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             }
             if (tx == 0) {
                 if (!whole) {
-                    p.part_m[prow] = m[a];
+                    p.part_m[prow] = paged_part_max(m[a], sum);
                     p.part_l[prow] = sum;
                 } else if (p.LSE) {
-                    p.LSE[tok * p.Hq + head] = sum > 0.f ? (m[a] + log2f(sum)) * kPagedLn2 : -INFINITY;
+                    p.LSE[tok * p.Hq + head] = sum != 0.f ? (m[a] + log2f(sum)) * kPagedLn2 : -INFINITY;
                 }
             }
         }
@@ -297,17 +298,8 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.min_share = 2 * kSimtKeys;
     paged_derive(p.gm);
     paged_carve(p, workspace, ctas, RT);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kSimtThreads);
-    cfg.dynamicSmemBytes = S::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return kErrCuda;
+    const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kSimtThreads, S::SMEM, stream, p);
+    if (rc != kOk) return rc;
     return launch_paged_merge(p, 0, ctas, nsm, stream);
 }
 

@@ -33,6 +33,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace eta {
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             const int tok_in = token_in(), head_in = row_in - paged_token(gm, row_in) * gm.g;
             const bool whole = w->slot < 0, valid = tok_in < w->ntok;
             const bool store = valid && !*abort_flag;
-            const bool any = l > 0.f;
+            const bool any = l != 0.f;   // (a NaN goes on)
             const float scale_o = whole ? (any ? 1.f / l : 0.f) : 1.f;
             const uint64_t inv2 = f2_pack(scale_o, scale_o);
             const int unit_row = q * tpt * gm.g + row_in;
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 if (whole) {
                     if (p.LSE) p.LSE[tok * p.Hq + head] = any ? (m + log2f(l)) * kPagedLn2 : kNegInfP;
                 } else {
-                    p.part_m[prow] = nkvq > 0 && any ? m : kNegInfP;
+                    p.part_m[prow] = nkvq > 0 ? paged_part_max(m, l) : kNegInfP;
                     p.part_l[prow] = l;
                 }
             }
@@ -646,17 +647,8 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.min_share = 4 * S::BC;
     paged_derive(p.gm);
     paged_carve(p, workspace, ctas, S::NQ * 128);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(S::THREADS);
-    cfg.dynamicSmemBytes = S::SMEM_BYTES;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p) != cudaSuccess) return kErrCuda;
+    const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), S::THREADS, S::SMEM_BYTES, stream, tq, tk, tv, p);
+    if (rc != kOk) return rc;
     return launch_paged_merge(p, 1, ctas, nsm, stream);
 }
 

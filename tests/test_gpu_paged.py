@@ -229,6 +229,39 @@ def test_scores_of_any_size(eta, new):
     attend(eta, cache, [new], 2)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new,n", [(1, 100), (1, 5000), (40, 100), (40, 5000)])
+def test_nan_reaches_its_own_rows_only(eta, dtype, new, n):
+    """A NaN in one query row, or in a key, is seen where it belongs and nowhere else."""
+    cache = build(eta, [n, 77], 2, 16, 64, dtype)
+    q = queries(new + 3, 8, 64, dtype)
+    q[0, 3] = math.nan
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, ints([0, new, new + 3]))
+    bad = torch.zeros(new + 3, 8, dtype=torch.bool)
+    bad[0, 3] = True
+    assert torch.equal(torch.isnan(o).all(2).cpu(), bad) and torch.equal(torch.isnan(o).any(2).cpu(), bad)
+    assert torch.equal(torch.isnan(lse).cpu(), bad)
+    q[0, 3] = 0.5
+    cache.k[0, int(cache.page_table[1, 74 // 16]), 1, 74 % 16, 5] = math.nan   # seen by the second entry's rows, kv head 1
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, ints([0, new, new + 3]))
+    bad = torch.zeros(new + 3, 8, dtype=torch.bool)
+    bad[new:, 4:] = True
+    assert torch.equal(torch.isnan(lse).cpu(), bad)
+    assert torch.equal(torch.isnan(o).all(2).cpu(), bad) and torch.equal(torch.isnan(o).any(2).cpu(), bad)
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_entries_past_max_q_are_left_out(eta, dtype):
+    cache = build(eta, [100, 90], 1, 16, 64, dtype)
+    q = queries(30, 4, 64, dtype)
+    o, lse = torch.full_like(q, 7.0), torch.full((30, 4), 7.0, device="cuda")
+    eta.attn_paged_fwd(q, cache, 0, None, ints([0, 20, 30]), max_q=10, out=o, lse=lse)
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert (o[:20] == 7).all() and (lse[:20] == 7).all()
+    check_attention(q[20:], cache, 0, ints([1]), ints([0, 10]), True, 0.125, o[20:], lse[20:])
+
+
 def test_streams_and_graphs(eta):
     """A call on another stream; a captured one replayed after the lengths changed."""
     cache = build(eta, [500, 40, 300], 2, 16, 128, BF16, spare=30, max_pages=40)
