@@ -473,6 +473,10 @@ def _paged_list(t, cache, name, n=None):
     return t.data_ptr()
 
 
+_lib_reserve, _lib_free, _lib_fork = lib.attn_cache_reserve, lib.attn_cache_free, lib.attn_cache_fork
+_lib_compact, _lib_append, _lib_paged_fwd = lib.attn_cache_compact, lib.attn_cache_append, lib.attn_paged_fwd
+
+
 @contextlib.contextmanager
 def _paged_scope(cache, stream):
     """The cache's device is current, and `stream` too, so that memory
@@ -486,12 +490,11 @@ def _paged_scope(cache, stream):
                 yield st.cuda_stream
 
 
-def _paged_call(cache, stream, body, *args):
-    """body(cache, stream handle, *args) on the cache's device and the stream."""
-    if stream is None and _device_index() == cache._index:
-        return body(cache, _raw_stream(cache._index), *args)
-    with _paged_scope(cache, stream) as st:
-        return body(cache, st, *args)
+def _paged_here(cache, stream):
+    """Whether a call can go out as things are: no stream of its own, and the
+    cache's device current.  (A decode step is made of calls that take a few
+    microseconds; entering _paged_scope costs as much.)"""
+    return stream is None and _device_index() == cache._index
 
 
 _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
@@ -532,7 +535,7 @@ def _granted(granted, cache, n):
 def _reserve(cache, st, a, b, n, granted, workspace):
     g = _granted(granted, cache, n)
     ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
-    _check(lib.attn_cache_reserve(cache._p, a, b, n, g.data_ptr(), ws[2], ws[1], st), "attn_cache_reserve")
+    _check(_lib_reserve(cache._p, a, b, n, g.data_ptr(), ws[2], ws[1], st), "attn_cache_reserve")
     return g
 
 
@@ -542,11 +545,10 @@ def attn_cache_reserve(cache, seqs, n_new, granted=None, workspace=None, stream=
     granted, int32 [n]: 1, or 0 for an entry that got nothing."""
     n = seqs.shape[0]
     a, b = _paged_list(seqs, cache, "seqs"), _paged_list(n_new, cache, "n_new", n)
-    return _paged_call(cache, stream, _reserve, a, b, n, granted, workspace)
-
-
-def _free(cache, st, a, b, n):
-    _check(lib.attn_cache_free(cache._p, a, b, n, st), "attn_cache_free")
+    if _paged_here(cache, stream):
+        return _reserve(cache, _raw_stream(cache._index), a, b, n, granted, workspace)
+    with _paged_scope(cache, stream) as st:
+        return _reserve(cache, st, a, b, n, granted, workspace)
 
 
 def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
@@ -554,13 +556,18 @@ def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
     n = seqs.shape[0]
     a = _paged_list(seqs, cache, "seqs")
     b = None if keep is None else _paged_list(keep, cache, "keep", n)
-    _paged_call(cache, stream, _free, a, b, n)
+    if _paged_here(cache, stream):
+        rc = _lib_free(cache._p, a, b, n, _raw_stream(cache._index))
+    else:
+        with _paged_scope(cache, stream) as st:
+            rc = _lib_free(cache._p, a, b, n, st)
+    _check(rc, "attn_cache_free")
 
 
 def _fork(cache, st, a, b, n, copy, granted, workspace):
     g = _granted(granted, cache, n)
     ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
-    _check(lib.attn_cache_fork(cache._p, a, b, n, copy, g.data_ptr(), ws[2], ws[1], st), "attn_cache_fork")
+    _check(_lib_fork(cache._p, a, b, n, copy, g.data_ptr(), ws[2], ws[1], st), "attn_cache_fork")
     return g
 
 
@@ -570,7 +577,10 @@ def attn_cache_fork(cache, parents, children, copy: bool = False, granted=None, 
     copied.  Returns granted, int32 [n]."""
     n = parents.shape[0]
     a, b = _paged_list(parents, cache, "parents"), _paged_list(children, cache, "children", n)
-    return _paged_call(cache, stream, _fork, a, b, n, int(bool(copy)), granted, workspace)
+    if _paged_here(cache, stream):
+        return _fork(cache, _raw_stream(cache._index), a, b, n, 1 if copy else 0, granted, workspace)
+    with _paged_scope(cache, stream) as st:
+        return _fork(cache, st, a, b, n, 1 if copy else 0, granted, workspace)
 
 
 def _compact(cache, st, inplace, workspace):
@@ -578,8 +588,7 @@ def _compact(cache, st, inplace, workspace):
     refs = cache.ref_counts if inplace else torch.empty_like(cache.ref_counts)
     n_live = torch.empty(1, dtype=torch.int32, device=cache.device)
     ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, 0), cache, st)
-    _check(lib.attn_cache_compact(cache._p, table.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws[2], ws[1], st),
-           "attn_cache_compact")
+    _check(_lib_compact(cache._p, table.data_ptr(), refs.data_ptr(), n_live.data_ptr(), ws[2], ws[1], st), "attn_cache_compact")
     return table, refs, n_live
 
 
@@ -588,11 +597,10 @@ def attn_cache_compact(cache, inplace: bool = True, workspace=None, stream=None)
     ref_counts, n_live): the cache's own tensors, updated, or with
     inplace=False new ones, the cache's staying as they were (and valid, since
     only free pages are written); n_live is an int32 device tensor [1]."""
-    return _paged_call(cache, stream, _compact, inplace, workspace)
-
-
-def _append(cache, st, *args):
-    _check(lib.attn_cache_append(cache._p, *args, st), "attn_cache_append")
+    if _paged_here(cache, stream):
+        return _compact(cache, _raw_stream(cache._index), inplace, workspace)
+    with _paged_scope(cache, stream) as st:
+        return _compact(cache, st, inplace, workspace)
 
 
 def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None) -> None:
@@ -611,7 +619,13 @@ def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=Non
     n = q_start.shape[0] - 1
     a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
     b = _paged_list(q_start, cache, "q_start")
-    _paged_call(cache, stream, _append, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n)
+    if _paged_here(cache, stream):
+        rc = _lib_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n,
+                         _raw_stream(cache._index))
+    else:
+        with _paged_scope(cache, stream) as st:
+            rc = _lib_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n, st)
+    _check(rc, "attn_cache_append")
 
 
 @functools.lru_cache(maxsize=256)
@@ -632,7 +646,7 @@ def _paged_fwd(cache, st, q, layer, shape, a, b, n, max_q, causal, scale, o, l, 
     # (arguments the library rejects give a size of 0 here; it then says which)
     ws = _paged_workspace(workspace, _paged_workspace_size(Hq, cache.heads, max(max_q, 1), d, cache._code), cache, st)
     qs, os_ = q.stride(), o.stride()
-    _check(lib.attn_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(), qs[0], qs[1],
+    _check(_lib_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(), qs[0], qs[1],
                               os_[0], os_[1], T, Hq, a, b, n, max_q, causal, scale, ws[2], ws[1], st),
            "attn_paged_fwd")
     return o, l
@@ -663,8 +677,12 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
                             lse.get_device() != cache._index):
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq] on q's device")
-    return _paged_call(cache, stream, _paged_fwd, q, layer, shape, a, b, n, shape[0] if max_q is None else int(max_q),
-                       1 if causal else 0, cache._scale if scale is None else float(scale), out, lse, want_lse, workspace)
+    args = (q, layer, shape, a, b, n, shape[0] if max_q is None else int(max_q), 1 if causal else 0,
+            cache._scale if scale is None else float(scale), out, lse, want_lse, workspace)
+    if _paged_here(cache, stream):
+        return _paged_fwd(cache, _raw_stream(cache._index), *args)
+    with _paged_scope(cache, stream) as st:
+        return _paged_fwd(cache, st, *args)
 
 
 def attn_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:
