@@ -10,9 +10,12 @@
 // 4 keys per thread, O one of RT/8 rows x d/16 columns.  What bounds it is
 // the multiply-add rate (1.07 GFLOP of the 200-token case below are 14 us), so
 // both products run on packed pairs (fma.rn.f32x2): S pairs up along d, O
-// along its columns, with each p stored twice so that no pair is put
-// together in the loop.  Tiles are fetched with cp.async while the other
+// along its rows, for which P lies key by key in shared memory.  Tiles are fetched with cp.async while the other
 // product runs: K of the next tile during softmax and P V, V during Q K^T.
+// Measured: 8.9 GFLOP (4 x 256 tokens over 2000, 16 heads of 64) in 246 us, the
+// multiply-add pipe busy 55 % of the time.  The two warps of a scheduler that fit
+// do not hide each other's latencies; a third CTA needs 168 registers, spills and
+// is slower (252 us), as are narrower register tiles (16 x 16 threads: 291 us).
 // Keys of pages that do not exist, and keys a row does not see, have score
 // -inf; what is not a token of the sequence is fetched as zero.
 #include <algorithm>
@@ -30,12 +33,12 @@ template <int E, int RT>   // E = d / 32, RT: query rows of a unit
 struct SimtShape {
     static constexpr int D = 32 * E;
     static constexpr int LD = D + 4;               // padded rows: 16 lanes reading 16 rows spread over the banks
-    static constexpr int LP = 2 * kSimtKeys + 4;   // each p twice
+    static constexpr int LP = RT + 4;              // P: [key][row]
     static constexpr int RR = RT / 8;              // rows of a thread
     static constexpr int NC = (D + 63) / 64;       // 4-column pieces of a thread
-    static constexpr int FLOATS = RT * LD + 2 * kSimtKeys * LD + RT * LP;
+    static constexpr int FLOATS = RT * LD + 2 * kSimtKeys * LD + kSimtKeys * LP;
     static constexpr int SMEM = FLOATS * 4 + 2 * kSimtKeys * 8;
-    static constexpr int CTAS = SMEM <= 112 * 1024 ? 2 : 1;   // at least, on an SM
+    static constexpr int CTAS = RT < 64 && SMEM <= 74 * 1024 ? 3 : SMEM <= 112 * 1024 ? 2 : 1;   // at least, on an SM
 };
 
 // 16 bytes from global to shared memory; zeros if !in.
@@ -55,7 +58,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
     extern __shared__ __align__(16) float smem[];
     __shared__ PagedUnit unit;
     float *qs = smem, *ks = qs + RT * LD, *vs = ks + kSimtKeys * LD, *ps = vs + kSimtKeys * LD;
-    long long *key_at = reinterpret_cast<long long *>(ps + RT * LP);   // [2]: offset of each key's row, or -1
+    long long *key_at = reinterpret_cast<long long *>(ps + kSimtKeys * LP);   // [2]: offset of each key's row, or -1
     const PagedGeom &gm = p.gm;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int cta = blockIdx.x;
@@ -117,16 +120,20 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
         }
         int vis[RR];   // keys that this thread's rows see
         float m[RR], l[RR];
-        uint64_t o[RR][NC][2];
+        uint64_t o[RR / 2][NC][4];   // pairs of rows
 #pragma unroll
         for (int a = 0; a < RR; ++a) {
             const int r = ty * RR + a;
             vis[a] = r < rows ? paged_unit_visible(gm, w, paged_token(gm, r)) : 0;
             m[a] = -INFINITY;
             l[a] = 0.f;
-#pragma unroll
-            for (int b = 0; b < NC; ++b) o[a][b][0] = o[a][b][1] = 0ull;
         }
+#pragma unroll
+        for (int a = 0; a < RR / 2; ++a)
+#pragma unroll
+            for (int b = 0; b < NC; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[a][b][e] = 0ull;
         for (int t = w.tile0; t < t1; ++t) {
             const int key0 = t * kSimtKeys;
             places(t + 1);
@@ -172,6 +179,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             for (int b = 0; b < 4; ++b) here[b] = key_at[(t & 1) * kSimtKeys + tx + 16 * b] >= 0;
             __syncthreads();   // K has been read
             fetch(ks, K, t + 1);
+            float alpha[RR];
 #pragma unroll
             for (int a = 0; a < RR; ++a) {
                 float mx = -INFINITY;
@@ -188,50 +196,59 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                 float sum = 0.f;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const float e = ex2(s[a][b] - mu);
-                    sum += e;
-                    *reinterpret_cast<uint64_t *>(ps + (ty * RR + a) * LP + 2 * (tx + 16 * b)) = f2_pack(e, e);
+                    s[a][b] = ex2(s[a][b] - mu);
+                    sum += s[a][b];
                 }
                 l[a] = l[a] * al + sum;   // (this thread's keys; joined at the end)
-                if (al != 1.f) {
-                    const uint64_t a2 = f2_pack(al, al);
+                alpha[a] = al;
+            }
 #pragma unroll
-                    for (int b = 0; b < NC; ++b) {
-                        o[a][b][0] = f2_mul(o[a][b][0], a2);
-                        o[a][b][1] = f2_mul(o[a][b][1], a2);
-                    }
+            for (int b = 0; b < 4; ++b) {
+                float *at = ps + (tx + 16 * b) * LP + ty * RR;
+                if constexpr (RR >= 4) {
+#pragma unroll
+                    for (int a = 0; a < RR; a += 4)
+                        *reinterpret_cast<float4 *>(at + a) = make_float4(s[a][b], s[a + 1][b], s[a + 2][b], s[a + 3][b]);
+                } else {
+                    *reinterpret_cast<float2 *>(at) = make_float2(s[0][b], s[1][b]);
                 }
+            }
+#pragma unroll
+            for (int a = 0; a < RR / 2; ++a) {
+                if (alpha[2 * a] == 1.f && alpha[2 * a + 1] == 1.f) continue;
+                const uint64_t a2 = f2_pack(alpha[2 * a], alpha[2 * a + 1]);
+#pragma unroll
+                for (int b = 0; b < NC; ++b)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[a][b][e] = f2_mul(o[a][b][e], a2);
             }
             copy_wait<1>();    // V has landed (the next K may be on its way)
             __syncthreads();
             // O: rows ty * RR + a, columns 4 tx + 64 b
 #pragma unroll 4
-            for (int k = 0; k < kSimtKeys; k += 2) {
-                ulonglong2 vf[2][NC];
+            for (int k = 0; k < kSimtKeys; ++k) {
+                uint64_t pp[RR / 2];
+                if constexpr (RR >= 4) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int b = 0; b < NC; ++b) {
-                        const int c = 4 * tx + 64 * b;
-                        vf[h][b] = (D % 64 == 0 || c < D) ? load2(vs + (k + h) * LD + c) : ulonglong2{0ull, 0ull};
+                    for (int a = 0; a < RR / 2; a += 2) {
+                        const ulonglong2 v = load2(ps + k * LP + ty * RR + 2 * a);
+                        pp[a] = v.x;
+                        pp[a + 1] = v.y;
                     }
-                ulonglong2 pp[RR];   // (p, p) of two keys
+                } else {
+                    pp[0] = *reinterpret_cast<const uint64_t *>(ps + k * LP + ty * RR);
+                }
 #pragma unroll
-                for (int a = 0; a < RR; ++a) pp[a] = load2(ps + (ty * RR + a) * LP + 2 * k);
+                for (int b = 0; b < NC; ++b) {
+                    const int c = 4 * tx + 64 * b;
+                    const float4 v = (D % 64 == 0 || c < D) ? *reinterpret_cast<const float4 *>(vs + k * LD + c)
+                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const uint64_t vv[4] = {f2_pack(v.x, v.x), f2_pack(v.y, v.y), f2_pack(v.z, v.z), f2_pack(v.w, v.w)};
 #pragma unroll
-                for (int a = 0; a < RR; ++a)
+                    for (int a = 0; a < RR / 2; ++a)
 #pragma unroll
-                    for (int b = 0; b < NC; ++b) {
-                        o[a][b][0] = f2_fma(pp[a].x, vf[0][b].x, o[a][b][0]);
-                        o[a][b][1] = f2_fma(pp[a].x, vf[0][b].y, o[a][b][1]);
-                    }
-#pragma unroll
-                for (int a = 0; a < RR; ++a)
-#pragma unroll
-                    for (int b = 0; b < NC; ++b) {
-                        o[a][b][0] = f2_fma(pp[a].y, vf[1][b].x, o[a][b][0]);
-                        o[a][b][1] = f2_fma(pp[a].y, vf[1][b].y, o[a][b][1]);
-                    }
+                        for (int e = 0; e < 4; ++e) o[a][b][e] = f2_fma(pp[a], vv[e], o[a][b][e]);
+                }
             }
             __syncthreads();   // V has been read
             fetch(vs, V, t + 1);
@@ -258,14 +275,14 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             for (int b = 0; b < NC; ++b) {
                 const int c = 4 * tx + 64 * b;
                 if (c >= D) continue;
-                float4 v;
-                f2_unpack(o[a][b][0], v.x, v.y);
-                f2_unpack(o[a][b][1], v.z, v.w);
-                v.x *= inv;
-                v.y *= inv;
-                v.z *= inv;
-                v.w *= inv;
-                *reinterpret_cast<float4 *>(dst + c) = v;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float lo, hi;
+                    f2_unpack(o[a / 2][b][e], lo, hi);
+                    v[e] = (a & 1 ? hi : lo) * inv;
+                }
+                *reinterpret_cast<float4 *>(dst + c) = make_float4(v[0], v[1], v[2], v[3]);
             }
             if (tx == 0) {
                 if (!whole) {
