@@ -384,61 +384,68 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const CacheVie
     pdl_done();
 }
 
+constexpr int kCompactList = 4096;   // moves whose lists fit shared memory
+
 // Compact, first part: how many pages are live, where the live pages above
-// that many go, and the new reference counts.
+// that many go, and the new reference counts.  One block: two ordered scans
+// over the counts, which a thread keeps in registers between them (up to
+// 16384 pages), and lists that stay in shared memory while the moves are
+// written out.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CacheView c, int *refs_out, int *n_live, void *ws) {
     __shared__ int wsum[32];
+    __shared__ int small_holes[kCompactList], small_strays[kCompactList];
     pdl_wait();
     int *totals = static_cast<int *>(ws), *holes = totals + 16, *strays = holes + c.pages, *map = strays + c.pages;
     constexpr long long step = static_cast<long long>(kPlanThreads) * kScan;
-    int live = 0;
+    const bool once = c.pages <= step;
+    int r[kScan], live = 0;
     for (long long c0 = 0; c0 < c.pages; c0 += step) {
-        int r[kScan], nf = 0, total;
+        int n = 0, total;
         const long long base = c0 + static_cast<long long>(threadIdx.x) * kScan;
         load_refs(c.ref_counts, c.pages, base, r);
 #pragma unroll
-        for (int q = 0; q < kScan; ++q) nf += r[q] > 0 && base + q < c.pages ? 1 : 0;
-        block_scan(nf, wsum, total);
+        for (int q = 0; q < kScan; ++q) n += r[q] > 0 && base + q < c.pages ? 1 : 0;
+        block_scan(n, wsum, total);
         live += total;
     }
+    // as many holes below as live pages above, and no more than either side has
+    const bool small = min(live, c.pages - live) <= kCompactList;
+    int *hl = small ? small_holes : holes, *sl = small ? small_strays : strays;
     int nh = 0, ns = 0;
     for (long long c0 = 0; c0 < c.pages; c0 += step) {
-        int r[kScan], h = 0, s = 0, total;
         const long long base = c0 + static_cast<long long>(threadIdx.x) * kScan;
-        load_refs(c.ref_counts, c.pages, base, r);
+        if (!once) load_refs(c.ref_counts, c.pages, base, r);
+        int both = 0, total;   // holes in the upper half, strays in the lower
 #pragma unroll
         for (int q = 0; q < kScan; ++q) {
-            const bool in = base + q < c.pages, used = r[q] > 0;
-            h += in && !used && base + q < live ? 1 : 0;
-            s += in && used && base + q >= live ? 1 : 0;
+            const bool in = base + q < c.pages, used = r[q] > 0, low = base + q < live;
+            both += (in && !used && low ? 1 << 16 : 0) + (in && used && !low ? 1 : 0);
         }
-        int ah = nh + block_scan(h, wsum, total);
-        nh += total;
-        int as = ns + block_scan(s, wsum, total);
-        ns += total;
+        const int before = block_scan(both, wsum, total);
+        int ah = nh + (before >> 16), as = ns + (before & 0xffff);
+        nh += total >> 16;
+        ns += total & 0xffff;
 #pragma unroll
         for (int q = 0; q < kScan; ++q) {
-            const long long id = base + q;
-            if (id >= c.pages) continue;
-            if (r[q] <= 0 && id < live) holes[ah++] = static_cast<int>(id);
-            if (r[q] <= 0 && id >= live) map[id] = -1;
-            if (r[q] > 0 && id >= live) {
-                map[id] = as;   // its rank for now
-                strays[as++] = static_cast<int>(id);
-            }
+            const int id = static_cast<int>(base) + q;
+            if (base + q >= c.pages) continue;
+            const bool used = r[q] > 0, low = base + q < live;
+            if (!used && low) hl[ah++] = id;
+            if (!used && !low) map[id] = -1;
+            if (used && !low) sl[as++] = id;
+            if (refs_out != c.ref_counts) refs_out[id] = used && low ? r[q] : 0;
         }
     }
     __syncthreads();
-    // as many holes below as live pages above
-    for (int k = threadIdx.x; k < ns; k += kPlanThreads) map[strays[k]] = holes[k];
-    // counts: what stays, then what moves (its old place is read before it is cleared)
-    if (refs_out != c.ref_counts)
-        for (int id = threadIdx.x; id < c.pages; id += kPlanThreads) refs_out[id] = id < live ? max(c.ref_counts[id], 0) : 0;
-    __syncthreads();
     for (int k = threadIdx.x; k < ns; k += kPlanThreads) {
-        const int r = c.ref_counts[strays[k]];
-        refs_out[holes[k]] = r;
-        if (refs_out == c.ref_counts) refs_out[strays[k]] = 0;
+        const int from = sl[k], to = hl[k], n = c.ref_counts[from];
+        map[from] = to;
+        refs_out[to] = n;
+        if (refs_out == c.ref_counts) refs_out[from] = 0;
+        if (small) {
+            strays[k] = from;
+            holes[k] = to;
+        }
     }
     if (threadIdx.x == 0) {
         totals[0] = ns;
@@ -447,6 +454,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const CacheV
     }
     pdl_done();
 }
+static_assert(kPlanThreads * kScan < (1 << 16), "two counts to a scan");
 
 // Compact, second part: the table and the pages.
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const CacheView c, int *table_out, const void *ws,
