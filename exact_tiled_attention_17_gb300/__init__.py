@@ -525,15 +525,15 @@ def attn_cache_workspace_size(pages: int, n: int) -> int:
     return int(lib.attn_cache_workspace_size(pages, n))
 
 
-def _granted(granted, cache, n):
+def _granted(granted, cache, n, like):
     if granted is None:
-        return torch.empty(n, dtype=torch.int32, device=cache.device)
+        return torch.empty_like(like)   # (the list: int32 [n], contiguous)
     _paged_list(granted, cache, "granted", n)
     return granted
 
 
-def _reserve(cache, st, a, b, n, granted, workspace):
-    g = _granted(granted, cache, n)
+def _reserve(cache, st, seqs, a, b, n, granted, workspace):
+    g = _granted(granted, cache, n, seqs)
     ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
     _check(_lib_reserve(cache._p, a, b, n, g.data_ptr(), ws[2], ws[1], st), "attn_cache_reserve")
     return g
@@ -546,9 +546,9 @@ def attn_cache_reserve(cache, seqs, n_new, granted=None, workspace=None, stream=
     n = seqs.shape[0]
     a, b = _paged_list(seqs, cache, "seqs"), _paged_list(n_new, cache, "n_new", n)
     if _paged_here(cache, stream):
-        return _reserve(cache, _raw_stream(cache._index), a, b, n, granted, workspace)
+        return _reserve(cache, _raw_stream(cache._index), seqs, a, b, n, granted, workspace)
     with _paged_scope(cache, stream) as st:
-        return _reserve(cache, st, a, b, n, granted, workspace)
+        return _reserve(cache, st, seqs, a, b, n, granted, workspace)
 
 
 def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
@@ -564,8 +564,8 @@ def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
     _check(rc, "attn_cache_free")
 
 
-def _fork(cache, st, a, b, n, copy, granted, workspace):
-    g = _granted(granted, cache, n)
+def _fork(cache, st, parents, a, b, n, copy, granted, workspace):
+    g = _granted(granted, cache, n, parents)
     ws = _paged_workspace(workspace, attn_cache_workspace_size(cache.pages, n), cache, st)
     _check(_lib_fork(cache._p, a, b, n, copy, g.data_ptr(), ws[2], ws[1], st), "attn_cache_fork")
     return g
@@ -578,9 +578,9 @@ def attn_cache_fork(cache, parents, children, copy: bool = False, granted=None, 
     n = parents.shape[0]
     a, b = _paged_list(parents, cache, "parents"), _paged_list(children, cache, "children", n)
     if _paged_here(cache, stream):
-        return _fork(cache, _raw_stream(cache._index), a, b, n, 1 if copy else 0, granted, workspace)
+        return _fork(cache, _raw_stream(cache._index), parents, a, b, n, 1 if copy else 0, granted, workspace)
     with _paged_scope(cache, stream) as st:
-        return _fork(cache, st, a, b, n, 1 if copy else 0, granted, workspace)
+        return _fork(cache, st, parents, a, b, n, 1 if copy else 0, granted, workspace)
 
 
 def _compact(cache, st, inplace, workspace):
@@ -640,7 +640,7 @@ def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) ->
 def _paged_fwd(cache, st, q, layer, shape, a, b, n, max_q, causal, scale, o, l, want_lse, workspace):
     T, Hq, d = shape
     if o is None:
-        o = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=cache.dtype, device=cache.device)
     if l is None and want_lse:
         l = torch.empty((T, Hq), dtype=torch.float32, device=cache.device)
     # (arguments the library rejects give a size of 0 here; it then says which)

@@ -565,6 +565,9 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
     const int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
     if (n < 0 || T < 0 || layer < 0 || layer >= w.layers) return kErrArg;
+    // (the stride of a dimension of one element means nothing)
+    if (T == 1) token_stride = 0;
+    if (w.heads == 1) head_stride = 0;
     const long long per = 16 / (cache->dtype == ATTN_BF16 ? 2 : 4);
     if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
     if (n == 0 || T == 0) return kOk;
@@ -594,6 +597,9 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     if (static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
     const int bf16 = cache->dtype == ATTN_BF16;
     const long long per = bf16 ? 8 : 4;
+    // (the stride of a dimension of one element means nothing)
+    if (T == 1) q_token_stride = o_token_stride = 0;
+    if (Hq == 1) q_head_stride = o_head_stride = 0;
     for (long long s : {q_token_stride, q_head_stride, o_token_stride, o_head_stride})
         if (s < 0 || s % per) return kErrArg;
     // the tensor maps of the bf16 path take strides below 2^40 bytes, and rows of Q that differ

@@ -6,7 +6,7 @@
  * device memory: tensors and workspaces are owned by the caller.  Work is
  * enqueued on the caller's stream (a cudaStream_t passed as void*; NULL means
  * the legacy default stream) on the current device.  The tensor-core forward,
- * the backward and the decode kernels are programmatic dependent launches:
+ * the backward, the decode and the paged-cache kernels are programmatic dependent launches:
  * each may be scheduled while the kernel before it in the stream finishes,
  * but reads or writes no global memory until that grid has completed, so
  * stream order holds as for an ordinary launch.

@@ -158,6 +158,21 @@ def test_strides(eta, dtype, new):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_dimensions_of_one(eta, dtype):
+    """One token, one head: whatever strides torch gives these dimensions."""
+    cache = build(eta, [21], 1, 16, 64, dtype)
+    wide = queries(3, 5, 64, dtype)
+    q = wide.as_strided((1, 1, 64), (3, 7, 1))
+    o, lse = eta.attn_paged_fwd(q, cache, 0, None, ints([0, 1]))
+    torch.cuda.synchronize()
+    check_attention(q, cache, 0, None, ints([0, 1]), True, 0.125, o, lse)
+    eta.attn_cache_append(cache, 0, q, q, None, ints([0, 1]))
+    torch.cuda.synchronize()
+    assert torch.equal(cache.k[0, int(cache.page_table[0, 1]), 0, 4], q[0, 0])
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("new", [1, 70])
 def test_offsets_past_32_bits(eta, dtype, new):
     """Pages further apart than 2^31 elements."""

@@ -91,6 +91,9 @@ def test_paged_fwd_rejection(lib):  # noqa: F811
         assert paged(lib, c, scale=s) == -1
     assert paged(lib, c, qt=516) == -1 and paged(lib, c, qh=-64) == -1
     assert paged(lib, c, oh=32) == -1 and paged(lib, c, ot=64, oh=64) == -1      # rows of O overlap
+    one = ctypes.byref(cache(heads=1))
+    assert paged(lib, one, Hq=1, qh=3, oh=5, qt=64, ot=64, T=0) == 0            # strides of a dimension of one: ignored
+    assert paged(lib, c, T=0, qt=4) == -1
     assert paged(lib, c, ws=None) == -3 and paged(lib, c, ws_bytes=need - 1) == -3 and paged(lib, c, ws=vp(264)) == -3
     assert paged(lib, c, T=0, max_q=0) == 0 and paged(lib, c, n=0) == 0          # nothing to do
 
