@@ -125,6 +125,23 @@ def test_long_and_split(eta, dtype, n, new):
     attend(eta, cache, [new], 2, seed=n, size=4.0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 7, 40])
+def test_one_unit_over_all_ctas(eta, dtype, new):
+    """More parts to a row than the merge kernel reads at once (one kv head, a long context)."""
+    cache = build(eta, [70001], 1, 64, 64, dtype, seed=new)
+    attend(eta, cache, [new], 4, seed=new)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
+def test_many_short_chunks(eta, dtype, d):
+    """Several list entries to a lane of the planning warp, in the kernels for many rows."""
+    lens = [(11 * i) % 150 for i in range(230)]
+    new = [(5 * i) % 23 for i in range(230)]
+    cache = build(eta, lens, 2, 16, d, dtype, seed=6)
+    attend(eta, cache, new, 3, seqs=[(i * 7) % 230 for i in range(230)], before=2, behind=3)
+
+
 def test_many_sequences(eta):
     """More list entries than a block has threads."""
     lens = [(7 * i) % 90 for i in range(1300)]
