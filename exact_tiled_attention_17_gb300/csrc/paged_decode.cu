@@ -17,8 +17,11 @@
 //   warps 0 .. 3   consumers.  S = Q K^T: warp w takes a quarter of the keys.
 //                  One vote a tile whether some row's maximum exceeds its
 //                  reference by 2^8; only then do the warps exchange maxima and
-//                  rescale.  P goes through shared memory as bf16, and warp w
-//                  forms O += P V for its quarter of the columns.
+//                  rescale.  P goes through shared memory as bf16 (units of
+//                  16 rows: as two bf16 parts, p and what rounding left over,
+//                  so that O is as exact as its own rounding; under the stream
+//                  the second product costs 0.3 us at most), and warp w forms
+//                  O += P V for its quarter of the columns.
 // Two barriers a tile among the four warps; with two CTAs on an SM one's
 // arithmetic covers the other's.
 //
@@ -49,9 +52,10 @@ struct PdShape {
     static constexpr int NS = 3;                                    // stages: 96 KB in flight to a CTA
     static constexpr int Q_BYTES = ROWS * DP * 2;
     static constexpr int P_BYTES = ROWS * KEYS * 2;                 // [KEYS / 64][ROWS][128 bytes]
+    static constexpr int PS = MT == 1 ? 2 : 1;                      // bf16 parts of a p
     static constexpr int OFF_Q = NS * STAGE;
     static constexpr int OFF_P = OFF_Q + QB * Q_BYTES;
-    static constexpr int OFF_MX = OFF_P + P_BYTES;                  // [4][ROWS] maxima
+    static constexpr int OFF_MX = OFF_P + PS * P_BYTES;                  // [4][ROWS] maxima
     static constexpr int OFF_L = OFF_MX + 4 * ROWS * 4;             // [4][ROWS] sums
     static constexpr int OFF_BAR = OFF_L + 4 * ROWS * 4;
     // a unit's words and its Q arrive on one barrier; QEMPTY: both have been read
@@ -354,10 +358,13 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                             const float p0 = ex2(s[mt][n][2 * i] - mu), p1 = ex2(s[mt][n][2 * i + 1] - mu);
                             l[mt][i] += p0 + p1;
                             const int chunk = warp * NK + n;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(sP + (chunk >> 3) * (ROWS * 128) + r * 128 +
-                                                                          (((chunk & 7) ^ (r & 7)) << 4) + col2 * 2),
-                                         "r"(pack_bf16x2(p0, p1))
-                                         : "memory");
+                            const uint32_t at = sP + (chunk >> 3) * (ROWS * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4) + col2 * 2;
+                            const uint32_t hi = pack_bf16x2(p0, p1);
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(hi) : "memory");
+                            if constexpr (S::PS == 2) {
+                                const uint32_t lo = pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
+                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + S::P_BYTES), "r"(lo) : "memory");
+                            }
                         }
                     }
                 named_bar_sync(1, 128);
@@ -384,11 +391,20 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                     for (int mt = 0; mt < MT; ++mt) {
                         uint32_t a[4];
                         const int r = mt * 16 + a_row;
-                        ldsm4(sP + (ks >> 2) * (ROWS * 128) + r * 128 + ((((ks & 3) * 2 + a_chunk) ^ (r & 7)) << 4), a);
+                        const uint32_t at = sP + (ks >> 2) * (ROWS * 128) + r * 128 + ((((ks & 3) * 2 + a_chunk) ^ (r & 7)) << 4);
+                        ldsm4(at, a);
 #pragma unroll
                         for (int n2 = 0; n2 < NT / 2; ++n2) {
                             mma16816(o[mt][2 * n2], a, vf[n2][0], vf[n2][1]);
                             mma16816(o[mt][2 * n2 + 1], a, vf[n2][2], vf[n2][3]);
+                        }
+                        if constexpr (S::PS == 2) {
+                            ldsm4(at + S::P_BYTES, a);
+#pragma unroll
+                            for (int n2 = 0; n2 < NT / 2; ++n2) {
+                                mma16816(o[mt][2 * n2], a, vf[n2][0], vf[n2][1]);
+                                mma16816(o[mt][2 * n2 + 1], a, vf[n2][2], vf[n2][3]);
+                            }
                         }
                     }
                 }

@@ -368,7 +368,8 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
  * page of the pool counts as page_size keys that no row sees.
  *
  * bf16: scores, softmax and sums in float32, probabilities rounded to bf16
- * for the product with V; d in {32, 64, 96, 128}.  float32: IEEE float32
+ * for the product with V (to two bf16 parts where an entry has at most 16
+ * rows of Q per kv head); d in {32, 64, 96, 128}.  float32: IEEE float32
  * throughout.  workspace: at least attn_paged_workspace_size(Hq, heads,
  * max_q, d, dtype) bytes, 16-byte aligned.  Asynchronous: two launches.
  */
