@@ -90,8 +90,9 @@ int launch_decode(const void *Q, const void *K, const void *V, void *O, float *L
 
 // Attention of new tokens over a paged cache (paged_*.cu); the parameters are
 // in paged.cuh.
-constexpr int kPagedMaxCtas = 640;    // CTAs a launch may use (sizes the workspace)
-constexpr int kPagedMaxTcCtas = 160;  // the tensor-core path: one per SM
+constexpr int kPagedMaxTcCtas = 160;       // CTAs a launch may use (sizes the workspace): one per SM,
+constexpr int kPagedMaxDecodeCtas = 320;   // two,
+constexpr int kPagedMaxSimtCtas = 640;     // up to four
 struct PagedParams;
 size_t paged_workspace_bytes(int g, int max_q, int d, int bf16);
 int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant);

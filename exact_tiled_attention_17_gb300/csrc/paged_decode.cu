@@ -8,7 +8,7 @@
 // the CUDA cores would not keep up (g * 2 FMAs to each element read), so both
 // products run on mma.sync with the rows padded to 16: at 16 rows that is
 // 16 * 4 FLOPs to a key's column, a small part of what the instruction can do.
-// tcgen05 would need 128-row tiles, of which these rows fill an eighth or less.
+// tcgen05 would need 128-row tiles, of which these rows fill a quarter at most.
 //
 //   warp 4         finds the CTA's work; TMA producer: gathers tiles of 64 keys
 //                  (128 at d <= 64: the same bytes), page by page, into a ring
@@ -28,6 +28,10 @@
 // Missing pages and pages past the end read as zeros (an out-of-range page
 // coordinate); masked scores are replaced by -inf, and V fragments of slots
 // past the end, which may hold NaN, are cleared in registers.
+//
+// Measured: 64 sequences of 2048 .. 8191 tokens, 8 kv heads of 128, 4 query heads
+// to each: 1.41 GB in 217 us, 0.97 of the measured copy rate.  4 sequences of 300
+// .. 1000: 13 us, of which 3 are launches and the rest a chain of dependent reads.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -483,7 +487,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
             cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, 160, S::SMEM_BYTES) != cudaSuccess)
             return kErrCuda;
-        grid = std::min(nsm * std::max(per, 1), kPagedMaxCtas);
+        grid = std::min(nsm * std::max(per, 1), kPagedMaxDecodeCtas);
         grids[dev].store(grid, std::memory_order_release);
     }
     const PagedGeom &gm = p.gm;
@@ -503,8 +507,8 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
 }  // namespace
 
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.gm.max_q) * p.gm.g;
-    if (rows <= 16) return p.d <= 64 ? launch_one<64, 1>(p, workspace, stream) : launch_one<128, 1>(p, workspace, stream);
+    if (paged_decode_rows(p.gm.g, p.gm.max_q) == 16)
+        return p.d <= 64 ? launch_one<64, 1>(p, workspace, stream) : launch_one<128, 1>(p, workspace, stream);
     return p.d <= 64 ? launch_one<64, 2>(p, workspace, stream) : launch_one<128, 2>(p, workspace, stream);
 }
 

@@ -315,8 +315,11 @@ Path path_of(int g, int max_q, int bf16) {
 }  // namespace
 
 size_t paged_workspace_bytes(int g, int max_q, int d, int bf16) {
-    if (path_of(g, max_q, bf16) == Path::kTc) return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
-    return paged_partial_bytes(kPagedMaxCtas, 64, d);
+    switch (path_of(g, max_q, bf16)) {
+        case Path::kTc: return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
+        case Path::kDecode: return paged_partial_bytes(kPagedMaxDecodeCtas, paged_decode_rows(g, max_q), d);
+        default: return paged_partial_bytes(kPagedMaxSimtCtas, paged_simt_rows(g, max_q, d), d);
+    }
 }
 
 int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant) {

@@ -308,7 +308,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
         cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kSimtThreads, S::SMEM) != cudaSuccess)
         return kErrCuda;
-    const int ctas = std::min(std::max(per_sm, 1) * std::max(nsm, 1), kPagedMaxCtas);
+    const int ctas = std::min(std::max(per_sm, 1) * std::max(nsm, 1), kPagedMaxSimtCtas);
     p.gm.tpu = RT / p.gm.g;
     p.gm.tk = kSimtKeys;
     p.gm.unit_cost = kSimtKeys;
@@ -323,20 +323,18 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
 }  // namespace
 
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream) {
-    // Units of 16 rows where an entry's rows fit; else of 32 at d > 64, where two
-    // CTAs then fit an SM, and of 64 below (and where a group alone has more than 32).
-    const bool few = static_cast<long long>(p.gm.max_q) * p.gm.g <= 16, mid = p.gm.g <= 32;
+    const int rows = paged_simt_rows(p.gm.g, p.gm.max_q, p.d);
     switch (p.d) {
-        case 32: return few ? launch_one<1, 16>(p, workspace, stream) : launch_one<1, 64>(p, workspace, stream);
-        case 64: return few ? launch_one<2, 16>(p, workspace, stream) : launch_one<2, 64>(p, workspace, stream);
+        case 32: return rows == 16 ? launch_one<1, 16>(p, workspace, stream) : launch_one<1, 64>(p, workspace, stream);
+        case 64: return rows == 16 ? launch_one<2, 16>(p, workspace, stream) : launch_one<2, 64>(p, workspace, stream);
         case 96:
-            return few   ? launch_one<3, 16>(p, workspace, stream)
-                   : mid ? launch_one<3, 32>(p, workspace, stream)
-                         : launch_one<3, 64>(p, workspace, stream);
+            return rows == 16   ? launch_one<3, 16>(p, workspace, stream)
+                   : rows == 32 ? launch_one<3, 32>(p, workspace, stream)
+                                : launch_one<3, 64>(p, workspace, stream);
         case 128:
-            return few   ? launch_one<4, 16>(p, workspace, stream)
-                   : mid ? launch_one<4, 32>(p, workspace, stream)
-                         : launch_one<4, 64>(p, workspace, stream);
+            return rows == 16   ? launch_one<4, 16>(p, workspace, stream)
+                   : rows == 32 ? launch_one<4, 32>(p, workspace, stream)
+                                : launch_one<4, 64>(p, workspace, stream);
         default: return kErrUnsupported;
     }
 }

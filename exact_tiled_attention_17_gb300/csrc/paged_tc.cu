@@ -28,6 +28,12 @@
 // the last page may hold anything: the producer waits for that V tile itself
 // and zeroes them before it hands the tile on (a masked p = 0 times NaN would
 // be NaN); masked scores are replaced, never added to.
+//
+// Bound by the softmax and the products together (tensor pipe 60 % active): a
+// step of 128 keys for both query tiles takes 1.5 us at d = 128, a unit about 5
+// us more.  Measured: four chunks of 511 .. 1024 tokens over 4000 .. 8192 cached
+// ones, 32 query heads of 128 on 8 kv heads: 346 GFLOP in 255 us, 1.36 PFLOP/s; 128
+// tokens over 130907, 16 query heads of 64 on 4: 92 us.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
