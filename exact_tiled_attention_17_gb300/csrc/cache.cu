@@ -26,25 +26,26 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 __device__ __forceinline__ void pdl_done() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Exclusive prefix of v over the block's threads, and the total.
-__device__ __forceinline__ int block_scan(int v, int *wsum, int &total) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *wsum, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int inc = v;
+    T inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, inc, o);
+        const T t = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += t;
     }
     __syncthreads();
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int w = wsum[lane];   // 32 warps
+    T w = wsum[lane];   // 32 warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, w, o);
+        const T t = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += t;
     }
     total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
+    const T before = warp == 0 ? T(0) : __shfl_sync(0xffffffffu, w, warp - 1);
     return before + inc - v;
 }
 
@@ -126,8 +127,9 @@ constexpr int kSmallList = 2048;   // free pages kept in shared memory
 // thread to an entry.
 struct PlanShared {
     int wsum[32];
+    long long wneed[32];
     int named[kPlanThreads];    // the list's rows of these entries
-    int end[kPlanThreads];      // needs up to and with an entry (of these entries)
+    int end[kPlanThreads];      // needs up to and with an entry (of these entries), or pages + 1 if that is less
     int list[kSmallList];
     int handed;
 };
@@ -148,9 +150,11 @@ __device__ __forceinline__ bool named_before(const PlanShared &sh, const int *li
 // `handed` how many, and sh.end says whose they are.
 __device__ __forceinline__ bool grant(const CacheView &c, PlanShared &sh, int need, int *big_list, bool &full, int *&list,
                                       int &handed) {
-    int total;
-    const int before = block_scan(max(need, 0), sh.wsum, total);
-    const int end = before + max(need, 0);
+    // (together the needs may pass 32 bits; more than there are pages is never met)
+    const long long most = static_cast<long long>(c.pages) + 1;
+    long long sum;
+    const long long before = block_scan(static_cast<long long>(max(need, 0)), sh.wneed, sum);
+    const int end = static_cast<int>(min(before + max(need, 0), most)), total = static_cast<int>(min(sum, most));
     sh.end[threadIdx.x] = end;
     if (threadIdx.x == 0) sh.handed = 0;
     list = total <= kSmallList ? sh.list : big_list;
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kFreeThreads) free_kernel(const CacheView c, c
     if (bad) {
         if (threadIdx.x == 0) atomicOr(err, kErrWordBadRow);
     } else {
-        const int len = c.seq_lens[s];
+        const int len = min(c.seq_lens[s], c.max_pages * c.page_size);
         const int left = max(0, min(keep ? keep[i] : 0, len));
         int *row = c.page_table + static_cast<long long>(s) * c.max_pages;
         for (int k = pages_of(left, c.page_size) + threadIdx.x; k < c.max_pages; k += kFreeThreads) {

@@ -476,6 +476,29 @@ def test_long_lists(eta):
     ref.check(cache)
 
 
+def test_needs_past_32_bits(eta):
+    """Entries that together ask for more pages than 32 bits count, in rows that could hold them."""
+    cols = 1 << 26
+    cache = eta.PagedCache.empty(1, 5000, 1, 16, 32, 70, cols)
+    seqs = list(range(69, 1, -1))
+    add = [40] + [16 * cols] * (len(seqs) - 3) + [0, 5]
+    granted = eta.attn_cache_reserve(cache, ints(seqs), ints(add)).tolist()
+    assert granted == [1] + [0] * (len(seqs) - 3) + [1, 0]
+    assert cache.seq_lens.tolist() == [0] * 69 + [40]
+    assert cache.ref_counts.nonzero().flatten().tolist() == [0, 1, 2] and int(cache.ref_counts.sum()) == 3
+    assert cache.page_table[69, :5].tolist() == [0, 1, 2, -1, -1]
+    assert int((cache.page_table >= 0).sum()) == 3
+    # a length at the row's end, and past it: cut to what the row can hold
+    cache.seq_lens[5] = 16 * cols
+    cache.seq_lens[6] = (1 << 31) - 1
+    cache.page_table[5, cols - 1] = 7
+    cache.ref_counts[7] = 1
+    eta.attn_cache_free(cache, ints([5, 6]), ints([16 * cols - 1, (1 << 31) - 1]))
+    assert cache.seq_lens[5:7].tolist() == [16 * cols - 1, 16 * cols]
+    assert cache.ref_counts[7] == 1 and cache.page_table[5, cols - 1] == 7
+    assert eta.attn_status() == eta.ATTN_OK
+
+
 def test_refused_entries(eta):
     """Sequences named twice, out of range, too long for their row; children that hold tokens."""
     cache = new_cache(eta, 12, 16, 6, 4)
