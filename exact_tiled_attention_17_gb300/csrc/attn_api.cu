@@ -107,62 +107,17 @@ bool make_bf16_rows_map(CUtensorMap *m, const void *base, int D, int N, int BH, 
     return true;
 }
 
-namespace {
-// Maps encoded before, by everything that goes into one: a map depends on
-// nothing else, so a hit is as good as a new one.  Direct-mapped.
-struct MapKey {
-    const void *base;
-    long long dev_rank;
-    cuuint64_t dims[5], strides[4];
-    cuuint32_t box[6];   // (one spare word: no padding to compare)
-};
-struct AnyMapEntry {
-    MapKey key;
-    CUtensorMap map;
-    bool used;
-};
-constexpr unsigned kAnyMaps = 1024;
-AnyMapEntry g_any_maps[kAnyMaps];
-std::mutex g_any_maps_mu;
-}  // namespace
-
 bool make_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box) {
-    int dev = 0;
-    if (rank < 1 || rank > 5 || cudaGetDevice(&dev) != cudaSuccess) return false;
-    MapKey k;
-    memset(&k, 0, sizeof(k));
-    k.base = base;
-    k.dev_rank = 8LL * dev + rank;
-    for (int i = 0; i < rank; ++i) {
-        k.dims[i] = dims[i];
-        k.box[i] = box[i];
-        // a dimension of one element may come with any stride: give it a valid one
-        if (i > 0) k.strides[i - 1] = dims[i] > 1 ? strides[i - 1] : 16 * ((dims[0] * 2 + 15) / 16);
-    }
-    uint64_t h = 1469598103934665603ull;
-    const uint64_t *words = reinterpret_cast<const uint64_t *>(&k);
-    for (size_t i = 0; i < sizeof(k) / 8; ++i) h = (h ^ words[i]) * 1099511628211ull;
-    AnyMapEntry &e = g_any_maps[(h >> 32) % kAnyMaps];
-    {
-        std::lock_guard<std::mutex> lk(g_any_maps_mu);
-        if (e.used && memcmp(&e.key, &k, sizeof(k)) == 0) {
-            *m = e.map;
-            return true;
-        }
-    }
     EncodeTiledFn enc = encode_tiled_fn();
-    if (!enc) return false;
+    if (rank < 1 || rank > 5 || !enc) return false;
+    cuuint64_t st[4] = {};
+    // a dimension of one element may come with any stride: give it a valid one
+    for (int i = 1; i < rank; ++i) st[i - 1] = dims[i] > 1 ? strides[i - 1] : 16 * ((dims[0] * 2 + 15) / 16);
     const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-    if (enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), k.dims, k.strides,
-            k.box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
-    std::lock_guard<std::mutex> lk(g_any_maps_mu);
-    e.key = k;
-    e.map = *m;
-    e.used = true;
-    return true;
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, st, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int *device_error_word() {
@@ -441,6 +396,13 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
 }
 
 namespace {
+constexpr long long kMaxTokens = 1LL << 30;   // of a sequence, and of a call
+
+// Whether `outer` >= (n - 1) * inner + block, without overflow.
+bool steps_over(long long outer, long long n, long long inner, long long block) {
+    return outer >= block && (n <= 1 || (outer - block) / (n - 1) >= inner);
+}
+
 // Checks a cache descriptor; fills the page kernels' view of it.
 int check_cache(const attn_cache_t *c, CacheView &w) {
     if (!c || !c->K || !c->V || !c->page_table || !c->seq_lens || !c->ref_counts) return kErrArg;
@@ -450,7 +412,8 @@ int check_cache(const attn_cache_t *c, CacheView &w) {
         return kErrArg;
     if (c->d > 128 || c->d % 32 != 0) return kErrUnsupported;
     if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return kErrUnsupported;
-    if (static_cast<long long>(c->max_pages) * c->page_size >= (1LL << 31)) return kErrArg;
+    // (positions, and the ends of tiles that reach past them, stay inside 32 bits)
+    if (static_cast<long long>(c->max_pages) * c->page_size > kMaxTokens) return kErrArg;
     if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->ref_counts)) return kErrArg;
     if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u)) return kErrArg;
     const long long per = 16 / (c->dtype == ATTN_BF16 ? 2 : 4);   // elements of a 16-byte piece
@@ -466,11 +429,9 @@ int check_cache(const attn_cache_t *c, CacheView &w) {
     const bool many_l = c->layers > 1, many_p = c->pages > 1;
     if (many_p && c->page_stride < block) return kErrArg;
     if (many_l && c->layer_stride < block) return kErrArg;
-    if (many_l && many_p) {
-        const bool pages_in = c->layer_stride >= (c->pages - 1) * c->page_stride + block;
-        const bool layers_in = c->page_stride >= (c->layers - 1) * c->layer_stride + block;
-        if (!pages_in && !layers_in) return kErrArg;
-    }
+    if (many_l && many_p && !steps_over(c->layer_stride, c->pages, c->page_stride, block) &&
+        !steps_over(c->page_stride, c->layers, c->layer_stride, block))
+        return kErrArg;
     w.k = static_cast<uint4 *>(c->K);
     w.v = static_cast<uint4 *>(c->V);
     w.page_table = c->page_table;
@@ -564,7 +525,7 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
     CacheView w;
     const int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (n < 0 || T < 0 || layer < 0 || layer >= w.layers) return kErrArg;
+    if (n < 0 || T < 0 || T > kMaxTokens || layer < 0 || layer >= w.layers) return kErrArg;
     // (the stride of a dimension of one element means nothing)
     if (T == 1) token_stride = 0;
     if (w.heads == 1) head_stride = 0;
@@ -594,7 +555,7 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     if (Hq / w.heads > 64) return kErrUnsupported;
     if (!(scale > 0.f) || !std::isfinite(scale)) return kErrArg;
     if (causal != 0 && causal != 1) return kErrArg;
-    if (static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
+    if (T > kMaxTokens || static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
     const int bf16 = cache->dtype == ATTN_BF16;
     const long long per = bf16 ? 8 : 4;
     // (the stride of a dimension of one element means nothing)
@@ -609,9 +570,9 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     if (T == 0 || n == 0) return kOk;
     if (max_q <= 0 || max_q > T) return kErrArg;
     // rows of O must not overlap: one of the strides steps over all of the other's range
-    const long long ht = o_head_stride, tt = o_token_stride;
-    const bool heads_in = (Hq == 1 || ht >= cache->d) && (T == 1 || tt >= (Hq - 1) * ht + cache->d);
-    const bool tokens_in = (T == 1 || tt >= cache->d) && (Hq == 1 || ht >= (T - 1) * tt + cache->d);
+    const long long ht = o_head_stride, tt = o_token_stride, d = cache->d;
+    const bool heads_in = (Hq == 1 || ht >= d) && (T == 1 || steps_over(tt, Hq, ht, d));
+    const bool tokens_in = (T == 1 || tt >= d) && (Hq == 1 || steps_over(ht, T, tt, d));
     if (!heads_in && !tokens_in) return kErrArg;
     if (!Q || !O || !q_start || !aligned16(Q) || !aligned16(O) || !aligned4(q_start) || !aligned4(seqs) || !aligned4(LSE))
         return kErrArg;

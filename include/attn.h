@@ -261,7 +261,8 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  *   dtype        ATTN_BF16 or ATTN_F32;  d in {32, 64, 96, 128};
  *   page_size    tokens to a page: 16, 32, 64, 128 or 256.
  *   page_table   [seqs][max_pages] int: the page of tokens page_size * k ..
- *                of each sequence, -1 where it has none.
+ *                of each sequence, -1 where it has none; max_pages *
+ *                page_size at most 2^30 tokens.
  *   seq_lens     [seqs] int: tokens of each sequence, those reserved included.
  *   ref_counts   [pages] int, 16-byte aligned: table entries that name each
  *                page; 0 = free.
@@ -269,9 +270,9 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  * past a sequence's length may hold anything, NaN included; what lies before
  * it must be finite.
  *
- * Lists (seqs, n_new, parents, ...) are int arrays in device memory.  Every
- * decision is taken on the device: no call waits for the host, and all can
- * be captured into a graph.  An index that is out of range (a sequence, a
+ * Lists (seqs, n_new, parents, ...) are int arrays in device memory that
+ * overlap nothing a call writes.  Every decision is taken on the device: no
+ * call waits for the host, and all can be captured into a graph.  An index that is out of range (a sequence, a
  * page named in the table, a token range) is never followed: that entry is
  * left out, and the next attn_status() returns ATTN_ERR_ARG.  So is a sequence
  * that a list names again, where the operator would change it twice (the
@@ -342,9 +343,9 @@ int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_
  * q_start[i] .. q_start[i+1] - 1 of Knew / Vnew; they are the sequence's last
  * tokens, so the room was reserved before.  Element (token t, head h, column
  * c) of Knew and Vnew lies at t * token_stride + h * head_stride + c (bases
- * 16-byte aligned, strides multiples of 16 bytes), T tokens in all; tokens
- * outside q_start[0] .. q_start[n] - 1 are not read.  q_start: [n + 1], not
- * decreasing.  Asynchronous.
+ * 16-byte aligned, strides multiples of 16 bytes), T tokens in all (at most
+ * 2^30); tokens outside q_start[0] .. q_start[n] - 1 go nowhere.  q_start: [n +
+ * 1], not decreasing.  Asynchronous.
  */
 int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
                       long long head_stride, int T, const int *seqs, const int *q_start, int n, void *stream);
@@ -361,7 +362,8 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
  *
  * Q, O: T rows; element (token t, head j, column c) at t * token_stride +
  * j * head_stride + c, of the cache's dtype (bases 16-byte aligned, strides
- * multiples of 16 bytes).  LSE: [T][Hq] float32 natural log, or NULL.  Rows
+ * positive multiples of 16 bytes; rows of O do not overlap, nor O and Q).  At
+ * most 2^30 tokens, and T * Hq below 2^31.  LSE: [T][Hq] float32 natural log, or NULL.  Rows
  * outside q_start[0] .. q_start[n] - 1 are left as they were.  A row that
  * sees no key gives O = 0, LSE = -inf.  max_q: at least the largest n_i (T
  * always is); an entry with more is left out.  A table entry that names no

@@ -44,7 +44,26 @@ BAD_CACHES = [
     (dict(layer_stride=4 * 16 * 64 * 9), -1),                 # layers overlap
     (dict(layer_stride=4 * 16 * 64, page_stride=4 * 16 * 64), -1),
     (dict(page_stride=-4 * 16 * 64), -1),
+    (dict(max_pages=(1 << 26) + 1), -1),                      # more than 2^30 tokens
+    (dict(pages=(1 << 31) - 1, page_stride=1 << 40, layer_stride=1 << 41), -1),   # layers overlap, past 64 bits
 ]
+
+
+def test_the_longest_sequence_a_cache_may_hold(lib):  # noqa: F811
+    assert paged(lib, ctypes.byref(cache(max_pages=1 << 26)), T=0) == 0
+    assert paged(lib, ctypes.byref(cache(max_pages=1 << 22, page_size=256)), T=0) == 0
+
+
+def test_the_most_tokens_of_a_call(lib):  # noqa: F811
+    one, most = ctypes.byref(cache(heads=1)), 1 << 30
+    kw = dict(Hq=1, qt=64, ot=64, n=0)
+    assert paged(lib, one, T=most, **kw) == 0 and paged(lib, one, T=most + 1, **kw) == -1
+    a = lib.attn_cache_append
+    assert a(one, ci(0), vp(256), vp(256), ll(64), ll(64), ci(most), None, vp(256), ci(0), None) == 0
+    assert a(one, ci(0), vp(256), vp(256), ll(64), ll(64), ci(most + 1), None, vp(256), ci(1), None) == -1
+    # rows of O that do not overlap only where 64 bits overflow
+    wide = ctypes.byref(cache())
+    assert paged(lib, wide, T=(1 << 27) + 1, max_q=1, Hq=8, oh=1 << 36, ot=1 << 37) == -1
 
 
 @pytest.mark.parametrize("bad,code", BAD_CACHES)
