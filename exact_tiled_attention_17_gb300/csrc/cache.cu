@@ -49,12 +49,14 @@ __device__ __forceinline__ T block_scan(T v, T *wsum, T &total) {
     return before + inc - v;
 }
 
-// Whether an earlier entry of the list names the same row (the first wins).
-// Whole warp; every lane gets the answer.
-__device__ __forceinline__ bool named_before(const int *list, int i, int row) {
+// Whether an earlier entry of the list names the same row (the first wins), of
+// those that `counts` lets count.  Whole warp; every lane gets the answer.
+template <typename Counts>
+__device__ __forceinline__ bool named_before(const int *list, int i, int row, const Counts &counts) {
     const int lane = threadIdx.x & 31;
     for (int j0 = 0; j0 < i; j0 += 32) {
-        const bool same = j0 + lane < i && list[j0 + lane] == row;
+        const int j = j0 + lane;
+        const bool same = j < i && list[j] == row && counts(j);
         if (__any_sync(0xffffffffu, same)) return true;
     }
     return false;
@@ -128,17 +130,18 @@ constexpr int kSmallList = 2048;   // free pages kept in shared memory
 struct PlanShared {
     int wsum[32];
     long long wneed[32];
-    int named[kPlanThreads];    // the list's rows of these entries
+    int named[kPlanThreads];    // the list's rows of these entries (-1: one that changes nothing)
     int end[kPlanThreads];      // needs up to and with an entry (of these entries), or pages + 1 if that is less
     int list[kSmallList];
     int handed;
 };
 
-// Whether an earlier entry of the list names the same row (the first wins).
-// Entries from c0 on are in sh.named.
-__device__ __forceinline__ bool named_before(const PlanShared &sh, const int *list, int c0, int row) {
+// Whether an earlier entry of the list names the same row (the first wins), of
+// those that `counts` lets count.  Entries from c0 on are in sh.named.
+template <typename Counts>
+__device__ __forceinline__ bool named_before(const PlanShared &sh, const int *list, int c0, int row, const Counts &counts) {
     bool same = false;
-    for (int j = 0; j < c0; ++j) same |= list[j] == row;
+    for (int j = 0; j < c0; ++j) same |= list[j] == row && counts(j);
     for (int j = 0; j < static_cast<int>(threadIdx.x); ++j) same |= sh.named[j] == row;
     return same;
 }
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const CacheView c
         const int i = c0 + tid;
         __syncthreads();   // the entries before are done with
         const int s = i < n ? seqs[i] : -1, add = i < n ? n_new[i] : 0;
-        sh.named[tid] = s;
+        sh.named[tid] = add > 0 ? s : -1;
         __syncthreads();
         int need = -1, len = 0;
         bool bad = false;
@@ -198,11 +201,18 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const CacheView c
             bad = s < 0 || s >= c.rows || add < 0;
             if (!bad) {
                 len = c.seq_lens[s];
-                bad = len < 0 || named_before(sh, seqs, c0, s);
+                bad = len < 0 || (add > 0 && named_before(sh, seqs, c0, s, [&](int j) { return n_new[j] > 0; }));
+            }
+            if (!bad && static_cast<long long>(len) + add <= static_cast<long long>(c.max_pages) * S) {
+                need = pages_of(len + add, S) - pages_of(len, S);
+                if (add > 0 && (len & (S - 1)) != 0) {
+                    // the new tokens begin inside the last page: it must be this sequence's own
+                    const int id = c.page_table[static_cast<long long>(s) * c.max_pages + len / S];
+                    bad = id < 0 || id >= c.pages || c.ref_counts[id] > 1;
+                    if (bad) need = -1;
+                }
             }
             if (bad) atomicOr(err, kErrWordBadRow);
-            else if (static_cast<long long>(len) + add <= static_cast<long long>(c.max_pages) * S)
-                need = pages_of(len + add, S) - pages_of(len, S);
         }
         have[tid] = pages_of(len, S);
         int *list, handed;
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const CacheView c
         }
         if (i < n) {
             granted[i] = ok ? 1 : 0;
-            if (ok) c.seq_lens[s] = len + add;
+            if (ok && add > 0) c.seq_lens[s] = len + add;
         }
     }
     pdl_done();
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kFreeThreads) free_kernel(const CacheView c, c
     const int s = seqs[i];
     __shared__ int bad;
     if (threadIdx.x < 32) {
-        const bool no = s < 0 || s >= c.rows || named_before(seqs, i, s);
+        const bool no = s < 0 || s >= c.rows || named_before(seqs, i, s, [](int) { return true; });
         if (threadIdx.x == 0) bad = no;
     }
     __syncthreads();
@@ -272,7 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const CacheView
         if (i < n) {
             if (a >= 0 && a < c.rows && b >= 0 && b < c.rows) {
                 len = c.seq_lens[a];
-                if (c.seq_lens[b] == 0 && len >= 0 && len <= cap && !named_before(sh, children, c0, b))
+                if (c.seq_lens[b] == 0 && len >= 0 && len <= cap && !named_before(sh, children, c0, b, [](int) { return true; }))
                     need = copy ? pages_of(len, S) : (len % S ? 1 : 0);
             }
             if (need < 0) atomicOr(err, kErrWordBadRow);
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
         if (i >= 0 && t < q_start[n]) {
             const int q0 = q_start[i], q1 = q_start[i + 1];
             const int s = seqs ? seqs[i] : i;
-            bad = !(q0 <= t && t < q1 && s >= 0 && s < c.rows) || (seqs && named_before(seqs, i, s));
+            bad = !(q0 <= t && t < q1 && s >= 0 && s < c.rows) || (seqs && named_before(seqs, i, s, [&](int j) { return q_start[j + 1] > q_start[j]; }));
             if (!bad) {
                 const int pos = c.seq_lens[s] - (q1 - q0) + (t - q0);
                 bad = pos < 0 || pos / S >= c.max_pages;

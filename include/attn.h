@@ -276,7 +276,9 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  * page named in the table, a token range) is never followed: that entry is
  * left out, and the next attn_status() returns ATTN_ERR_ARG.  So is a sequence
  * that a list names again, where the operator would change it twice (the
- * first mention counts).  n = 0 is allowed and does nothing.
+ * first mention counts; an entry of attn_cache_reserve or _append without
+ * tokens is none, so that a list may be padded with such).  n = 0 is allowed
+ * and does nothing.
  *
  * Calls on one cache are ordered by the caller (one stream, or events).  A
  * workspace belongs to one call until that call's work has run: calls that
@@ -299,7 +301,10 @@ size_t attn_cache_workspace_size(int pages, int n);
  * order) and its length grows by n_new[i].  Entries are granted in list order
  * as long as the free pages last; one that needs more pages than are left, or
  * than its table row has, gets nothing and keeps its length (so do later ones
- * that need pages).  granted: [n] int, written: 1 or 0.  Asynchronous.
+ * that need pages).  Nor does one whose next token would go into a page that
+ * other sequences name too (a fork cut back into a page that it shares), and
+ * attn_status then returns ATTN_ERR_ARG: a fork of that sequence has a copy of
+ * the page and can grow.  granted: [n] int, written: 1 or 0.  Asynchronous.
  */
 int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_new, int n, int *granted,
                        void *workspace, size_t ws_bytes, void *stream);

@@ -105,6 +105,7 @@ class Pages:
         self.lens = cache.seq_lens.tolist()
         self.refs = cache.ref_counts.tolist()
         self.copies = []   # (src, dst, slots) of the last call
+        self.shared = False   # whether a sequence was refused to grow into a shared page
 
     def _free(self):
         return [p for p in range(self.n_pages) if self.refs[p] <= 0]
@@ -112,9 +113,14 @@ class Pages:
     def reserve(self, seqs, n_new):
         free, at, total, out, seen = self._free(), 0, 0, [], set()
         for s, add in zip(seqs, n_new):
-            ok = 0 <= s < len(self.lens) and add >= 0 and s not in seen
-            seen.add(s)
+            ok = 0 <= s < len(self.lens) and add >= 0 and not (add and s in seen)
+            if add > 0:
+                seen.add(s)
             if not ok or self.lens[s] + add > self.cols * self.S:
+                out.append(0)
+                continue
+            if add and self.lens[s] % self.S and self.refs[self.table[s][self.lens[s] // self.S]] > 1:
+                self.shared = True
                 out.append(0)
                 continue
             have, want = -(-self.lens[s] // self.S), -(-(self.lens[s] + add) // self.S)

@@ -430,6 +430,33 @@ def test_pages_against_plain_integers(eta, seed):
         ref.check(cache)
         ref.consistent()
         check_copies(cache, before, ref.copies)
+    assert eta.attn_status() == (eta.ATTN_ERR_ARG if ref.shared else eta.ATTN_OK)
+
+
+def test_growing_into_a_shared_page(eta):
+    """A fork that is cut back into a full page, which its parent reads too: neither grows into it."""
+    cache = new_cache(eta, 12, 16, 5, 4)
+    ref = Pages(cache)
+    assert eta.attn_cache_reserve(cache, ints([0]), ints([32])).tolist() == ref.reserve([0], [32]) == [1]
+    assert eta.attn_cache_fork(cache, ints([0, 0]), ints([1, 2])).tolist() == ref.fork([0, 0], [1, 2], False) == [1, 1]
+    eta.attn_cache_free(cache, ints([1, 2]), ints([20, 16]))
+    ref.free([1, 2], [20, 16])
+    assert eta.attn_status() == eta.ATTN_OK
+    # sequence 1's next token would go into page 1; sequence 2's starts a page, sequence 0's too
+    assert eta.attn_cache_reserve(cache, ints([1, 2, 0]), ints([1, 5, 1])).tolist() == ref.reserve([1, 2, 0], [1, 5, 1]) == [0, 1, 1]
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    ref.check(cache)
+    # a fork of it has a copy
+    before = (cache.k.clone(), cache.v.clone())
+    assert eta.attn_cache_fork(cache, ints([1]), ints([3])).tolist() == ref.fork([1], [3], False) == [1]
+    check_copies(cache, before, ref.copies)
+    assert eta.attn_cache_reserve(cache, ints([3]), ints([6])).tolist() == ref.reserve([3], [6]) == [1]
+    # and once the others have left, the page is its own
+    eta.attn_cache_free(cache, ints([0]))
+    ref.free([0])
+    assert eta.attn_cache_reserve(cache, ints([1]), ints([6])).tolist() == ref.reserve([1], [6]) == [1]
+    ref.check(cache)
+    ref.consistent()
     assert eta.attn_status() == eta.ATTN_OK
 
 
@@ -555,6 +582,29 @@ def test_append(eta, dtype, layout, d, heads):
     assert eta.attn_status() == eta.ATTN_OK
     assert torch.equal(cache.k.nan_to_num(9.0), want[0].nan_to_num(9.0))
     assert torch.equal(cache.v.nan_to_num(9.0), want[1].nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("pad", [2, 1500])
+def test_padded_lists(eta, pad):
+    """Entries without tokens before and behind the others, of the same sequences."""
+    cache = new_cache(eta, 40, 16, 6, 4)
+    ref = Pages(cache)
+    front, back = [i % 3 for i in range(pad)], [2] * pad
+    seqs, add = front + [0, 1, 2] + back, [0] * pad + [20, 5, 33] + [0] * pad
+    for _ in range(2):
+        add[pad + 2] -= 10
+        assert eta.attn_cache_reserve(cache, ints(seqs), ints(add)).tolist() == ref.reserve(seqs, add) == [1] * len(seqs)
+        ref.check(cache)
+    kn = queries(7, cache.heads, cache.d, cache.dtype)
+    want, table = cache.k.clone(), cache.page_table.tolist()
+    for i, (s, n) in enumerate([(0, 2), (1, 4), (2, 1)]):
+        for t in range(n):
+            at = ref.lens[s] - n + t
+            want[0, table[s][at // 16], :, at % 16] = kn[[0, 2, 6][i] + t]
+    qs = [0] * (pad + 1) + [2, 6] + [7] * (pad + 1)
+    eta.attn_cache_append(cache, 0, kn, kn, ints(seqs), ints(qs))
+    assert eta.attn_status() == eta.ATTN_OK
+    assert torch.equal(cache.k.nan_to_num(9.0), want.nan_to_num(9.0))
 
 
 def test_append_bad_places(eta):
