@@ -321,7 +321,8 @@ int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep,
  * a copy of sequence parents[i] as it was before the call.  copy = 0: it
  * shares the parent's full pages, and a partly filled last page is copied to
  * a free page, so that both can grow.  copy = 1: every page is copied.
- * Copies are taken in every layer, of the slots that hold tokens.  Pages are
+ * Copies are taken in every layer, of the slots that hold tokens (so append a
+ * sequence's reserved tokens before it is forked).  Pages are
  * handed out as by attn_cache_reserve; granted: [n] int, written.  A child
  * that is not empty is refused (granted 0, and attn_status reports
  * ATTN_ERR_ARG).  Asynchronous.
