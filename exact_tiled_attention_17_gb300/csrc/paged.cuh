@@ -230,15 +230,16 @@ __device__ __forceinline__ PagedHdr paged_read_header(const PagedParams &p, int 
 int launch_paged_merge(const PagedParams &p, int bf16, int ctas, int sms, cudaStream_t stream);
 
 // Rows of a unit (sizes the workspace too).  The stream kernel: 16 or 32,
-// whichever holds an entry.  The CUDA-core kernel: 16 where an entry's rows
-// fit; else 32 at d > 64, where two CTAs then fit an SM, and 64 below (and where
-// a group alone has more than 32).
+// whichever holds an entry.  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
+// the one that tiles).
 inline int paged_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 16 ? 16 : 32; }
-inline int paged_simt_rows(int g, int max_q, int d) {
-    return static_cast<long long>(g) * max_q <= 16 ? 16 : d > 64 && g <= 32 ? 32 : 64;
+inline int paged_simt_rows(int g, int max_q) {
+    const long long rows = static_cast<long long>(g) * max_q;
+    return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 // The variants (each sets its own unit size, partial layout and grid).
+int launch_paged_few(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream);

@@ -307,9 +307,11 @@ bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUte
 namespace {
 // The kernel of a call.  bf16: the stream kernel takes units of up to 32 rows
 // (tokens of an entry x query heads of a group), the matrix kernel more.
-enum class Path { kSimt, kDecode, kTc };
+// float32: units of up to 8 rows are streamed through registers (32 x 8000 tokens,
+// d 128, 4 rows: 160 us, tiled 365; 16 rows, 16 x 4000: 161, tiled 106).
+enum class Path { kFew, kSimt, kDecode, kTc };
 Path path_of(int g, int max_q, int bf16) {
-    if (!bf16) return Path::kSimt;
+    if (!bf16) return paged_simt_rows(g, max_q) <= 8 ? Path::kFew : Path::kSimt;
     return static_cast<long long>(g) * max_q <= 32 ? Path::kDecode : Path::kTc;
 }
 }  // namespace
@@ -318,7 +320,7 @@ size_t paged_workspace_bytes(int g, int max_q, int d, int bf16) {
     switch (path_of(g, max_q, bf16)) {
         case Path::kTc: return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
         case Path::kDecode: return paged_partial_bytes(kPagedMaxDecodeCtas, paged_decode_rows(g, max_q), d);
-        default: return paged_partial_bytes(kPagedMaxSimtCtas, paged_simt_rows(g, max_q, d), d);
+        default: return paged_partial_bytes(kPagedMaxSimtCtas, paged_simt_rows(g, max_q), d);
     }
 }
 
@@ -330,6 +332,9 @@ int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t s
         case Path::kDecode:
             if (variant) *variant = p.d <= 64 ? "paged_decode_bf16_d64" : "paged_decode_bf16_d128";
             return launch_paged_decode(p, workspace, stream);
+        case Path::kFew:
+            if (variant) *variant = "paged_few_f32";
+            return launch_paged_few(p, workspace, stream);
         default:
             if (variant) *variant = "paged_simt_f32";
             return launch_paged_simt(p, workspace, stream);

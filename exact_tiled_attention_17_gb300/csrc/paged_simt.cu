@@ -5,17 +5,20 @@
 // of new tokens, all query heads of the group), key tile by key tile with the
 // running maximum m and sum l of the online softmax.
 //
-// A CTA of 128 threads walks its share of the units.  Q, a tile of 64 keys and
-// its values are staged in shared memory; S is a register tile of RT/8 rows x
-// 4 keys per thread, O one of RT/8 rows x d/16 columns.  What bounds it is
-// the multiply-add rate (1.07 GFLOP of the 200-token case below are 14 us), so
-// both products run on packed pairs (fma.rn.f32x2): S pairs up along d, O
-// along its rows, for which P lies key by key in shared memory.  Tiles are fetched with cp.async while the other
-// product runs: K of the next tile during softmax and P V, V during Q K^T.
-// Measured: 8.9 GFLOP (4 x 256 tokens over 2000, 16 heads of 64) in 246 us, the
-// multiply-add pipe busy 55 % of the time.  The two warps of a scheduler that fit
-// do not hide each other's latencies; a third CTA needs 168 registers, spills and
-// is slower (252 us), as are narrower register tiles (16 x 16 threads: 291 us).
+// A CTA of 128 threads walks its share of the units.  Q, a tile of keys and
+// its values are staged in shared memory; S and O are register tiles: 4 rows x
+// 8 (d > 64: 4) keys, and 4 rows x d / 8 columns, of a thread in units of 64 rows.
+// What bounds it is the multiply-add rate (1.07 GFLOP of the 200-token case below
+// are 14 us), so both products run on packed pairs (fma.rn.f32x2): S pairs up
+// along d, O along its rows, for which P lies key by key in shared memory.  Tiles
+// are fetched with cp.async while the other product runs: K of the next tile
+// during softmax and P V, V during Q K^T.
+// Measured (4 x 256 tokens over 2000, 16 query heads): d 64 208 us, d 128 380, 41
+// TFLOP/s; 3 x 77 .. 200 tokens over 700 .. 1500, 8 heads of 64: 47 us.  What is
+// left is latency: two or three warps of a scheduler fit, and what hides it best is
+// to unroll (both products by 16 steps: 208 us, by 4: 222).  16 threads along
+// the keys instead of 8 (8 x 4 register tiles): 205 us at d 64, but 393 at 128 and 156
+// for 125 at 32.
 // Keys of pages that do not exist, and keys a row does not see, have score
 // -inf; what is not a token of the sequence is fetched as zero.
 #include <algorithm>
@@ -27,18 +30,19 @@ namespace eta {
 namespace {
 
 constexpr int kSimtThreads = 128;
-constexpr int kSimtKeys = 64;
 
 template <int E, int RT>   // E = d / 32, RT: query rows of a unit
 struct SimtShape {
     static constexpr int D = 32 * E;
-    static constexpr int LD = D + 4;               // padded rows: 16 lanes reading 16 rows spread over the banks
+    static constexpr int KT = RT == 64 && D > 64 ? 32 : 64;   // keys of a tile: two CTAs fit an SM (d = 128: 456 us with
+                                                              // units of 32 rows and tiles of 64 keys instead, 376)
+    static constexpr int TX = RT == 16 ? 16 : 8, TY = 128 / TX;   // threads along keys and columns, along rows
+    static constexpr int LD = D + 4;               // padded rows: lanes reading different rows spread over the banks
     static constexpr int LP = RT + 4;              // P: [key][row]
-    static constexpr int RR = RT / 8;              // rows of a thread
-    static constexpr int NC = (D + 63) / 64;       // 4-column pieces of a thread
-    static constexpr int FLOATS = RT * LD + 2 * kSimtKeys * LD + kSimtKeys * LP;
-    static constexpr int SMEM = FLOATS * 4 + 2 * kSimtKeys * 8;
-    static constexpr int CTAS = RT < 64 && SMEM <= 74 * 1024 ? 3 : SMEM <= 112 * 1024 ? 2 : 1;   // at least, on an SM
+    static constexpr int RR = RT / TY, KB = KT / TX, NC = (D + 4 * TX - 1) / (4 * TX);   // rows, keys, 4-column pieces of a thread
+    static constexpr int FLOATS = RT * LD + 2 * KT * LD + KT * LP;
+    static constexpr int SMEM = FLOATS * 4 + 2 * KT * 8;
+    static constexpr int CTAS = (RT < 64 || KT < 64) && SMEM <= 74 * 1024 ? 3 : SMEM <= 112 * 1024 ? 2 : 1;   // at least, on an SM
 };
 
 // 16 bytes from global to shared memory; zeros if !in.
@@ -54,13 +58,14 @@ __device__ __forceinline__ ulonglong2 load2(const float *p) { return *reinterpre
 template <int E, int RT>
 __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_simt_kernel(const PagedParams p) {
     using S = SimtShape<E, RT>;
-    constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = S::RR, NC = S::NC;
+    constexpr int D = S::D, LD = S::LD, LP = S::LP, RR = S::RR, KT = S::KT, KB = S::KB, TX = S::TX, NC = S::NC;
     extern __shared__ __align__(16) float smem[];
     __shared__ PagedUnit unit;
-    float *qs = smem, *ks = qs + RT * LD, *vs = ks + kSimtKeys * LD, *ps = vs + kSimtKeys * LD;
-    long long *key_at = reinterpret_cast<long long *>(ps + kSimtKeys * LP);   // [2]: offset of each key's row, or -1
+    __shared__ int gaps[2][KT / 32];   // whether a tile has keys of missing pages
+    float *qs = smem, *ks = qs + RT * LD, *vs = ks + KT * LD, *ps = vs + KT * LD;
+    long long *key_at = reinterpret_cast<long long *>(ps + KT * LP);   // [2]: offset of each key's row, or -1
     const PagedGeom &gm = p.gm;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int tid = threadIdx.x, tx = tid % TX, ty = tid / TX;
     const int cta = blockIdx.x;
     paged_touch(p);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -81,24 +86,30 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
         const PagedUnit w = unit;
         if (w.tiles == 0) break;
         const int rows = w.ntok * gm.g, tok0 = w.tok0, t1 = w.tile0 + w.tiles;
+        const int vis_all = paged_unit_visible(gm, w, 0);   // what every row sees
         // where the keys of tile t lie
         auto places = [&](int t) {
-            if (tid < kSimtKeys && t < t1) {
-                const int key = t * kSimtKeys + tid;
+            if (tid < KT && t < t1) {
+                const int key = t * KT + tid;
                 long long at = -1;
+                bool gap = false;
                 if (key < w.len) {
                     const int id = paged_page(gm, w.seq, key >> gm.page_shift);
-                    if (id >= 0) at = id * p.page_stride + (key & (gm.page_size - 1)) * p.slot_stride + w.head * p.head_stride;
+                    gap = id < 0;
+                    if (!gap) at = id * p.page_stride + (key & (gm.page_size - 1)) * p.slot_stride + w.head * p.head_stride;
                     else atomicOr(p.err, kErrWordBadRow);
                 }
-                key_at[(t & 1) * kSimtKeys + tid] = at;
+                key_at[(t & 1) * KT + tid] = at;
+                const bool any = __any_sync(0xffffffffu, gap);
+                if ((tid & 31) == 0) gaps[t & 1][tid >> 5] = any;
             }
         };
         auto fetch = [&](float *dst, const float *src, int t) {
             if (t < t1) {
-                for (int i = tid; i < kSimtKeys * (D / 4); i += kSimtThreads) {
+#pragma unroll 4
+                for (int i = tid; i < KT * (D / 4); i += kSimtThreads) {
                     const int r = i / (D / 4), c = 4 * (i % (D / 4));
-                    const long long at = key_at[(t & 1) * kSimtKeys + r];
+                    const long long at = key_at[(t & 1) * KT + r];
                     copy16(dst + r * LD + c, at >= 0 ? src + at + c : src, at >= 0);
                 }
             }
@@ -135,67 +146,71 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[a][b][e] = 0ull;
         for (int t = w.tile0; t < t1; ++t) {
-            const int key0 = t * kSimtKeys;
+            const int key0 = t * KT;
             places(t + 1);
             copy_wait<1>();    // K has landed (V may be on its way)
             __syncthreads();
-            // S: rows ty * RR + a, keys tx + 16 b
-            float s[RR][4];
+            // S: rows ty * RR + a, keys tx + TX b
+            float s[RR][KB];
             {
-                uint64_t acc[RR][4];
+                uint64_t acc[RR][KB];
 #pragma unroll
                 for (int a = 0; a < RR; ++a)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) acc[a][b] = 0ull;
-#pragma unroll 4
+                    for (int b = 0; b < KB; ++b) acc[a][b] = 0ull;
+#pragma unroll 16
                 for (int c = 0; c < D; c += 4) {
-                    ulonglong2 kf[4];
+                    ulonglong2 kf[KB], qf[RR];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) kf[b] = load2(ks + (tx + 16 * b) * LD + c);
-                    // (no product next to one that it depends on)
-                    ulonglong2 qf[RR];
+                    for (int b = 0; b < KB; ++b) kf[b] = load2(ks + (tx + TX * b) * LD + c);
 #pragma unroll
                     for (int a = 0; a < RR; ++a) qf[a] = load2(qs + (ty * RR + a) * LD + c);
+                    // (no product next to one that it depends on)
 #pragma unroll
                     for (int a = 0; a < RR; ++a)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) acc[a][b] = f2_fma(qf[a].x, kf[b].x, acc[a][b]);
+                        for (int b = 0; b < KB; ++b) acc[a][b] = f2_fma(qf[a].x, kf[b].x, acc[a][b]);
 #pragma unroll
                     for (int a = 0; a < RR; ++a)
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) acc[a][b] = f2_fma(qf[a].y, kf[b].y, acc[a][b]);
+                        for (int b = 0; b < KB; ++b) acc[a][b] = f2_fma(qf[a].y, kf[b].y, acc[a][b]);
                 }
 #pragma unroll
                 for (int a = 0; a < RR; ++a)
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
+                    for (int b = 0; b < KB; ++b) {
                         float x, y;
                         f2_unpack(acc[a][b], x, y);
-                        s[a][b] = x + y;
+                        s[a][b] = (x + y) * p.scale_log2;
                     }
             }
-            bool here[4];
+            bool edge = key0 + KT > vis_all;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) here[b] = key_at[(t & 1) * kSimtKeys + tx + 16 * b] >= 0;
+            for (int i = 0; i < KT / 32; ++i) edge = edge || gaps[t & 1][i];
+            if (edge) {
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    const bool here = key_at[(t & 1) * KT + tx + TX * b] >= 0;
+#pragma unroll
+                    for (int a = 0; a < RR; ++a) s[a][b] = here && key0 + tx + TX * b < vis[a] ? s[a][b] : -INFINITY;
+                }
+            }
             __syncthreads();   // K has been read
             fetch(ks, K, t + 1);
             float alpha[RR];
 #pragma unroll
             for (int a = 0; a < RR; ++a) {
-                float mx = -INFINITY;
+                float mx = s[a][0];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    s[a][b] = here[b] && key0 + tx + 16 * b < vis[a] ? s[a][b] * p.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[a][b]);
-                }
+                for (int b = 1; b < KB; ++b) mx = fmaxf(mx, s[a][b]);
 #pragma unroll
-                for (int q = 1; q < 16; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
+                for (int q = 1; q < TX; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, q));
                 const float mn = fmaxf(m[a], mx), mu = mn == -INFINITY ? 0.f : mn;
                 const float al = m[a] == -INFINITY ? 0.f : ex2(m[a] - mu);
                 m[a] = mn;
                 float sum = 0.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
+                for (int b = 0; b < KB; ++b) {
                     s[a][b] = ex2(s[a][b] - mu);
                     sum += s[a][b];
                 }
@@ -203,8 +218,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                 alpha[a] = al;
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float *at = ps + (tx + 16 * b) * LP + ty * RR;
+            for (int b = 0; b < KB; ++b) {
+                float *at = ps + (tx + TX * b) * LP + ty * RR;
                 if constexpr (RR >= 4) {
 #pragma unroll
                     for (int a = 0; a < RR; a += 4)
@@ -224,9 +239,9 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
             }
             copy_wait<1>();    // V has landed (the next K may be on its way)
             __syncthreads();
-            // O: rows ty * RR + a, columns 4 tx + 64 b
-#pragma unroll 4
-            for (int k = 0; k < kSimtKeys; ++k) {
+            // O: rows ty * RR + a, columns 4 tx + 4 TX b
+#pragma unroll 16
+            for (int k = 0; k < KT; ++k) {
                 uint64_t pp[RR / 2];
                 if constexpr (RR >= 4) {
 #pragma unroll
@@ -240,9 +255,9 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                 }
 #pragma unroll
                 for (int b = 0; b < NC; ++b) {
-                    const int c = 4 * tx + 64 * b;
-                    const float4 v = (D % 64 == 0 || c < D) ? *reinterpret_cast<const float4 *>(vs + k * LD + c)
-                                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const int c = 4 * tx + 4 * TX * b;
+                    const float4 v = (D % (4 * TX) == 0 || c < D) ? *reinterpret_cast<const float4 *>(vs + k * LD + c)
+                                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
                     const uint64_t vv[4] = {f2_pack(v.x, v.x), f2_pack(v.y, v.y), f2_pack(v.z, v.z), f2_pack(v.w, v.w)};
 #pragma unroll
                     for (int a = 0; a < RR / 2; ++a)
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
         for (int a = 0; a < RR; ++a) {
             float sum = l[a];
 #pragma unroll
-            for (int q = 1; q < 16; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
+            for (int q = 1; q < TX; q <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, q);
             const int r = ty * RR + a;
             if (r >= rows) continue;
             const int tr = paged_token(gm, r);
@@ -273,8 +288,8 @@ __global__ void __launch_bounds__(kSimtThreads, SimtShape<E, RT>::CTAS) paged_si
                                : p.part_o + prow * D;
 #pragma unroll
             for (int b = 0; b < NC; ++b) {
-                const int c = 4 * tx + 64 * b;
-                if (c >= D) continue;
+                const int c = 4 * tx + 4 * TX * b;
+                if (D % (4 * TX) != 0 && c >= D) continue;
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -310,9 +325,9 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
         return kErrCuda;
     const int ctas = std::min(std::max(per_sm, 1) * std::max(nsm, 1), kPagedMaxSimtCtas);
     p.gm.tpu = RT / p.gm.g;
-    p.gm.tk = kSimtKeys;
-    p.gm.unit_cost = kSimtKeys;
-    p.gm.min_share = 2 * kSimtKeys;
+    p.gm.tk = S::KT;
+    p.gm.unit_cost = S::KT;
+    p.gm.min_share = 128;
     paged_derive(p.gm);
     paged_carve(p, workspace, ctas, RT);
     const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), kSimtThreads, S::SMEM, stream, p);
@@ -322,19 +337,21 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
 
 }  // namespace
 
+template <int E>
+static int launch_rows(PagedParams &p, void *workspace, cudaStream_t stream) {
+    switch (paged_simt_rows(p.gm.g, p.gm.max_q)) {
+        case 16: return launch_one<E, 16>(p, workspace, stream);
+        case 32: return launch_one<E, 32>(p, workspace, stream);
+        default: return launch_one<E, 64>(p, workspace, stream);
+    }
+}
+
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream) {
-    const int rows = paged_simt_rows(p.gm.g, p.gm.max_q, p.d);
     switch (p.d) {
-        case 32: return rows == 16 ? launch_one<1, 16>(p, workspace, stream) : launch_one<1, 64>(p, workspace, stream);
-        case 64: return rows == 16 ? launch_one<2, 16>(p, workspace, stream) : launch_one<2, 64>(p, workspace, stream);
-        case 96:
-            return rows == 16   ? launch_one<3, 16>(p, workspace, stream)
-                   : rows == 32 ? launch_one<3, 32>(p, workspace, stream)
-                                : launch_one<3, 64>(p, workspace, stream);
-        case 128:
-            return rows == 16   ? launch_one<4, 16>(p, workspace, stream)
-                   : rows == 32 ? launch_one<4, 32>(p, workspace, stream)
-                                : launch_one<4, 64>(p, workspace, stream);
+        case 32: return launch_rows<1>(p, workspace, stream);
+        case 64: return launch_rows<2>(p, workspace, stream);
+        case 96: return launch_rows<3>(p, workspace, stream);
+        case 128: return launch_rows<4>(p, workspace, stream);
         default: return kErrUnsupported;
     }
 }

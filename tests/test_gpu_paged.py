@@ -126,6 +126,18 @@ def test_long_and_split(eta, dtype, n, new):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("g,new", [(1, 1), (3, 1), (2, 2), (8, 1), (1, 7), (5, 2), (4, 4), (3, 9), (8, 4)])
+def test_few_rows(eta, dtype, d, g, new):
+    """Every size of the units for few rows: short lengths, ends inside a batch of keys, entries with less than the most tokens."""
+    lens = [1, 700, 2, 15, 33, 0, 64, 65, 5, 1291]
+    cache = build(eta, lens, 2, 16 if g < 4 else 128, d, dtype, ["head", "token"][g % 2], seed=d + g)
+    some = [min(n, 1 + (new * i) % (new + 1)) for i, n in enumerate(lens)]
+    some[1] = new
+    attend(eta, cache, some, g, causal=new != 2, before=1, behind=1, seed=g)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("new", [1, 7, 40])
 def test_one_unit_over_all_ctas(eta, dtype, new):
     """More parts to a row than the merge kernel reads at once (one kv head, a long context)."""
