@@ -590,13 +590,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
         if (i >= 0 && t < q_start[n]) {
             const int q0 = q_start[i], q1 = q_start[i + 1];
             const int s = seqs ? seqs[i] : i;
-            bad = !(q0 <= t && t < q1 && s >= 0 && s < c.rows) || (seqs && named_before(seqs, i, s, [&](int j) { return q_start[j + 1] > q_start[j]; }));
+            bad = !(q0 <= t && t < q1 && s >= 0 && s < c.rows);
             if (!bad) {
-                const int pos = c.seq_lens[s] - (q1 - q0) + (t - q0);
-                bad = pos < 0 || pos / S >= c.max_pages;
+                const int len = c.seq_lens[s];   // (on its way while the list is looked through)
+                const bool again = seqs && named_before(seqs, i, s, [&](int j) { return q_start[j + 1] > q_start[j]; });
+                const int pos = len - (q1 - q0) + (t - q0);
+                bad = again || pos < 0 || pos / S >= c.max_pages;
                 if (!bad) {
                     const int id = c.page_table[static_cast<long long>(s) * c.max_pages + pos / S];
-                    bad = id < 0 || id >= c.pages;
+                    // (a page that other table entries name too is read by those sequences: it is never written)
+                    bad = id < 0 || id >= c.pages || c.ref_counts[id] > 1;
                     if (!bad) at = layer * c.layer_vecs + id * c.page_vecs + (pos % S) * c.slot_stride_vecs;
                 }
             }
@@ -681,7 +684,7 @@ int launch_cache_append(const CacheView &c, int layer, const void *Kn, const voi
     int *err = device_error_word();
     if (!err) return kErrCuda;
     const uint4 *k = static_cast<const uint4 *>(Kn), *v = static_cast<const uint4 *>(Vn);
-    // up to 4096 tokens two to a CTA (131 tokens x 8 heads x 128: 3.4 us, 3.9 with
+    // up to 4096 tokens two to a CTA (131 tokens x 8 heads x 128: 3.2 us, 3.9 with
     // eight), more eight (8000: 10.2 us, 10.4 with two; 7000 tokens' 58 MB at 0.97 of the copy rate)
     if (T <= 4096)
         return launch(append_kernel<2>, static_cast<unsigned>((T + 1) / 2), kAppendThreads, stream, c, layer, k, v,

@@ -472,6 +472,38 @@ def test_growing_into_a_shared_page(eta):
     assert eta.attn_status() == eta.ATTN_OK
 
 
+@pytest.mark.parametrize("tokens", [1, 9, 5000])
+def test_append_leaves_shared_pages_alone(eta, tokens):
+    """Tokens appended although no room was granted for them: none goes into a page that another sequence reads."""
+    rows, page = max(2 * tokens, 32) // 16 * 16 + 16, 16
+    cache = new_cache(eta, 3 * rows // page, page, 4, 2 * rows // page)
+    assert eta.attn_cache_reserve(cache, ints([0]), ints([rows])).tolist() == [1]
+    assert eta.attn_cache_fork(cache, ints([0]), ints([1])).tolist() == [1]
+    eta.attn_cache_free(cache, ints([1]), ints([rows - 3]))      # cut back into a page that sequence 0 names too
+    kn, vn = queries(tokens, 2, 32, BF16, 1), queries(tokens, 2, 32, BF16, 2)
+    q = queries(1, 4, 32, BF16)
+    qs = ints([0, tokens])
+    o, lse = eta.attn_paged_fwd(q, cache, 0, ints([0]), ints([0, 1]))
+    held = (cache.k.clone(), cache.v.clone())
+    assert eta.attn_cache_reserve(cache, ints([1]), ints([tokens])).tolist() == [0]
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    for row in (0, 1):   # neither of the two may write what both read
+        for layer in range(2):
+            eta.attn_cache_append(cache, layer, kn, vn, ints([row]), qs)
+        assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert torch.equal(cache.k, held[0]) and torch.equal(cache.v, held[1])
+    o2, lse2 = eta.attn_paged_fwd(q, cache, 0, ints([0]), ints([0, 1]))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # what has room of its own is written all the same, beside a sequence that has none
+    assert eta.attn_cache_reserve(cache, ints([2]), ints([1])).tolist() == [1]
+    both = queries(tokens + 1, 2, 32, BF16, 3)
+    eta.attn_cache_append(cache, 1, both, both, ints([1, 2]), ints([0, tokens, tokens + 1]))
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    want = held[0].clone()
+    want[1, int(cache.page_table[2, 0]), :, 0] = both[tokens]
+    assert torch.equal(cache.k, want)
+
+
 @pytest.mark.parametrize("pages", [1, 16, 17, 16384, 16385, 70001])
 def test_pools_of_any_size(eta, pages):
     """The scan over the reference counts: its steps, its tail, a pool that is used up."""
