@@ -41,7 +41,8 @@ ATTN_ERR_DEVICE_TIMEOUT = -5
 EXPORTS = ("attn_fwd", "attn_fwd_host_workspace_size", "attn_fwd_host", "attn_fwd_block_sparse", "attn_naive_workspace_size", "attn_naive_fwd", "attn_deviation_workspace_size",
            "attn_deviation", "attn_deviation_noalloc", "attn_decode_workspace_size", "attn_decode_fwd",
            "attn_cache_workspace_size", "attn_cache_reserve", "attn_cache_free", "attn_cache_fork", "attn_cache_compact",
-           "attn_cache_append", "attn_paged_workspace_size", "attn_paged_fwd",
+           "attn_cache_append", "attn_cache_append_granted", "attn_paged_workspace_size", "attn_paged_fwd",
+           "attn_paged_fwd_granted",
            "attn_bwd_workspace_size", "attn_bwd", "attn_emul_fwd", "attn_emul_round", "attn_status",
            "attn_strerror", "attn_last_variant", "attn_debug_wait_timeout")
 DEVIATION_NOALLOC_MAX_N = 1 << 20
@@ -111,10 +112,14 @@ def _load() -> ctypes.CDLL:
     lib.attn_cache_compact.restype = i
     lib.attn_cache_append.argtypes = [cp, i, vp, vp, ll, ll, i, vp, vp, i, vp]
     lib.attn_cache_append.restype = i
+    lib.attn_cache_append_granted.argtypes = [cp, i, vp, vp, ll, ll, i, vp, vp, vp, i, vp]
+    lib.attn_cache_append_granted.restype = i
     lib.attn_paged_workspace_size.argtypes = [i, i, i, i, i]
     lib.attn_paged_workspace_size.restype = sz
     lib.attn_paged_fwd.argtypes = [cp, i, vp, vp, vp, ll, ll, ll, ll, i, i, vp, vp, i, i, i, f, vp, sz, vp]
     lib.attn_paged_fwd.restype = i
+    lib.attn_paged_fwd_granted.argtypes = [cp, i, vp, vp, vp, ll, ll, ll, ll, i, i, vp, vp, vp, i, i, i, f, vp, sz, vp]
+    lib.attn_paged_fwd_granted.restype = i
     lib.attn_bwd_workspace_size.argtypes = [i, i, i, i]
     lib.attn_bwd_workspace_size.restype = sz
     lib.attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp, vp, sz, vp]
@@ -475,6 +480,7 @@ def _paged_list(t, cache, name, n=None):
 
 _lib_reserve, _lib_free, _lib_fork = lib.attn_cache_reserve, lib.attn_cache_free, lib.attn_cache_fork
 _lib_compact, _lib_append, _lib_paged_fwd = lib.attn_cache_compact, lib.attn_cache_append, lib.attn_paged_fwd
+_lib_append_granted, _lib_paged_fwd_granted = lib.attn_cache_append_granted, lib.attn_paged_fwd_granted
 
 
 @contextlib.contextmanager
@@ -603,12 +609,20 @@ def attn_cache_compact(cache, inplace: bool = True, workspace=None, stream=None)
         return _compact(cache, st, inplace, workspace)
 
 
-def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None) -> None:
+def _append(cache, st, layer, k, v, strides, T, a, b, c, n):
+    if c is None:
+        return _lib_append(cache._p, layer, k, v, strides[0], strides[1], T, a, b, n, st)
+    return _lib_append_granted(cache._p, layer, k, v, strides[0], strides[1], T, a, b, c, n, st)
+
+
+def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None, granted=None) -> None:
     """Writes the keys and values of new tokens into one layer.  k_new, v_new:
     [T, heads, d] of the cache's dtype, any strides with a contiguous last
     dimension (one pair of strides for both).  Entry i: sequence seqs[i]
     (seqs None: sequence i), tokens q_start[i] .. q_start[i+1] - 1, the last
-    ones of the sequence (reserved before)."""
+    ones of the sequence (reserved before).  granted: what attn_cache_reserve
+    returned for these entries; those that got no room are left out (without
+    it they write over the sequence's last tokens)."""
     shape, strides = k_new.shape, k_new.stride()
     if (len(shape) != 3 or shape != v_new.shape or strides != v_new.stride() or shape[1] != cache.heads or
             shape[2] != cache.d or strides[2] != 1):
@@ -619,12 +633,13 @@ def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=Non
     n = q_start.shape[0] - 1
     a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
     b = _paged_list(q_start, cache, "q_start")
+    c = None if granted is None else _paged_list(granted, cache, "granted", n)
+    args = (layer, k_new.data_ptr(), v_new.data_ptr(), strides, shape[0], a, b, c, n)
     if _paged_here(cache, stream):
-        rc = _lib_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n,
-                         _raw_stream(cache._index))
+        rc = _append(cache, _raw_stream(cache._index), *args)
     else:
         with _paged_scope(cache, stream) as st:
-            rc = _lib_append(cache._p, layer, k_new.data_ptr(), v_new.data_ptr(), strides[0], strides[1], shape[0], a, b, n, st)
+            rc = _append(cache, st, *args)
     _check(rc, "attn_cache_append")
 
 
@@ -637,7 +652,7 @@ def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) ->
     return _paged_workspace_size(Hq, heads, max_q, d, _DTYPE[dtype] if not isinstance(dtype, int) else dtype)
 
 
-def _paged_fwd(cache, st, q, layer, shape, a, b, n, max_q, causal, scale, o, l, want_lse, workspace):
+def _paged_fwd(cache, st, q, layer, shape, a, b, c, n, max_q, causal, scale, o, l, want_lse, workspace):
     T, Hq, d = shape
     if o is None:
         o = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=cache.dtype, device=cache.device)
@@ -646,14 +661,17 @@ def _paged_fwd(cache, st, q, layer, shape, a, b, n, max_q, causal, scale, o, l, 
     # (arguments the library rejects give a size of 0 here; it then says which)
     ws = _paged_workspace(workspace, _paged_workspace_size(Hq, cache.heads, max(max_q, 1), d, cache._code), cache, st)
     qs, os_ = q.stride(), o.stride()
-    _check(_lib_paged_fwd(cache._p, layer, q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(), qs[0], qs[1],
-                              os_[0], os_[1], T, Hq, a, b, n, max_q, causal, scale, ws[2], ws[1], st),
-           "attn_paged_fwd")
+    ptrs = (q.data_ptr(), o.data_ptr(), None if l is None else l.data_ptr(), qs[0], qs[1], os_[0], os_[1], T, Hq, a, b)
+    rest = (n, max_q, causal, scale, ws[2], ws[1], st)
+    rc = (_lib_paged_fwd(cache._p, layer, *ptrs, *rest) if c is None else
+          _lib_paged_fwd_granted(cache._p, layer, *ptrs, c, *rest))
+    _check(rc, "attn_paged_fwd")
     return o, l
 
 
 def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None, causal: bool = True,
-                   scale: float | None = None, out=None, lse=None, workspace=None, stream=None, want_lse: bool = True):
+                   scale: float | None = None, out=None, lse=None, workspace=None, stream=None, want_lse: bool = True,
+                   granted=None):
     """Attention of new tokens over one layer of a paged cache.  q: [T, Hq, d]
     of the cache's dtype, any strides with a contiguous last dimension; Hq a
     multiple of the cache's heads (query head j reads kv head j // (Hq /
@@ -661,8 +679,9 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     tokens are rows q_start[i] .. q_start[i+1] - 1 of q; causal: token t of the
     entry's n sees keys j <= len - n + t.  max_q: at least the most new tokens
     of an entry (default T; a close bound lets short entries take the path for
-    few rows).  Returns (o, lse): o like q, lse [T, Hq] float32; rows outside
-    the list are left as they were."""
+    few rows).  granted: what attn_cache_reserve returned for these entries;
+    those that got no room are left out.  Returns (o, lse): o like q, lse [T,
+    Hq] float32; rows of no entry, or of one left out, are as they were."""
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.d or q.stride(2) != 1:
         raise ValueError("q must be [T, Hq, d] with a contiguous last dimension")
@@ -677,7 +696,8 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or
                             lse.get_device() != cache._index):
         raise ValueError("lse must be a contiguous float32 tensor [T, Hq] on q's device")
-    args = (q, layer, shape, a, b, n, shape[0] if max_q is None else int(max_q), 1 if causal else 0,
+    c = None if granted is None else _paged_list(granted, cache, "granted", n)
+    args = (q, layer, shape, a, b, c, n, shape[0] if max_q is None else int(max_q), 1 if causal else 0,
             cache._scale if scale is None else float(scale), out, lse, want_lse, workspace)
     if _paged_here(cache, stream):
         return _paged_fwd(cache, _raw_stream(cache._index), *args)

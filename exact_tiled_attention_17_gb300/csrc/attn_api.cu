@@ -522,6 +522,13 @@ int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_
 
 int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
                       long long head_stride, int T, const int *seqs, const int *q_start, int n, void *stream) {
+    return attn_cache_append_granted(cache, layer, Knew, Vnew, token_stride, head_stride, T, seqs, q_start, nullptr, n,
+                                     stream);
+}
+
+int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew,
+                              long long token_stride, long long head_stride, int T, const int *seqs, const int *q_start,
+                              const int *granted, int n, void *stream) {
     CacheView w;
     const int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
@@ -532,9 +539,10 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
     const long long per = 16 / (cache->dtype == ATTN_BF16 ? 2 : 4);
     if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
     if (n == 0 || T == 0) return kOk;
-    if (!Knew || !Vnew || !q_start || !aligned16(Knew) || !aligned16(Vnew) || !aligned4(q_start) || !aligned4(seqs))
+    if (!Knew || !Vnew || !q_start || !aligned16(Knew) || !aligned16(Vnew) || !aligned4(q_start) || !aligned4(seqs) ||
+        !aligned4(granted))
         return kErrArg;
-    return launch_cache_append(w, layer, Knew, Vnew, token_stride / per, head_stride / per, T, seqs, q_start, n,
+    return launch_cache_append(w, layer, Knew, Vnew, token_stride / per, head_stride / per, T, seqs, q_start, granted, n,
                                static_cast<cudaStream_t>(stream));
 }
 
@@ -548,6 +556,14 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
                    long long q_head_stride, long long o_token_stride, long long o_head_stride, int T, int Hq,
                    const int *seqs, const int *q_start, int n, int max_q, int causal, float scale, void *workspace,
                    size_t ws_bytes, void *stream) {
+    return attn_paged_fwd_granted(cache, layer, Q, O, LSE, q_token_stride, q_head_stride, o_token_stride, o_head_stride, T, Hq,
+                                  seqs, q_start, nullptr, n, max_q, causal, scale, workspace, ws_bytes, stream);
+}
+
+int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE,
+                           long long q_token_stride, long long q_head_stride, long long o_token_stride,
+                           long long o_head_stride, int T, int Hq, const int *seqs, const int *q_start, const int *granted,
+                           int n, int max_q, int causal, float scale, void *workspace, size_t ws_bytes, void *stream) {
     CacheView w;
     int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
@@ -574,7 +590,8 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     const bool heads_in = (Hq == 1 || ht >= d) && (T == 1 || steps_over(tt, Hq, ht, d));
     const bool tokens_in = (T == 1 || tt >= d) && (Hq == 1 || steps_over(ht, T, tt, d));
     if (!heads_in && !tokens_in) return kErrArg;
-    if (!Q || !O || !q_start || !aligned16(Q) || !aligned16(O) || !aligned4(q_start) || !aligned4(seqs) || !aligned4(LSE))
+    if (!Q || !O || !q_start || !aligned16(Q) || !aligned16(O) || !aligned4(q_start) || !aligned4(seqs) || !aligned4(LSE) ||
+        !aligned4(granted))
         return kErrArg;
     rc = check_workspace(workspace, ws_bytes, paged_workspace_bytes(Hq / w.heads, max_q, cache->d, bf16));
     if (rc != kOk) return rc;
@@ -586,6 +603,7 @@ int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O,
     p.gm.seq_lens = w.seq_lens;
     p.gm.seqs = seqs;
     p.gm.q_start = q_start;
+    p.gm.granted = granted;
     p.gm.n = n;
     p.gm.rows = w.rows;
     p.gm.max_pages = w.max_pages;

@@ -544,7 +544,8 @@ constexpr int kAppendThreads = 256;
 template <int TOK>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView c, int layer, const uint4 *Kn, const uint4 *Vn,
                                                                 long long token_vecs, long long head_vecs, int T,
-                                                                const int *seqs, const int *q_start, int n, int *err) {
+                                                                const int *seqs, const int *q_start, const int *granted, int n,
+                                                                int *err) {
     static_assert(TOK <= kAppendThreads / 32, "one warp finds one token's place");
     __shared__ long long dst[TOK];   // first 16-byte piece of the slot's head 0, or -1
     pdl_wait();
@@ -590,10 +591,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
         if (i >= 0 && t < q_start[n]) {
             const int q0 = q_start[i], q1 = q_start[i + 1];
             const int s = seqs ? seqs[i] : i;
-            bad = !(q0 <= t && t < q1 && s >= 0 && s < c.rows);
-            if (!bad) {
+            const bool here = !granted || granted[i] != 0;
+            bad = here && !(q0 <= t && t < q1 && s >= 0 && s < c.rows);
+            if (here && !bad) {
                 const int len = c.seq_lens[s];   // (on its way while the list is looked through)
-                const bool again = seqs && named_before(seqs, i, s, [&](int j) { return q_start[j + 1] > q_start[j]; });
+                const bool again = seqs && named_before(seqs, i, s, [&](int j) {
+                    return q_start[j + 1] > q_start[j] && (!granted || granted[j] != 0);
+                });
                 const int pos = len - (q1 - q0) + (t - q0);
                 bad = again || pos < 0 || pos / S >= c.max_pages;
                 if (!bad) {
@@ -680,7 +684,8 @@ int launch_cache_compact(const CacheView &c, int *table_out, int *refs_out, int 
 }
 
 int launch_cache_append(const CacheView &c, int layer, const void *Kn, const void *Vn, long long token_vecs,
-                        long long head_vecs, int T, const int *seqs, const int *q_start, int n, cudaStream_t stream) {
+                        long long head_vecs, int T, const int *seqs, const int *q_start, const int *granted, int n,
+                        cudaStream_t stream) {
     int *err = device_error_word();
     if (!err) return kErrCuda;
     const uint4 *k = static_cast<const uint4 *>(Kn), *v = static_cast<const uint4 *>(Vn);
@@ -688,9 +693,9 @@ int launch_cache_append(const CacheView &c, int layer, const void *Kn, const voi
     // eight), more eight (8000: 10.2 us, 10.4 with two; 7000 tokens' 58 MB at 0.97 of the copy rate)
     if (T <= 4096)
         return launch(append_kernel<2>, static_cast<unsigned>((T + 1) / 2), kAppendThreads, stream, c, layer, k, v,
-                      token_vecs, head_vecs, T, seqs, q_start, n, err);
+                      token_vecs, head_vecs, T, seqs, q_start, granted, n, err);
     return launch(append_kernel<8>, static_cast<unsigned>((T + 7) / 8), kAppendThreads, stream, c, layer, k, v,
-                  token_vecs, head_vecs, T, seqs, q_start, n, err);
+                  token_vecs, head_vecs, T, seqs, q_start, granted, n, err);
 }
 
 }  // namespace eta

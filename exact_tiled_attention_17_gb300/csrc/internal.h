@@ -115,7 +115,8 @@ int launch_cache_fork(const CacheView &c, const int *parents, const int *childre
                       cudaStream_t stream);
 int launch_cache_compact(const CacheView &c, int *table_out, int *refs_out, int *n_live, void *ws, cudaStream_t stream);
 int launch_cache_append(const CacheView &c, int layer, const void *Kn, const void *Vn, long long token_vecs,
-                        long long head_vecs, int T, const int *seqs, const int *q_start, int n, cudaStream_t stream);
+                        long long head_vecs, int T, const int *seqs, const int *q_start, const int *granted, int n,
+                        cudaStream_t stream);
 
 // FP32 backward on the CUDA cores (bwd_f32.cu); workspace: B*H*N floats.
 int launch_bwd_f32(const float *Q, const float *K, const float *V, const float *O, const float *dO, const float *LSE,

@@ -27,6 +27,7 @@ struct PagedGeom {
     const int *seq_lens;     // [rows]
     const int *seqs;         // [n] table rows of the list, or null: 0 .. n-1
     const int *q_start;      // [n + 1] first new token of each entry
+    const int *granted = nullptr;   // [n], or null: an entry with 0 takes no part
     int n, rows, max_pages, pages, page_size;
     int T, max_q;            // rows of Q; the most new tokens of an entry
     int heads, g;            // kv heads, query heads to each
@@ -56,7 +57,7 @@ ETA_HD long long paged_div(long long a, long long b) {
     return a / b;
 }
 
-// One entry of the list.  nq = 0: nothing to do (or a bad entry).
+// One entry of the list.  nq = 0: nothing to do (or a bad entry, or one that got no room).
 struct PagedEntry {
     int seq, q0, nq, len;
 };
@@ -71,6 +72,7 @@ ETA_HD bool paged_entry(const PagedGeom &gm, int i, PagedEntry &e) {
     e.q0 = 0;
     e.nq = 0;
     e.len = 0;
+    if (gm.granted && gm.granted[i] == 0) return true;   // (left out on purpose)
     if (seq < 0 || seq >= gm.rows || q0 < 0 || q1 < q0 || q1 > gm.T || q1 - q0 > gm.max_q) return false;
     const int cap = gm.max_pages * gm.page_size;
     const int len = gm.seq_lens[seq];

@@ -354,9 +354,18 @@ int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_
  * 1], not decreasing.  A token whose page other table entries name too (its
  * reserve was refused, or the sequence was forked in between) is not written,
  * and attn_status returns ATTN_ERR_ARG.  Asynchronous.
+ *
+ * attn_cache_append_granted — the same with the list that attn_cache_reserve
+ * wrote for the same entries (granted: [n] int, or NULL): one that got no room
+ * (0) is left out and not reported.  Without it, an entry that was refused
+ * writes over the sequence's last tokens: use this form wherever a reserve may
+ * be refused and the host does not look.
  */
 int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
                       long long head_stride, int T, const int *seqs, const int *q_start, int n, void *stream);
+int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew,
+                              long long token_stride, long long head_stride, int T, const int *seqs, const int *q_start,
+                              const int *granted, int n, void *stream);
 
 /*
  * attn_paged_fwd — attention of new tokens over one layer of a paged cache.
@@ -382,12 +391,20 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
  * rows of Q per kv head); d in {32, 64, 96, 128}.  float32: IEEE float32
  * throughout.  workspace: at least attn_paged_workspace_size(Hq, heads,
  * max_q, d, dtype) bytes, 16-byte aligned.  Asynchronous: two launches.
+ *
+ * attn_paged_fwd_granted — the same with the list that attn_cache_reserve
+ * wrote for the same entries (granted: [n] int, or NULL): one that got no room
+ * (0) is left out and not reported, its rows left as they were.
  */
 size_t attn_paged_workspace_size(int Hq, int heads, int max_q, int d, int dtype);
 int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE, long long q_token_stride,
                    long long q_head_stride, long long o_token_stride, long long o_head_stride, int T, int Hq,
                    const int *seqs, const int *q_start, int n, int max_q, int causal, float scale, void *workspace,
                    size_t ws_bytes, void *stream);
+int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE,
+                           long long q_token_stride, long long q_head_stride, long long o_token_stride,
+                           long long o_head_stride, int T, int Hq, const int *seqs, const int *q_start, const int *granted,
+                           int n, int max_q, int causal, float scale, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * attn_bwd — gradients of exact attention: for O = softmax(Q K^T * scale +

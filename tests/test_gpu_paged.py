@@ -7,7 +7,7 @@ import random
 import pytest
 import torch
 
-from paged_ref import Pages, check_attention
+from paged_ref import Pages, check_attention, gather
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
@@ -502,6 +502,90 @@ def test_append_leaves_shared_pages_alone(eta, tokens):
     want = held[0].clone()
     want[1, int(cache.page_table[2, 0]), :, 0] = both[tokens]
     assert torch.equal(cache.k, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 6, 40])
+def test_entries_without_room_are_left_out(eta, dtype, new):
+    """The pool runs out inside a list: what was refused keeps its tokens, and its rows stay as they were."""
+    lens, page, heads, g = [29, 64, 47, 16], 16, 2, 4
+    cache = build(eta, lens, heads, page, 64, dtype, spare=-(-new // page), max_pages=20)
+    ref = Pages(cache)
+    seqs, add = [1, 3, 0, 2, 2], [new] * 4 + [1]
+    T = sum(add)
+    room = eta.attn_cache_reserve(cache, ints(seqs), ints(add))
+    # (sequence 2's second mention does not count in any case)
+    assert room.tolist() == ref.reserve(seqs, add) and 0 < sum(room.tolist()) < 4
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    kn, vn = queries(T, heads, 64, dtype, 1), queries(T, heads, 64, dtype, 2)
+    qs = ints(starts(add))
+    want, table = [cache.k.clone(), cache.v.clone()], cache.page_table.tolist()
+    for i, s in enumerate(seqs):
+        for t in range(add[i] if room[i] else 0):
+            at = ref.lens[s] - add[i] + t
+            for pool, x in zip(want, (kn, vn)):
+                pool[0, table[s][at // page], :, at % page] = x[sum(add[:i]) + t]
+    eta.attn_cache_append(cache, 0, kn, vn, ints(seqs), qs, granted=room)
+    assert eta.attn_status() == eta.ATTN_OK
+    for pool, x in zip((cache.k, cache.v), want):
+        assert torch.equal(pool.nan_to_num(9.0), x.nan_to_num(9.0))
+    q = queries(T, heads * g, 64, dtype)
+    o, lse = torch.full_like(q, 7.0), torch.full((T, heads * g), 7.0, device="cuda")
+    eta.attn_paged_fwd(q, cache, 0, ints(seqs), qs, max_q=new, out=o, lse=lse, granted=room)
+    assert eta.attn_status() == eta.ATTN_OK
+    for i, s in enumerate(seqs):
+        a, b = sum(add[:i]), sum(add[:i + 1])
+        if room[i]:
+            check_attention(q[a:b], cache, 0, ints([s]), ints([0, b - a]), True, 0.125, o[a:b], lse[a:b])
+        else:
+            assert (o[a:b] == 7).all() and (lse[a:b] == 7).all()
+    # a refused mention is none: the sequence's next entry is its first
+    room2 = ints([0, 1])
+    eta.attn_cache_append(cache, 0, kn[:2], vn[:2], ints([1, 1]), ints([0, 1, 2]), granted=room2)
+    assert eta.attn_status() == eta.ATTN_OK
+    at = ref.lens[1] - 1
+    assert torch.equal(cache.k[0, table[1][at // page], :, at % page], kn[1])
+    with pytest.raises(ValueError):
+        eta.attn_cache_append(cache, 0, kn[:2], vn[:2], ints([1, 1]), ints([0, 1, 2]), granted=room)
+    with pytest.raises(ValueError):
+        eta.attn_paged_fwd(q, cache, 0, ints(seqs), qs, granted=room.float())
+
+
+def test_a_captured_step_outlives_its_pool(eta):
+    """Reserve, append and attention in one graph, replayed until the pages have run out and beyond."""
+    page, heads, g, d = 16, 2, 2, 64
+    cache = new_cache(eta, 9, page, 3, 8, layers=1, heads=heads, d=d)
+    assert eta.attn_cache_reserve(cache, ints([0, 1, 2]), ints([16, 30, 7])).tolist() == [1, 1, 1]
+    ref = Pages(cache)
+    seqs, add, qs = ints([2, 0, 1]), ints([3, 5, 2]), ints([0, 3, 8, 10])
+    kn, q = queries(10, heads, d, BF16, 1), queries(10, heads * g, d, BF16)
+    o, lse = torch.zeros_like(q), torch.zeros((10, heads * g), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        room = eta.attn_cache_reserve(cache, seqs, add)
+        eta.attn_cache_append(cache, 0, kn, kn, seqs, qs, granted=room)
+        eta.attn_paged_fwd(q, cache, 0, seqs, qs, max_q=5, out=o, lse=lse, granted=room)
+    held = {s: gather(cache, 0, s, ref.lens[s])[0] for s in range(3)}
+    refused = 0
+    for _ in range(25):
+        kn.normal_()
+        q.normal_()
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        assert room.tolist() == ref.reserve([2, 0, 1], [3, 5, 2])
+        refused += 3 - sum(room.tolist())
+        ref.check(cache)
+        for i, s in enumerate([2, 0, 1]):
+            a, b = [0, 3, 8, 10][i:i + 2]
+            if room[i]:
+                held[s] = torch.cat([held[s], kn[a:b].transpose(0, 1).cpu().double()], 1)
+                check_attention(q[a:b], cache, 0, ints([s]), ints([0, b - a]), True, d ** -0.5, o[a:b], lse[a:b])
+            else:
+                assert (o[a:b] == 7).all() and (lse[a:b] == 7).all()
+            assert torch.equal(gather(cache, 0, s, ref.lens[s])[0], held[s])
+    assert refused > 20 and eta.attn_status() == eta.ATTN_OK
 
 
 @pytest.mark.parametrize("pages", [1, 16, 17, 16384, 16385, 70001])

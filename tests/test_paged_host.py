@@ -333,6 +333,50 @@ def test_bad_entries_are_left_out(shim):
         assert shim.entry(ctypes.byref(a), i, out) == ok and list(out) == want, (seqs, qs)
 
 
+def test_granted_lists_are_checked_and_null_is_none(lib):  # noqa: F811
+    c = ctypes.byref(cache())
+    p = vp(256)
+    a, f = lib.attn_cache_append_granted, lib.attn_paged_fwd_granted
+    a.argtypes = [vp, ci, vp, vp, ll, ll, ci, vp, vp, vp, ci, vp]
+    f.argtypes = [vp, ci, vp, vp, vp, ll, ll, ll, ll, ci, ci, vp, vp, vp, ci, ci, ci, ctypes.c_float, vp, sz, vp]
+    for g, T, n, code in ((vp(258), 4, 1, -1), (vp(257), 4, 1, -1), (p, 4, 0, 0), (None, 4, 0, 0), (p, 0, 1, 0)):
+        assert a(c, 0, p, p, 256, 64, T, p, p, g, n, None) == code
+        assert f(c, 0, p, p, None, 512, 64, 512, 64, T, 8, p, p, g, n, 4, 1, 0.125, p, 1 << 40, None) == code
+    assert a(c, 0, None, p, 256, 64, 4, p, p, p, 1, None) == -1
+    assert f(c, 0, p, p, None, 512, 64, 512, 64, 4, 8, p, p, p, 1, 4, 1, 0.125, None, 1 << 40, None) == -3
+
+
+def test_entries_without_room_take_no_part(tmp_path):
+    """granted = 0: no tokens, no work, nothing to report, whatever else the entry says."""
+    src, out = tmp_path / "granted.cpp", tmp_path / "granted.so"
+    src.write_text(r"""
+#include "paged_index.h"
+using namespace eta;
+extern "C" int entry(const int *lens, const int *seqs, const int *qs, const int *granted, int n, int i, int *out) {
+    PagedGeom m;
+    m.page_table = nullptr; m.seq_lens = lens; m.seqs = seqs; m.q_start = qs; m.granted = granted;
+    m.n = n; m.rows = 2; m.max_pages = 4; m.pages = 9; m.page_size = 16; m.T = 20; m.max_q = 9; m.heads = 2; m.g = 3;
+    m.causal = 1; m.tpu = 4; m.tk = 64; m.unit_cost = 64; m.min_share = 128;
+    paged_derive(m);
+    PagedEntry e;
+    const bool ok = paged_entry(m, i, e);
+    out[0] = e.seq; out[1] = e.q0; out[2] = e.nq; out[3] = e.len; out[4] = paged_entry_work(m, e) > 0;
+    return ok;
+}
+""")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I",
+                    os.path.join(ROOT, "exact_tiled_attention_17_gb300", "csrc"), str(src), "-o", str(out)], check=True)
+    f, got = ctypes.CDLL(str(out)).entry, (ci * 5)()
+    ints = lambda v: (ci * len(v))(*v)  # noqa: E731
+    lens, seqs, qs = ints([10, 20]), ints([0, 1, 7, 0]), ints([0, 3, 5, 8, 30])
+    for granted, i, ok, want in ((None, 0, 1, [0, 0, 3, 10, 1]), ([1, 1, 1, 1], 1, 1, [1, 3, 2, 20, 1]),
+                                 ([0, 1, 0, 0], 0, 1, [0, 0, 0, 0, 0]), ([0, 1, 0, 0], 1, 1, [1, 3, 2, 20, 1]),
+                                 ([0, 1, 0, 0], 2, 1, [0, 0, 0, 0, 0]), ([1, 1, 1, 1], 2, 0, [0, 0, 0, 0, 0]),
+                                 ([0, 1, 0, 0], 3, 1, [0, 0, 0, 0, 0]), ([0, 0, 0, 5], 3, 0, [0, 0, 0, 0, 0])):
+        assert f(lens, seqs, qs, ints(granted) if granted else None, 4, i, got) == ok
+        assert list(got) == want, (granted, i)
+
+
 def test_bad_pages_are_not_followed(shim):
     table = [0, 49, 50, -1, -2147483648, 2147483647, 7, 8]
     a = geom([128], [0], [0, 1], 1, 1, max_pages=8, table=table)
