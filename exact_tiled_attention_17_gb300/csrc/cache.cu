@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
             const int q0 = q_start[i], q1 = q_start[i + 1];
             const int s = seqs ? seqs[i] : i;
             const bool here = !granted || granted[i] != 0;
-            bad = here && !(q0 <= t && t < q1 && s >= 0 && s < c.rows);
+            bad = here && !(q0 >= 0 && q0 <= t && t < q1 && q1 <= T && s >= 0 && s < c.rows);
             if (here && !bad) {
                 const int len = c.seq_lens[s];   // (on its way while the list is looked through)
                 const bool again = seqs && named_before(seqs, i, s, [&](int j) {
@@ -608,6 +608,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const CacheView 
                 }
             }
         }
+    }
+    // entries whose range is none, or reaches past the tokens: reported once, since none of their tokens need be met above
+    if (blockIdx.x == 0 && warp == kAppendThreads / 32 - 1) {
+        bool none = false;
+        for (int j = lane; j < n; j += 32) {
+            const int a = q_start[j], b = q_start[j + 1];
+            none |= (a < 0 || b < a || b > T) && (!granted || granted[j] != 0);
+        }
+        if (none) atomicOr(err, kErrWordBadRow);
     }
     if (warp < TOK && lane == 0) {
         dst[warp] = at;

@@ -351,7 +351,8 @@ int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_
  * c) of Knew and Vnew lies at t * token_stride + h * head_stride + c (bases
  * 16-byte aligned, strides multiples of 16 bytes), T tokens in all (at most
  * 2^30); tokens outside q_start[0] .. q_start[n] - 1 go nowhere.  q_start: [n +
- * 1], not decreasing.  A token whose page other table entries name too (its
+ * 1], not decreasing; an entry whose range is not within 0 .. T is left out.
+ * A token whose page other table entries name too (its
  * reserve was refused, or the sequence was forked in between) is not written,
  * and attn_status returns ATTN_ERR_ARG.  Asynchronous.
  *

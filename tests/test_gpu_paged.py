@@ -504,6 +504,28 @@ def test_append_leaves_shared_pages_alone(eta, tokens):
     assert torch.equal(cache.k, want)
 
 
+@pytest.mark.parametrize("T", [10, 5000])
+def test_append_token_ranges(eta, T):
+    """Entries whose tokens are not all rows of the call are left out whole and reported, as in the attention."""
+    big, lens = 2 ** 31 - 1, [T + 8, 40]
+    for qs, ok in (([0, 4, T + 2], [1, 0]), ([-2, 4, 10], [0, 1]), ([0, 4, big], [1, 0]), ([0, T, T + 3], [1, 0]),
+                   ([-5, 0, 3], [0, 1]), ([-9, -5, 3], [0, 0]), ([4, 2, 9], [0, 1]), ([T, T + 1, T + 1], [0, 0])):   # (the last: empty, but past the rows)
+        cache = build(eta, lens, 2, 16, 64)
+        kn = queries(T, 2, 64, BF16)
+        want, table = cache.k.clone(), cache.page_table.tolist()
+        for i in (0, 1):
+            for t in range(qs[i], qs[i + 1] if ok[i] else qs[i]):
+                at = lens[i] - qs[i + 1] + t
+                want[0, table[i][at // 16], :, at % 16] = kn[t]
+        eta.attn_cache_append(cache, 0, kn, kn, None, ints(qs))
+        assert eta.attn_status() == eta.ATTN_ERR_ARG, qs
+        assert torch.equal(cache.k.nan_to_num(9.0), want.nan_to_num(9.0)), qs
+        # an entry that got no room is not looked at
+        eta.attn_cache_append(cache, 0, kn, kn, None, ints(qs), granted=ints(ok))
+        assert eta.attn_status() == eta.ATTN_OK, qs
+        assert torch.equal(cache.k.nan_to_num(9.0), want.nan_to_num(9.0)), qs
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("new", [1, 6, 40])
 def test_entries_without_room_are_left_out(eta, dtype, new):
