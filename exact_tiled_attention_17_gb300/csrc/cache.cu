@@ -409,12 +409,20 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const CacheVie
         int *to = c.page_table + static_cast<long long>(children[i]) * c.max_pages;
         for (int k = threadIdx.x; k < c.max_pages; k += kCopyThreads) {
             int id = -1;
-            if (k < shared) {
-                id = from[k];
-                if (id >= 0 && id < c.pages) atomicAdd(c.ref_counts + id, 1);
-                else atomicOr(err, kErrWordBadRow);
-            } else if (k < shared + need) {
-                id = q.list[q.need_end[i] - need + k - shared];
+            if (k < shared + need) {
+                const int src = from[k];
+                const bool there = src >= 0 && src < c.pages;
+                if (k < shared) {
+                    id = there ? src : -1;
+                    if (there) atomicAdd(c.ref_counts + id, 1);
+                } else {
+                    id = q.list[q.need_end[i] - need + k - shared];
+                    if (!there) {   // nothing to copy: the page goes back
+                        c.ref_counts[id] = 0;
+                        id = -1;
+                    }
+                }
+                if (!there) atomicOr(err, kErrWordBadRow);   // what the parent lacks the child lacks too
             }
             to[k] = id;
         }

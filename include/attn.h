@@ -323,7 +323,8 @@ int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep,
  * a free page, so that both can grow.  copy = 1: every page is copied.
  * Copies are taken in every layer, of the slots that hold tokens (so append a
  * sequence's reserved tokens before it is forked).  Pages are
- * handed out as by attn_cache_reserve; granted: [n] int, written.  A child
+ * handed out as by attn_cache_reserve; granted: [n] int, written.  Where the
+ * parent's table names no page of the pool the child's is -1.  A child
  * that is not empty is refused (granted 0, and attn_status reports
  * ATTN_ERR_ARG).  Asynchronous.
  */

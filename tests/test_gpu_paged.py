@@ -610,6 +610,34 @@ def test_a_captured_step_outlives_its_pool(eta):
     assert refused > 20 and eta.attn_status() == eta.ATTN_OK
 
 
+@pytest.mark.parametrize("copy", [False, True])
+def test_fork_of_a_sequence_that_lacks_pages(eta, copy):
+    """A table entry of the parent that names no page: the child has none there either, and no page is lost."""
+    cache = build(eta, [200, 53, 0, 0, 64, 0], 2, 16, 64, spare=25)
+    cache.k.nan_to_num_(50.0)         # what a handed-out page would bring with it
+    cache.v.nan_to_num_(50.0)
+    for row, col, id_ in ((0, 3, -1), (0, 12, cache.pages), (1, 3, -7), (1, 0, 2 ** 31 - 1)):
+        cache.ref_counts[int(cache.page_table[row, col])] = 0
+        cache.page_table[row, col] = id_
+    assert eta.attn_cache_fork(cache, ints([0, 1, 4]), ints([2, 3, 5]), copy=copy).tolist() == [1, 1, 1]
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert cache.seq_lens.tolist() == [200, 53, 200, 53, 64, 64]
+    table = cache.page_table.tolist()
+    for parent, child in ((0, 2), (1, 3), (4, 5)):
+        assert [0 <= x < cache.pages for x in table[parent]] == [x >= 0 for x in table[child]]
+    names = [0] * cache.pages
+    for row in table:
+        for p in row:
+            if 0 <= p < cache.pages:
+                names[p] += 1
+    assert names == cache.ref_counts.tolist()
+    q = queries(3, 4, 64, BF16)
+    a = eta.attn_paged_fwd(q, cache, 0, ints([0, 1, 4]), ints([0, 1, 2, 3]), max_q=1)
+    b = eta.attn_paged_fwd(q, cache, 0, ints([2, 3, 5]), ints([0, 1, 2, 3]), max_q=1)
+    assert eta.attn_status() == eta.ATTN_ERR_ARG
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("pages", [1, 16, 17, 16384, 16385, 70001])
 def test_pools_of_any_size(eta, pages):
     """The scan over the reference counts: its steps, its tail, a pool that is used up."""
