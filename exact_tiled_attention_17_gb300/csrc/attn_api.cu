@@ -397,6 +397,10 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
 
 namespace {
 constexpr long long kMaxTokens = 1LL << 30;   // of a sequence, and of a call
+// Entries of a list.  Sequences named twice are found by looking through the
+// entries before, so the longest list bounds a kernel's time (seconds), not only
+// the 32-bit arithmetic on entry numbers.
+constexpr int kMaxList = 1 << 20;
 
 // Whether `outer` >= (n - 1) * inner + block, without overflow.
 bool steps_over(long long outer, long long n, long long inner, long long block) {
@@ -468,7 +472,7 @@ int check_device() {
 }  // namespace
 
 size_t attn_cache_workspace_size(int pages, int n) {
-    if (pages <= 0 || n < 0) return 0;
+    if (pages <= 0 || n < 0 || n > kMaxList) return 0;
     return cache_workspace_bytes(pages, n);
 }
 
@@ -477,7 +481,7 @@ int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_
     CacheView w;
     int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (n < 0) return kErrArg;
+    if (n < 0 || n > kMaxList) return kErrArg;
     if (n == 0) return kOk;
     if (!seqs || !n_new || !granted || !aligned4(seqs) || !aligned4(n_new) || !aligned4(granted)) return kErrArg;
     rc = check_workspace(workspace, ws_bytes, cache_workspace_bytes(w.pages, n));
@@ -489,7 +493,7 @@ int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep,
     CacheView w;
     const int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (n < 0) return kErrArg;
+    if (n < 0 || n > kMaxList) return kErrArg;
     if (n == 0) return kOk;
     if (!seqs || !aligned4(seqs) || !aligned4(keep)) return kErrArg;
     return launch_cache_free(w, seqs, keep, n, static_cast<cudaStream_t>(stream));
@@ -500,7 +504,7 @@ int attn_cache_fork(const attn_cache_t *cache, const int *parents, const int *ch
     CacheView w;
     int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (n < 0 || (copy != 0 && copy != 1)) return kErrArg;
+    if (n < 0 || n > kMaxList || (copy != 0 && copy != 1)) return kErrArg;
     if (n == 0) return kOk;
     if (!parents || !children || !granted || !aligned4(parents) || !aligned4(children) || !aligned4(granted)) return kErrArg;
     rc = check_workspace(workspace, ws_bytes, cache_workspace_bytes(w.pages, n));
@@ -532,7 +536,7 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
     CacheView w;
     const int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (n < 0 || T < 0 || T > kMaxTokens || layer < 0 || layer >= w.layers) return kErrArg;
+    if (n < 0 || n > kMaxList || T < 0 || T > kMaxTokens || layer < 0 || layer >= w.layers) return kErrArg;
     // (the stride of a dimension of one element means nothing)
     if (T == 1) token_stride = 0;
     if (w.heads == 1) head_stride = 0;
@@ -567,7 +571,7 @@ int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, 
     CacheView w;
     int rc = check_cache(cache, w);
     if (rc != kOk) return rc;
-    if (layer < 0 || layer >= w.layers || T < 0 || n < 0 || Hq <= 0 || Hq % w.heads) return kErrArg;
+    if (layer < 0 || layer >= w.layers || T < 0 || n < 0 || n > kMaxList || Hq <= 0 || Hq % w.heads) return kErrArg;
     if (Hq / w.heads > 64) return kErrUnsupported;
     if (!(scale > 0.f) || !std::isfinite(scale)) return kErrArg;
     if (causal != 0 && causal != 1) return kErrArg;

@@ -270,8 +270,8 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  * past a sequence's length may hold anything, NaN included; what lies before
  * it must be finite.
  *
- * Lists (seqs, n_new, parents, ...) are int arrays in device memory that
- * overlap nothing a call writes.  Every decision is taken on the device: no
+ * Lists (seqs, n_new, parents, ...) are int arrays in device memory, of at most
+ * 2^20 entries, that overlap nothing a call writes.  Every decision is taken on the device: no
  * call waits for the host, and all can be captured into a graph.  An index that is out of range (a sequence, a
  * page named in the table, a token range) is never followed: that entry is
  * left out, and the next attn_status() returns ATTN_ERR_ARG.  So is a sequence

@@ -157,6 +157,22 @@ def test_cache_entries_rejection(lib):  # noqa: F811
     assert a(c, ci(0), p, p, ll(256), ll(64), ci(4), p, p, ci(0), None) == 0
 
 
+def test_the_longest_list(lib):  # noqa: F811
+    """Entry numbers, and the ends of blocks of entries that reach past them, stay inside 32 bits."""
+    c, p, big = ctypes.byref(cache(max_pages=1)), vp(256), sz(1 << 62)
+    f = lib.attn_cache_workspace_size
+    f.restype, f.argtypes = sz, [ci, ci]
+    assert f(10, 1 << 20) >= (3 << 20) * 4
+    for n in ((1 << 20) + 1, 1 << 30, (1 << 31) - 1024, (1 << 31) - 1):
+        assert f(10, n) == 0
+        assert lib.attn_cache_reserve(c, p, p, ci(n), p, p, big, None) == -1
+        assert lib.attn_cache_free(c, p, p, ci(n), None) == -1
+        assert lib.attn_cache_fork(c, p, p, ci(n), ci(0), p, p, big, None) == -1
+        assert lib.attn_cache_append(c, ci(0), p, p, ll(256), ll(64), ci(0), p, p, ci(n), None) == -1
+        assert paged(lib, c, n=n, T=0) == -1
+    assert paged(lib, c, n=1 << 20, T=0) == 0
+
+
 def test_accepted_layouts(lib):  # noqa: F811
     """Layouts the header allows pass the checks (n = 0: nothing is launched)."""
     p = vp(256)
