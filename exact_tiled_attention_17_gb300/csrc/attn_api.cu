@@ -573,7 +573,8 @@ int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, 
     if (rc != kOk) return rc;
     if (layer < 0 || layer >= w.layers || T < 0 || n < 0 || n > kMaxList || Hq <= 0 || Hq % w.heads) return kErrArg;
     if (Hq / w.heads > 64) return kErrUnsupported;
-    if (!(scale > 0.f) || !std::isfinite(scale)) return kErrArg;
+    // (the kernels work in powers of two: scale * log2(e) has to be a number too, or a score of 0 would be NaN)
+    if (!(scale > 0.f) || !std::isfinite(scale * kPagedLog2e)) return kErrArg;
     if (causal != 0 && causal != 1) return kErrArg;
     if (T > kMaxTokens || static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
     const int bf16 = cache->dtype == ATTN_BF16;

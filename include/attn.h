@@ -377,7 +377,7 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
  * sequence's length and n_i its new tokens, token t sees keys j <= len - n_i +
  * t (causal = 1) or every key j < len (causal = 0).  Hq query heads read
  * cache->heads kv heads: query head j reads head j / (Hq / heads); Hq must be
- * a multiple, at most 64 to a head.
+ * a multiple, at most 64 to a head.  scale: positive, scale * log2(e) finite.
  *
  * Q, O: T rows; element (token t, head j, column c) at t * token_stride +
  * j * head_stride + c, of the cache's dtype (bases 16-byte aligned, strides

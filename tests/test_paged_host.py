@@ -117,6 +117,13 @@ def test_paged_fwd_rejection(lib):  # noqa: F811
     assert paged(lib, c, T=0, max_q=0) == 0 and paged(lib, c, n=0) == 0          # nothing to do
 
 
+def test_the_largest_scale(lib):  # noqa: F811
+    """Scores are kept in powers of two: scale * log2(e) must be finite in float32."""
+    c = ctypes.byref(cache())
+    for scale, code in ((2.35e38, 0), (2.36e38, -1), (3.4e38, -1), (1e-30, 0)):
+        assert paged(lib, c, scale=scale, n=0) == code, scale
+
+
 def test_cache_entries_rejection(lib):  # noqa: F811
     c = ctypes.byref(cache())
     p, big = vp(256), sz(1 << 40)
