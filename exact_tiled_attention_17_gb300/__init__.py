@@ -442,7 +442,7 @@ class PagedCache:
         self._index = k.get_device()
         self._scale = 1.0 / math.sqrt(d)
         self._code = _DTYPE[k.dtype]
-        self._spaces = {}
+        self._spaces = threading.local()   # workspaces of calls that bring none (_paged_workspace)
         self._c = CacheT(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
                          _DTYPE[k.dtype], layers, pages, heads, page_size, d, self.seqs, self.max_pages, k.stride(0),
                          k.stride(1), k.stride(2), k.stride(3))
@@ -509,17 +509,18 @@ _capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.
 def _paged_workspace(workspace, need, cache, st):
     """The caller's workspace, or one of the cache object's own: one for each
     thread and stream, whose calls run in order, so no two calls in flight
-    share it.  A call that is being captured gets memory of its own, which
-    belongs to the graph."""
+    share it.  It is kept as long as the thread and the cache are there (the
+    stream that it was allocated on orders what comes after it).  A call that
+    is being captured gets memory of its own, which belongs to the graph."""
     if workspace is None:
         if _capturing():
             t = torch.empty(need, dtype=torch.uint8, device=cache.device)
             return t, need, t.data_ptr()
-        key = (threading.get_ident(), st)
-        ws = cache._spaces.get(key)
+        spaces = cache._spaces.__dict__   # (this thread's)
+        ws = spaces.get(st)
         if ws is None or ws[1] < need:
             t = torch.empty(need, dtype=torch.uint8, device=cache.device)
-            ws = cache._spaces[key] = (t, need, t.data_ptr())
+            ws = spaces[st] = (t, need, t.data_ptr())
         return ws
     if workspace.get_device() != cache._index or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the cache's device")

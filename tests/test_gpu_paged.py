@@ -3,6 +3,7 @@ definition in float64 (bounds derived in paged_ref.py), the page operators
 against plain integers, and both together as a server uses them."""
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -335,6 +336,33 @@ def test_streams_and_graphs(eta):
         if step in (0, 7, 19):
             check_attention(q, cache, 0, seqs, qs, True, 128 ** -0.5, o, lse)
     ref.check(cache)
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+def test_workspaces_of_threads(eta):
+    """Threads on one stream and on streams of their own: right results, and no workspace outlives its thread."""
+    cache = build(eta, [300, 90], 2, 16, 128, BF16)
+    q, qs = queries(40, 8, 128, BF16), ints([0, 30, 40])
+    want = eta.attn_paged_fwd(q, cache, 0, None, qs)
+    torch.cuda.synchronize()
+    held, got = torch.cuda.memory_allocated(), []
+
+    def work(stream):
+        for _ in range(20):
+            o, lse = eta.attn_paged_fwd(q, cache, 0, None, qs, stream=stream)
+        torch.cuda.synchronize()
+        got.append((o.cpu(), lse.cpu()))
+
+    for _ in range(3):
+        threads = [threading.Thread(target=work, args=(s,)) for s in (None, None, torch.cuda.Stream(), torch.cuda.Stream())]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert len(got) == 12
+    for o, lse in got:
+        assert torch.equal(o, want[0].cpu()) and torch.equal(lse, want[1].cpu())
+    assert torch.cuda.memory_allocated() == held
     assert eta.attn_status() == eta.ATTN_OK
 
 
