@@ -299,12 +299,14 @@ size_t attn_cache_workspace_size(int pages, int n);
  * attn_cache_reserve — room for n_new[i] more tokens in sequence seqs[i]: the
  * sequence gets the pages it lacks (free ones, lowest number first, in list
  * order) and its length grows by n_new[i].  Entries are granted in list order
- * as long as the free pages last; one that needs more pages than are left, or
- * than its table row has, gets nothing and keeps its length (so do later ones
- * that need pages).  Nor does one whose next token would go into a page that
- * other sequences name too (a fork cut back into a page that it shares), and
- * attn_status then returns ATTN_ERR_ARG: a fork of that sequence has a copy of
- * the page and can grow.  granted: [n] int, written: 1 or 0.  Asynchronous.
+ * as long as the free pages last: one that needs more pages than are left gets
+ * nothing and keeps its length, and so do all later ones that need pages.  Two
+ * kinds of entries get nothing and take no part in this (later ones are
+ * granted as if they were not in the list): one that needs more pages than
+ * its table row has; and one whose next token would go into a page that other
+ * sequences name too (a fork cut back into a page that it shares), for which
+ * attn_status returns ATTN_ERR_ARG: a fork of that sequence has a copy of the
+ * page and can grow.  granted: [n] int, written: 1 or 0.  Asynchronous.
  */
 int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_new, int n, int *granted,
                        void *workspace, size_t ws_bytes, void *stream);
