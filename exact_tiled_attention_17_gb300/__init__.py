@@ -679,8 +679,10 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     heads)).  Entry i: sequence seqs[i] (seqs None: sequence i), whose last
     tokens are rows q_start[i] .. q_start[i+1] - 1 of q; causal: token t of the
     entry's n sees keys j <= len - n + t.  max_q: at least the most new tokens
-    of an entry (default T; a close bound lets short entries take the path for
-    few rows).  granted: what attn_cache_reserve returned for these entries;
+    of an entry, at most T.  The default, T, is right for one entry only: it
+    sends a decode batch to the kernel for chunks, which is slower there, takes
+    a workspace of up to 42 MB, and rounds probabilities to bf16 once where
+    decoding (Hq / heads * max_q <= 16) keeps two bf16 parts.  granted: what attn_cache_reserve returned for these entries;
     those that got no room are left out.  Returns (o, lse): o like q, lse [T,
     Hq] float32; rows of no entry, or of one left out, are as they were."""
     shape = q.shape

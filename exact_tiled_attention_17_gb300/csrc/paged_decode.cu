@@ -20,8 +20,10 @@
 //                  rescale.  P goes through shared memory as bf16 (units of
 //                  16 rows: as two bf16 parts, p and what rounding left over,
 //                  so that O is as exact as its own rounding; under the stream
-//                  the second product costs 0.3 us at most), and warp w forms
-//                  O += P V for its quarter of the columns.
+//                  the second product costs 0.3 us at most; with 32 rows the
+//                  second part's buffer, 4 KB, does not fit beside another CTA's,
+//                  and P is rounded once), and warp w forms O += P V for its
+//                  quarter of the columns.
 // Two barriers a tile among the four warps; with two CTAs on an SM one's
 // arithmetic covers the other's.
 //

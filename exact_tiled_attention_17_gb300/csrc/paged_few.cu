@@ -1,5 +1,6 @@
-// Attention of a few new tokens over a paged cache, IEEE float32 throughout
-// (no TF32): units (paged_index.h) of at most R = 4 or 8 query rows.
+// Attention of a few new tokens over a paged cache, float32: IEEE products and
+// sums (no TF32), exponentials from ex2.approx (relative error 2^-22 at most):
+// units (paged_index.h) of at most R = 4 or 8 query rows.
 //
 // The work is one pass over K and V, bound by HBM, so a warp streams keys from
 // global memory into registers, and a row of K lies across the lanes that hold

@@ -1,5 +1,6 @@
-// Attention of new tokens over a paged cache on the CUDA cores: IEEE float32
-// throughout (no TF32), float32 storage.
+// Attention of new tokens over a paged cache on the CUDA cores, float32: IEEE
+// products and sums (no TF32), exponentials from ex2.approx (relative error
+// 2^-22 at most).
 //
 // O = softmax(scale Q K^T) V of each unit (paged_index.h: one kv head, a block
 // of new tokens, all query heads of the group), key tile by key tile with the

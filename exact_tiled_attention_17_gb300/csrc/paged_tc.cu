@@ -12,7 +12,11 @@
 //                  the tile's 64-key halves of S and of O's columns, one
 //                  thread per row; running maximum m (moved only when a tile
 //                  exceeds it by 2^8, so O is rescaled rarely) and float32
-//                  sum l of the unrounded p; P as bf16 over S in tensor memory.
+//                  sum l of the unrounded p; P as bf16 over S in tensor memory
+//                  (the instruction takes 16-bit operands next to a bf16 V; a
+//                  second part, what the rounding left over, would add half to
+//                  the products of a kernel whose tensor pipe is 60 % busy; a
+//                  weight is off by 2^-8 of itself at most, the sum l is not).
 //   warp 16        finds the CTA's work and announces it unit by unit; TMA
 //                  producer of the Q tiles and of K_j.
 //   warp 17        MMA issuer: S_q = Q_q K_j^T, O_q += P_q V_j.

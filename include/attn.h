@@ -386,14 +386,18 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
  * positive multiples of 16 bytes; rows of O do not overlap, nor O and Q).  At
  * most 2^30 tokens, and T * Hq below 2^31.  LSE: [T][Hq] float32 natural log, or NULL.  Rows
  * outside q_start[0] .. q_start[n] - 1 are left as they were.  A row that
- * sees no key gives O = 0, LSE = -inf.  max_q: at least the largest n_i (T
- * always is); an entry with more is left out.  A table entry that names no
- * page of the pool counts as page_size keys that no row sees.
+ * sees no key gives O = 0, LSE = -inf.  max_q: at least the largest n_i and at
+ * most T (a larger one is refused); an entry with more is left out.  It
+ * chooses the kernel for the whole call, whatever the entries then hold, so a
+ * close bound is faster and, for bf16, more exact.  A table entry that names
+ * no page of the pool counts as page_size keys that no row sees.
  *
- * bf16: scores, softmax and sums in float32, probabilities rounded to bf16
- * for the product with V (to two bf16 parts where an entry has at most 16
- * rows of Q per kv head); d in {32, 64, 96, 128}.  float32: IEEE float32
- * throughout.  workspace: at least attn_paged_workspace_size(Hq, heads,
+ * bf16: scores, softmax and sums in float32; probabilities are rounded to bf16
+ * for the product with V, once, or where Hq / heads * max_q is at most 16 to
+ * two bf16 parts (O is then off by little more than its own rounding).
+ * float32: products and sums in IEEE float32, no TF32.  Both take exponentials
+ * from the hardware's power of two (relative error 2^-22 at most); d in {32,
+ * 64, 96, 128}.  workspace: at least attn_paged_workspace_size(Hq, heads,
  * max_q, d, dtype) bytes, 16-byte aligned.  Asynchronous: two launches.
  *
  * attn_paged_fwd_granted — the same with the list that attn_cache_reserve
