@@ -8,6 +8,7 @@ import threading
 import pytest
 import torch
 
+from paged_bounds import close_weights, counts, fine_keys
 from paged_ref import Pages, check_attention, gather
 
 pytestmark = pytest.mark.gpu
@@ -144,6 +145,40 @@ def test_one_unit_over_all_ctas(eta, dtype, new):
     """More parts to a row than the merge kernel reads at once (one kv head, a long context)."""
     cache = build(eta, [70001], 1, 64, 64, dtype, seed=new)
     attend(eta, cache, [new], 4, seed=new)
+
+
+def run_known(eta, known, page=64):
+    """The known case as a sequence on random pages, beside NaN."""
+    (n, d), dtype = known.k.shape, known.q.dtype
+    cache = build(eta, [3, n], 1, page, d, dtype, seed=n)
+    at = torch.arange(n, device="cuda")
+    ids = cache.page_table[1].long()[at // page]
+    cache.k[0, ids, 0, at % page] = known.k.cuda()
+    cache.v[0, ids, 0, at % page] = known.v.cuda()
+    T = known.q.shape[0]
+    o, lse = eta.attn_paged_fwd(known.q.cuda(), cache, 0, ints([1]), ints([0, T]), scale=known.scale)
+    assert eta.attn_status() == eta.ATTN_OK
+    known.check(o, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 2, 7, 40])
+def test_every_key_of_a_long_context_counts(eta, dtype, new):
+    """One unit over all CTAs, more parts than the merge reads at once: none may be lost."""
+    run_known(eta, counts(70001, new, 4, 64, dtype))
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("n,new,g", [(2, 1, 8), (17, 1, 4), (40, 4, 4), (64, 16, 1)])
+def test_probabilities_in_two_parts(eta, d, n, new, g):
+    """At most 16 rows: one rounding of P to bf16 would be far outside the bound."""
+    run_known(eta, close_weights(n, new, g, d), page=16)
+
+
+@pytest.mark.parametrize("n,new", [(50, 1), (5000, 1), (5000, 2), (5000, 4), (5000, 8), (5000, 40), (70001, 1), (70001, 40)])
+def test_float32_keeps_its_bits(eta, n, new):
+    """Keys that TF32 does not tell apart, at lengths where a bound by the worst sum would hide it."""
+    run_known(eta, fine_keys(n, new, 4))
 
 
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (F32, 64)])
