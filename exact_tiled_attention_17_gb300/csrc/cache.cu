@@ -723,7 +723,7 @@ int launch_cache_append(const CacheView &c, int layer, const void *Kn, const voi
     if (!err) return kErrCuda;
     const uint4 *k = static_cast<const uint4 *>(Kn), *v = static_cast<const uint4 *>(Vn);
     // up to 4096 tokens two to a CTA (131 tokens x 8 heads x 128: 2.7 us, 3.9 with
-    // eight), more eight (8000: 10.2 us, 10.4 with two; 7000 tokens' 58 MB at 0.97 of the copy rate)
+    // eight), more eight (8000: 10.2 us, 10.4 with two; 7000 tokens of 58 MB, two layers in turn: 10.4 us, 0.84 of the copy rate)
     if (T <= 4096)
         return launch(append_kernel<2>, static_cast<unsigned>((T + 1) / 2), kAppendThreads, stream, c, layer, k, v,
                       token_vecs, head_vecs, T, seqs, q_start, granted, n, err);

@@ -15,15 +15,18 @@
 //          bytes of shared memory.
 // A lane has 4 columns, so d < 128 puts several keys side by side (d 64: two, d
 // 32: four; at d 96 a quarter of the lanes repeats others' work).  K of the next batch
-// is on its way while P V runs, V during the next scores: 2 to 8 KB a warp, 12 or 16
-// warps an SM.
+// is on its way while P V runs, V during the next scores: 1 KB a warp (d 32, 8 rows:
+// one load a lane of each) to 8 KB (d 128, 4 rows), 12 or 16 warps an SM.
 // A batch lies in one page (pages begin at multiples of 16), looked up two
 // batches ahead.  Keys past the end and of missing pages are not read (zeros);
 // keys a row does not see have score -inf.
 //
-// Measured, 32 sequences of 8000 tokens, 4 rows: d 128, 4 kv heads: 1.05 GB in 162 us, 0.97 of
+// Measured, 32 sequences of 8000 tokens, 4 rows: d 128, 4 kv heads: 1.05 GB in 160 us, 0.98 of
 // the measured copy rate (units of 16 rows in the tiling kernel: 365); d 64, 8 heads:
-// 165 us (366); d 96 131 us; d 32, 16 heads: 200 us.  8 rows, d 128: 204 us.
+// 166 us (366); d 96, 4 heads: 130 us, 0.91; d 32, 16 heads: 200 us, 0.79.  8 rows: d 128 206
+// us, 0.76; d 96 203, 0.58; d 64 258, 0.61; d 32 372, 0.42: twice the products and
+// half the bytes on their way (and at d 64 148 bytes of spills a thread; 57 % of the
+// issue slots are used).
 #include <algorithm>
 
 #include "launch.cuh"
@@ -43,8 +46,8 @@ struct FewShape {
     static constexpr int SIDE = 32 / NV;                 // keys side by side
     static constexpr int NK = NV / R;                    // loads of a batch
     static constexpr int KEYS = NK * SIDE;               // keys of a batch: 32 / R
-    // on an SM; registers decide (32 x 8000 tokens, 4 rows, d 128: three 162 us, four,
-    // which spill, 191; d 64: 175 and 165)
+    // on an SM; registers decide (32 x 8000 tokens, 4 rows, d 128: three 160 us, four,
+    // which spill, 191; d 64: 175 and 166)
     static constexpr int CTAS = E >= 3 ? 3 : 4;
     static_assert(KEYS == 32 / R && NK >= 1, "a score to a lane");
 };
