@@ -559,7 +559,7 @@ def attn_cache_reserve(cache, seqs, n_new, granted=None, workspace=None, stream=
 
 
 def attn_cache_free(cache, seqs, keep=None, stream=None) -> None:
-    """Cuts sequence seqs[i] to its first keep[i] tokens (None: to none)."""
+    """Cuts sequence seqs[i] to its first keep[i] tokens (None, or negative: to none)."""
     n = seqs.shape[0]
     a = _paged_list(seqs, cache, "seqs")
     b = None if keep is None else _paged_list(keep, cache, "keep", n)

@@ -673,6 +673,21 @@ def test_a_captured_step_outlives_its_pool(eta):
     assert refused > 20 and eta.attn_status() == eta.ATTN_OK
 
 
+def test_free_keeps_what_it_is_told(eta):
+    """Counts of none, negative ones, all, and more than there is."""
+    cache = new_cache(eta, 30, 16, 6, 4)
+    ref = Pages(cache)
+    everyone, lens = list(range(6)), [33, 16, 1, 64, 20, 0]
+    assert eta.attn_cache_reserve(cache, ints(everyone), ints(lens)).tolist() == ref.reserve(everyone, lens)
+    keep = [-1, 16, 0, 2 ** 31 - 1, -2 ** 31, 3]
+    eta.attn_cache_free(cache, ints(everyone), ints(keep))
+    ref.free(everyone, keep)
+    assert ref.lens == [0, 16, 0, 64, 0, 0]
+    ref.check(cache)
+    ref.consistent()
+    assert eta.attn_status() == eta.ATTN_OK
+
+
 @pytest.mark.parametrize("copy", [False, True])
 def test_fork_of_a_sequence_that_lacks_pages(eta, copy):
     """A table entry of the parent that names no page: the child has none there either, and no page is lost."""
