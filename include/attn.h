@@ -313,8 +313,8 @@ int attn_cache_reserve(const attn_cache_t *cache, const int *seqs, const int *n_
 
 /*
  * attn_cache_free — cuts sequence seqs[i] to its first keep[i] tokens (keep
- * NULL, or negative: none; more than it has: no change).  Pages past them leave the table
- * and lose a reference.  Asynchronous.
+ * NULL, or negative: none; more than it has: no change).  Pages past them
+ * leave the table and lose a reference.  Asynchronous.
  */
 int attn_cache_free(const attn_cache_t *cache, const int *seqs, const int *keep, int n, void *stream);
 
