@@ -11,9 +11,11 @@ import fails loudly; there is no CPU or PyTorch fallback.
     attn_naive_fwd(...)      materialising baseline (S and P in the input dtype)
     attn_deviation(a, b)     max-abs, Wasserstein-1 (via sort), mean/std |a-b|
 
-A paged key/value cache (``PagedCache``): pages are handed out, shared and
-released on the device by attn_cache_reserve / _free / _fork / _compact, new
-tokens are written by attn_cache_append and attended to by attn_paged_fwd.
+A paged key/value cache (``PagedCache``), of bf16, float32 or 4-bit values: pages
+are handed out, shared and released on the device by attn_cache_reserve / _free /
+_fork / _compact; new tokens are written by attn_cache_append, or with the position
+rotation by attn_cache_append_rotated, attended to by attn_paged_fwd and copied out
+by attn_cache_read.
 """
 from __future__ import annotations
 
@@ -29,7 +31,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn.so")
 
-ATTN_F32, ATTN_BF16, ATTN_F64 = 0, 1, 2
+ATTN_F32, ATTN_BF16, ATTN_F64, ATTN_E2M1 = 0, 1, 2, 3
 ATTN_OK = 0
 ATTN_ERR_ARG = -1
 ATTN_ERR_UNSUPPORTED = -2
@@ -42,7 +44,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_host_workspace_size", "attn_fwd_host", "attn_fw
            "attn_deviation", "attn_deviation_noalloc", "attn_decode_workspace_size", "attn_decode_fwd",
            "attn_cache_workspace_size", "attn_cache_reserve", "attn_cache_free", "attn_cache_fork", "attn_cache_compact",
            "attn_cache_append", "attn_cache_append_granted", "attn_paged_workspace_size", "attn_paged_fwd",
-           "attn_paged_fwd_granted",
+           "attn_paged_fwd_granted", "attn_cache_append_rotated", "attn_cache_read",
            "attn_bwd_workspace_size", "attn_bwd", "attn_emul_fwd", "attn_emul_round", "attn_status",
            "attn_strerror", "attn_last_variant", "attn_debug_wait_timeout")
 DEVIATION_NOALLOC_MAX_N = 1 << 20
@@ -69,6 +71,12 @@ class CacheT(ctypes.Structure):
                 ("d", ctypes.c_int), ("seqs", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("layer_stride", ctypes.c_longlong), ("page_stride", ctypes.c_longlong),
                 ("head_stride", ctypes.c_longlong), ("slot_stride", ctypes.c_longlong)]
+
+
+class RotationT(ctypes.Structure):
+    """attn_rotation_t"""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rows", ctypes.c_int), ("dims", ctypes.c_int),
+                ("neighbours", ctypes.c_int)]
 
 
 def _load() -> ctypes.CDLL:
@@ -120,6 +128,11 @@ def _load() -> ctypes.CDLL:
     lib.attn_paged_fwd.restype = i
     lib.attn_paged_fwd_granted.argtypes = [cp, i, vp, vp, vp, ll, ll, ll, ll, i, i, vp, vp, vp, i, i, i, f, vp, sz, vp]
     lib.attn_paged_fwd_granted.restype = i
+    lib.attn_cache_append_rotated.argtypes = [cp, i, vp, vp, ll, ll, vp, vp, i, ll, ll, ll, ll, i, vp, vp, vp, i,
+                                              ctypes.POINTER(RotationT), vp]
+    lib.attn_cache_append_rotated.restype = i
+    lib.attn_cache_read.argtypes = [cp, i, vp, vp, ll, ll, i, vp, vp, vp, i, vp]
+    lib.attn_cache_read.restype = i
     lib.attn_bwd_workspace_size.argtypes = [i, i, i, i]
     lib.attn_bwd_workspace_size.restype = sz
     lib.attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp, vp, sz, vp]
@@ -413,19 +426,32 @@ class PagedCache:
     float32, with equal strides; a page of one layer is one contiguous block,
     head by head (a contiguous tensor) or token by token (a tensor of
     [layers, pages, page_size, heads, d] seen through transpose(2, 3)).
+    Or uint8, [layers, pages, heads, page_size, 9 * d / 16], head by head: a
+    cache of 4-bit values.  The last two dimensions are one run of bytes, first
+    the codes, page_size x d / 2, then the scales, page_size x d / 16 (views of
+    both: ``parts``); what goes in and out of the cache is bfloat16.
     page_table: int32 [seqs, max_pages], -1 where a sequence has no page;
     seq_lens: int32 [seqs]; ref_counts: int32 [pages].  The object keeps the
-    tensors; all are changed in place by the operators below.
+    tensors; all are changed in place by the operators below.  dtype is that of
+    rows that go in and out.
     """
 
     def __init__(self, k, v, page_table, seq_lens, ref_counts):
         if k.dim() != 5 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
             raise ValueError("k and v must be [layers, pages, heads, page_size, d] with one shape, dtype and strides")
-        if k.dtype not in _DTYPE:
+        four = k.dtype == torch.uint8
+        if k.dtype not in _DTYPE and not four:
             raise ValueError(f"unsupported dtype {k.dtype}")
         if k.shape[4] > 1 and k.stride(4) != 1:
             raise ValueError("the last dimension of k and v must be contiguous")
         layers, pages, heads, page_size, d = k.shape
+        slot_stride = k.stride(3)
+        if four:
+            if d % 18 or (page_size > 1 and slot_stride != d):
+                raise ValueError("k and v of 4-bit values must be [layers, pages, heads, page_size, 9 * d / 16] bytes, "
+                                 "the last two dimensions contiguous")
+            d = d // 9 * 16
+            slot_stride = d // 2
         for t, shape, name in ((page_table, 2, "page_table [seqs, max_pages]"), (seq_lens, 1, "seq_lens [seqs]"),
                                (ref_counts, 1, "ref_counts [pages]")):
             if t.dtype != torch.int32 or t.dim() != shape or not t.is_contiguous():
@@ -436,23 +462,38 @@ class PagedCache:
             if not t.is_cuda or t.device != k.device:
                 raise ValueError("the tensors of a cache must be on one CUDA device")
         self.k, self.v, self.page_table, self.seq_lens, self.ref_counts = k, v, page_table, seq_lens, ref_counts
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype = k.device, torch.bfloat16 if four else k.dtype
         self.layers, self.pages, self.heads, self.page_size, self.d = layers, pages, heads, page_size, d
         self.seqs, self.max_pages = page_table.shape
         self._index = k.get_device()
         self._scale = 1.0 / math.sqrt(d)
-        self._code = _DTYPE[k.dtype]
+        self._code = ATTN_E2M1 if four else _DTYPE[k.dtype]
         self._spaces = threading.local()   # workspaces of calls that bring none (_paged_workspace)
         self._c = CacheT(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-                         _DTYPE[k.dtype], layers, pages, heads, page_size, d, self.seqs, self.max_pages, k.stride(0),
-                         k.stride(1), k.stride(2), k.stride(3))
+                         self._code, layers, pages, heads, page_size, d, self.seqs, self.max_pages, k.stride(0),
+                         k.stride(1), k.stride(2), slot_stride)
         self._p = ctypes.pointer(self._c)
+
+    def parts(self, pool):
+        """Views of a pool (``k`` or ``v``) of 4-bit values: codes [layers, pages,
+        heads, page_size, d / 2], two columns to a byte, and scales [layers, pages,
+        heads, page_size, d / 16], uint8."""
+        if self._code != ATTN_E2M1:
+            raise ValueError("only a cache of 4-bit values has codes and scales")
+        block, S, d = pool.flatten(3), self.page_size, self.d
+        return (block[..., :S * d // 2].unflatten(3, (S, d // 2)), block[..., S * d // 2:].unflatten(3, (S, d // 16)))
 
     @classmethod
     def empty(cls, layers: int, pages: int, heads: int, page_size: int, d: int, seqs: int, max_pages: int,
               dtype=torch.bfloat16, device="cuda", token_major: bool = False):
-        """A new cache without sequences.  token_major: pages lie token by
+        """A new cache without sequences.  dtype: bfloat16, float32, or
+        torch.float4_e2m1fn_x2 for 4-bit values.  token_major: pages lie token by
         token instead of head by head."""
+        if dtype == torch.float4_e2m1fn_x2:
+            if token_major or d % 32:
+                raise ValueError("pages of 4-bit values lie head by head, with d a multiple of 32")
+            dtype, d = torch.uint8, 9 * d // 16
+
         def pool():
             if token_major:
                 return torch.empty((layers, pages, page_size, heads, d), dtype=dtype, device=device).transpose(2, 3)
@@ -481,6 +522,7 @@ def _paged_list(t, cache, name, n=None):
 _lib_reserve, _lib_free, _lib_fork = lib.attn_cache_reserve, lib.attn_cache_free, lib.attn_cache_fork
 _lib_compact, _lib_append, _lib_paged_fwd = lib.attn_cache_compact, lib.attn_cache_append, lib.attn_paged_fwd
 _lib_append_granted, _lib_paged_fwd_granted = lib.attn_cache_append_granted, lib.attn_paged_fwd_granted
+_lib_append_rotated, _lib_read = lib.attn_cache_append_rotated, lib.attn_cache_read
 
 
 @contextlib.contextmanager
@@ -616,6 +658,17 @@ def _append(cache, st, layer, k, v, strides, T, a, b, c, n):
     return _lib_append_granted(cache._p, layer, k, v, strides[0], strides[1], T, a, b, c, n, st)
 
 
+def _new_rows(cache, k, v, ks, vs):
+    shape, strides = k.shape, k.stride()
+    if (len(shape) != 3 or shape != v.shape or strides != v.stride() or shape[1] != cache.heads or
+            shape[2] != cache.d or strides[2] != 1):
+        raise ValueError(f"{ks} and {vs} must be [T, heads, d] with one shape and strides, the last dimension contiguous")
+    if (k.dtype != cache.dtype or v.dtype != cache.dtype or k.get_device() != cache._index or
+            v.get_device() != cache._index):
+        raise ValueError(f"{ks} and {vs} must have the cache's dtype and device")
+    return shape, strides
+
+
 def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=None, granted=None) -> None:
     """Writes the keys and values of new tokens into one layer.  k_new, v_new:
     [T, heads, d] of the cache's dtype, any strides with a contiguous last
@@ -624,13 +677,7 @@ def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=Non
     ones of the sequence (reserved before).  granted: what attn_cache_reserve
     returned for these entries; those that got no room are left out (without
     it they write over the sequence's last tokens)."""
-    shape, strides = k_new.shape, k_new.stride()
-    if (len(shape) != 3 or shape != v_new.shape or strides != v_new.stride() or shape[1] != cache.heads or
-            shape[2] != cache.d or strides[2] != 1):
-        raise ValueError("k_new and v_new must be [T, heads, d] with one shape and strides, the last dimension contiguous")
-    if (k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or k_new.get_device() != cache._index or
-            v_new.get_device() != cache._index):
-        raise ValueError("k_new and v_new must have the cache's dtype and device")
+    shape, strides = _new_rows(cache, k_new, v_new, "k_new", "v_new")
     n = q_start.shape[0] - 1
     a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
     b = _paged_list(q_start, cache, "q_start")
@@ -644,13 +691,103 @@ def attn_cache_append(cache, layer: int, k_new, v_new, seqs, q_start, stream=Non
     _check(rc, "attn_cache_append")
 
 
+def _append_rotated(cache, st, layer, k, v, strides, q, q_out, Hq, T, a, b, c, n, rotation):
+    qp, op, qs, os_ = None, None, (0, 0), (0, 0)
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qp, op, qs, os_ = q.data_ptr(), q_out.data_ptr(), q.stride(), q_out.stride()
+    _check(_lib_append_rotated(cache._p, layer, k, v, strides[0], strides[1], qp, op, Hq, qs[0], qs[1], os_[0], os_[1], T, a, b,
+                               c, n, ctypes.byref(rotation), st), "attn_cache_append_rotated")
+    return q_out
+
+
+def attn_cache_append_rotated(cache, layer: int, k_new, v_new, seqs, q_start, table, q=None, q_out=None,
+                              neighbours: bool = False, positions=None, granted=None, stream=None):
+    """attn_cache_append with the position rotation applied to the keys on the
+    way, and to the queries of the same tokens.  table: contiguous float32
+    [positions, dims], of each position dims / 2 cosines and then as many sines;
+    the first dims columns of a row turn, dims <= d.  Pair i is columns i and
+    i + dims / 2, or (neighbours) 2 i and 2 i + 1.  A token's position is its
+    index in its sequence, or positions[t] (int32 [T]).  q: [T, Hq, d] as for
+    attn_paged_fwd, or None; q_out: where its rotated rows go (q itself: in
+    place; default: a new tensor).  Returns q_out (None without q); its rows of
+    tokens that are not written are as they were."""
+    shape, strides = _new_rows(cache, k_new, v_new, "k_new", "v_new")
+    T, Hq = shape[0], 0
+    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != cache._index:
+        raise ValueError("table must be a contiguous float32 tensor [positions, dims] on the cache's device")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        if Hq == 0 or q.shape[0] != T or q.shape[2] != cache.d or q.stride(2) != 1:
+            raise ValueError("q must be [T, Hq, d] with a contiguous last dimension")
+        if q.dtype != cache.dtype or q.get_device() != cache._index:
+            raise ValueError("q must have the cache's dtype and device")
+        if q_out is not None and (q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != cache._index or
+                                  q_out.stride(2) != 1):
+            raise ValueError("q_out must be like q, with a contiguous last dimension")
+    n = q_start.shape[0] - 1
+    a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
+    b = _paged_list(q_start, cache, "q_start")
+    c = None if granted is None else _paged_list(granted, cache, "granted", n)
+    p = None if positions is None else _paged_list(positions, cache, "positions", T)
+    rotation = RotationT(table.data_ptr(), p, table.shape[0], table.shape[1], 1 if neighbours else 0)
+    args = (layer, k_new.data_ptr(), v_new.data_ptr(), strides, q, q_out, Hq, T, a, b, c, n, rotation)
+    if _paged_here(cache, stream):
+        return _append_rotated(cache, _raw_stream(cache._index), *args)
+    with _paged_scope(cache, stream) as st:
+        return _append_rotated(cache, st, *args)
+
+
+def _read(cache, st, layer, shape, k, v, T, a, b, c, n):
+    if k is None:
+        k = torch.empty(shape, dtype=cache.dtype, device=cache.device)
+        v = torch.empty_like(k)
+    s = k.stride()
+    _check(_lib_read(cache._p, layer, k.data_ptr(), v.data_ptr(), s[0], s[1], T, a, b, c, n, st), "attn_cache_read")
+    return k, v
+
+
+def attn_cache_read(cache, layer: int, seqs, q_start, T: int | None = None, first=None, k_out=None, v_out=None, stream=None):
+    """Copies tokens of one layer out of the cache (of 4-bit values: the values
+    that they stand for, exact in bfloat16).  Entry i: sequence seqs[i] (seqs
+    None: sequence i), whose tokens first[i], first[i] + 1, ... (first None: the
+    last ones) go to rows q_start[i] .. q_start[i+1] - 1.  T: rows in all;
+    k_out, v_out: [T, heads, d] of the cache's dtype with one pair of strides, or
+    new tensors (T needed).  Returns (k, v); rows of no entry, and of tokens that
+    the cache does not hold, are as they were."""
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is not None:
+        shape, _ = _new_rows(cache, k_out, v_out, "k_out", "v_out")
+        if T is not None and T != shape[0]:
+            raise ValueError("k_out and v_out must have T rows")
+        T = shape[0]
+    elif T is None or T < 0:
+        raise ValueError("T, the rows in all, is needed where k_out and v_out are not given")
+    n = q_start.shape[0] - 1
+    a = None if seqs is None else _paged_list(seqs, cache, "seqs", n)
+    b = _paged_list(q_start, cache, "q_start")
+    c = None if first is None else _paged_list(first, cache, "first", n)
+    args = (layer, (T, cache.heads, cache.d), k_out, v_out, T, a, b, c, n)
+    if _paged_here(cache, stream):
+        return _read(cache, _raw_stream(cache._index), *args)
+    with _paged_scope(cache, stream) as st:
+        return _read(cache, st, *args)
+
+
 @functools.lru_cache(maxsize=256)
 def _paged_workspace_size(Hq, heads, max_q, d, dtype) -> int:
     return int(lib.attn_paged_workspace_size(Hq, heads, max_q, d, dtype))
 
 
 def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) -> int:
-    return _paged_workspace_size(Hq, heads, max_q, d, _DTYPE[dtype] if not isinstance(dtype, int) else dtype)
+    """dtype: the cache's (torch.float4_e2m1fn_x2 for 4-bit values)."""
+    code = dtype if isinstance(dtype, int) else ATTN_E2M1 if dtype == torch.float4_e2m1fn_x2 else _DTYPE[dtype]
+    return _paged_workspace_size(Hq, heads, max_q, d, code)
 
 
 def _paged_fwd(cache, st, q, layer, shape, a, b, c, n, max_q, causal, scale, o, l, want_lse, workspace):

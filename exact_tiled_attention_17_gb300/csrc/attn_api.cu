@@ -410,7 +410,8 @@ bool steps_over(long long outer, long long n, long long inner, long long block) 
 // Checks a cache descriptor; fills the page kernels' view of it.
 int check_cache(const attn_cache_t *c, CacheView &w) {
     if (!c || !c->K || !c->V || !c->page_table || !c->seq_lens || !c->ref_counts) return kErrArg;
-    if (c->dtype != ATTN_F32 && c->dtype != ATTN_BF16) return c->dtype == ATTN_F64 ? kErrUnsupported : kErrArg;
+    if (c->dtype != ATTN_F32 && c->dtype != ATTN_BF16 && c->dtype != ATTN_E2M1)
+        return c->dtype == ATTN_F64 ? kErrUnsupported : kErrArg;
     if (c->layers <= 0 || c->pages <= 0 || c->heads <= 0 || c->page_size <= 0 || c->d <= 0 || c->seqs <= 0 ||
         c->max_pages <= 0)
         return kErrArg;
@@ -420,13 +421,17 @@ int check_cache(const attn_cache_t *c, CacheView &w) {
     if (static_cast<long long>(c->max_pages) * c->page_size > kMaxTokens) return kErrArg;
     if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->ref_counts)) return kErrArg;
     if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) || (reinterpret_cast<uintptr_t>(c->seq_lens) & 3u)) return kErrArg;
-    const long long per = 16 / (c->dtype == ATTN_BF16 ? 2 : 4);   // elements of a 16-byte piece
-    const long long block = static_cast<long long>(c->heads) * c->page_size * c->d;
+    // elements of a 16-byte piece (4-bit values: an element is a byte), and of one head's rows of a page
+    const bool q4 = c->dtype == ATTN_E2M1;
+    const long long per = q4 ? 16 : c->dtype == ATTN_BF16 ? 8 : 4;
+    const long long head = static_cast<long long>(c->page_size) * (q4 ? c->d / 16 * 9 : c->d);
+    const long long block = c->heads * head;
     if (block / per >= (1LL << 30)) return kErrArg;
-    const bool by_head = c->head_stride == static_cast<long long>(c->page_size) * c->d && c->slot_stride == c->d;
-    const bool by_token = c->slot_stride == static_cast<long long>(c->heads) * c->d && c->head_stride == c->d;
+    const long long row = q4 ? c->d / 2 : c->d;
+    const bool by_head = c->head_stride == head && c->slot_stride == row;
+    const bool by_token = !q4 && c->slot_stride == static_cast<long long>(c->heads) * c->d && c->head_stride == c->d;
     // (with one head, or as strides of a single head may be given, both agree)
-    const bool one_head = c->heads == 1 && c->slot_stride == c->d && c->head_stride >= 0 && c->head_stride % per == 0;
+    const bool one_head = c->heads == 1 && c->slot_stride == row && c->head_stride >= 0 && c->head_stride % per == 0;
     if (!by_head && !by_token && !one_head) return kErrArg;
     if (c->page_stride < 0 || c->layer_stride < 0 || c->page_stride % per || c->layer_stride % per) return kErrArg;
     // blocks of different (layer, page) do not overlap, whichever stride is the outer one
@@ -454,9 +459,40 @@ int check_cache(const attn_cache_t *c, CacheView &w) {
     w.block_vecs = static_cast<int>(block / per);
     w.slot_vecs = static_cast<int>(c->slot_stride / per);
     w.row_vecs = static_cast<int>(c->d / per);
+    w.bits = q4 ? 4 : c->dtype == ATTN_BF16 ? 16 : 32;
     return kOk;
 }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Whether rows of d elements at (t * token, h * head) do not overlap: one of the strides steps over all of the other's range.
+bool rows_apart(long long T, long long heads, long long token, long long head, long long d) {
+    const bool heads_in = (heads == 1 || head >= d) && (T == 1 || steps_over(token, heads, head, d));
+    const bool tokens_in = (T == 1 || token >= d) && (heads == 1 || steps_over(head, T, token, d));
+    return heads_in || tokens_in;
+}
+// Checks what the calls that move rows of tokens share (bases, strides, the list); `none`: there is nothing to do.
+int check_append(const attn_cache_t *cache, int layer, const void *K, const void *V, long long token_stride,
+                 long long head_stride, const RowList &li, CacheView &w, RowIn &in, bool &none) {
+    const int rc = check_cache(cache, w);
+    if (rc != kOk) return rc;
+    if (li.n < 0 || li.n > kMaxList || li.T < 0 || li.T > kMaxTokens || layer < 0 || layer >= w.layers) return kErrArg;
+    // (the stride of a dimension of one element means nothing)
+    if (li.T == 1) token_stride = 0;
+    if (w.heads == 1) head_stride = 0;
+    const long long es = w.bits == 32 ? 4 : 2, per = 16 / es;
+    if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
+    none = li.n == 0 || li.T == 0;
+    if (none) return kOk;
+    if (!K || !V || !li.q_start || !aligned16(K) || !aligned16(V) || !aligned4(li.q_start) || !aligned4(li.seqs) ||
+        !aligned4(li.granted))
+        return kErrArg;
+    in.K = static_cast<const char *>(K);
+    in.V = static_cast<const char *>(V);
+    in.token_bytes = token_stride * es;
+    in.head_bytes = head_stride * es;
+    in.d = cache->d;
+    return kOk;
+}
+constexpr long long kMaxRows = 1LL << 20;   // rows of a token (K, V and Q) in the calls that count them in 32 bits
 int check_workspace(const void *ws, size_t have, size_t need) {
     return !ws || have < need || !aligned16(ws) ? kErrWorkspace : kOk;
 }
@@ -534,26 +570,79 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
                               long long token_stride, long long head_stride, int T, const int *seqs, const int *q_start,
                               const int *granted, int n, void *stream) {
     CacheView w;
-    const int rc = check_cache(cache, w);
-    if (rc != kOk) return rc;
-    if (n < 0 || n > kMaxList || T < 0 || T > kMaxTokens || layer < 0 || layer >= w.layers) return kErrArg;
-    // (the stride of a dimension of one element means nothing)
-    if (T == 1) token_stride = 0;
-    if (w.heads == 1) head_stride = 0;
-    const long long per = 16 / (cache->dtype == ATTN_BF16 ? 2 : 4);
-    if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
-    if (n == 0 || T == 0) return kOk;
-    if (!Knew || !Vnew || !q_start || !aligned16(Knew) || !aligned16(Vnew) || !aligned4(q_start) || !aligned4(seqs) ||
-        !aligned4(granted))
-        return kErrArg;
-    return launch_cache_append(w, layer, Knew, Vnew, token_stride / per, head_stride / per, T, seqs, q_start, granted, n,
+    RowIn in = {};
+    const RowList li{seqs, q_start, granted, nullptr, n, T};
+    bool none = false;
+    const int rc = check_append(cache, layer, Knew, Vnew, token_stride, head_stride, li, w, in, none);
+    if (rc != kOk || none) return rc;
+    if (w.bits == 4 && 2LL * w.heads > kMaxRows) return kErrUnsupported;
+    if (w.bits == 4) return launch_cache_rows_in(w, layer, in, li, Rotation{}, static_cast<cudaStream_t>(stream));
+    return launch_cache_append(w, layer, Knew, Vnew, in.token_bytes / 16, in.head_bytes / 16, T, seqs, q_start, granted, n,
                                static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_append_rotated(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew, long long token_stride,
+                              long long head_stride, const void *Q, void *Qout, int Hq, long long q_token_stride,
+                              long long q_head_stride, long long o_token_stride, long long o_head_stride, int T,
+                              const int *seqs, const int *q_start, const int *granted, int n,
+                              const attn_rotation_t *rotation, void *stream) {
+    CacheView w;
+    RowIn in = {};
+    const RowList li{seqs, q_start, granted, nullptr, n, T};
+    bool none = false;
+    const int rc = check_append(cache, layer, Knew, Vnew, token_stride, head_stride, li, w, in, none);
+    if (rc != kOk) return rc;
+    if (!rotation || rotation->rows <= 0 || rotation->dims < 2 || rotation->dims % 2 || rotation->dims > cache->d ||
+        (rotation->neighbours != 0 && rotation->neighbours != 1))
+        return kErrArg;
+    if (Hq < 0 || (Hq == 0 && (Q || Qout))) return kErrArg;
+    if (2LL * w.heads + Hq > kMaxRows) return kErrUnsupported;
+    if (T == 1) q_token_stride = o_token_stride = 0;
+    if (Hq <= 1) q_head_stride = o_head_stride = 0;
+    const long long es = w.bits == 32 ? 4 : 2, per = 16 / es;
+    if (Hq > 0) {
+        for (long long s : {q_token_stride, q_head_stride, o_token_stride, o_head_stride}) {
+            if (s < 0 || s % per) return kErrArg;
+            if (s >= (1LL << 38)) return kErrUnsupported;
+        }
+        if (T > 0 && !rows_apart(T, Hq, o_token_stride, o_head_stride, cache->d)) return kErrArg;
+        if (Q == Qout && (q_token_stride != o_token_stride || q_head_stride != o_head_stride)) return kErrArg;
+    }
+    if (none) return kOk;
+    if (!rotation->table || !aligned16(rotation->table) || !aligned4(rotation->positions)) return kErrArg;
+    if (Hq > 0 && (!Q || !Qout || !aligned16(Q) || !aligned16(Qout))) return kErrArg;
+    in.Q = static_cast<const char *>(Q);
+    in.Qout = static_cast<char *>(Qout);
+    in.q_token_bytes = q_token_stride * es;
+    in.q_head_bytes = q_head_stride * es;
+    in.o_token_bytes = o_token_stride * es;
+    in.o_head_bytes = o_head_stride * es;
+    in.Hq = Hq;
+    const Rotation r{rotation->table, rotation->positions, rotation->rows, rotation->dims, rotation->neighbours};
+    return launch_cache_rows_in(w, layer, in, li, r, static_cast<cudaStream_t>(stream));
+}
+
+int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout, long long token_stride, long long head_stride,
+                    int T, const int *seqs, const int *q_start, const int *first, int n, void *stream) {
+    CacheView w;
+    RowIn in = {};
+    const RowList li{seqs, q_start, nullptr, first, n, T};
+    bool none = false;
+    const int rc = check_append(cache, layer, Kout, Vout, token_stride, head_stride, li, w, in, none);
+    if (rc != kOk) return rc;
+    if (2LL * w.heads > kMaxRows) return kErrUnsupported;
+    const long long es = w.bits == 32 ? 4 : 2;
+    if (T > 0 && !rows_apart(T, w.heads, in.token_bytes / es, in.head_bytes / es, cache->d)) return kErrArg;
+    if (none) return kOk;
+    if (Kout == Vout || !aligned4(first)) return kErrArg;
+    const RowOut out{static_cast<char *>(Kout), static_cast<char *>(Vout), in.token_bytes, in.head_bytes, cache->d};
+    return launch_cache_rows_out(w, layer, out, li, static_cast<cudaStream_t>(stream));
 }
 
 size_t attn_paged_workspace_size(int Hq, int heads, int max_q, int d, int dtype) {
     if (Hq <= 0 || heads <= 0 || Hq % heads || Hq / heads > 64 || max_q <= 0 || d <= 0 || d > 128 || d % 32) return 0;
-    if (dtype != ATTN_F32 && dtype != ATTN_BF16) return 0;
-    return paged_workspace_bytes(Hq / heads, max_q, d, dtype == ATTN_BF16);
+    if (dtype != ATTN_F32 && dtype != ATTN_BF16 && dtype != ATTN_E2M1) return 0;
+    return paged_workspace_bytes(Hq / heads, max_q, d, dtype == ATTN_E2M1 ? 4 : dtype == ATTN_BF16 ? 16 : 32);
 }
 
 int attn_paged_fwd(const attn_cache_t *cache, int layer, const void *Q, void *O, float *LSE, long long q_token_stride,
@@ -577,8 +666,7 @@ int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, 
     if (!(scale > 0.f) || !std::isfinite(scale * kPagedLog2e)) return kErrArg;
     if (causal != 0 && causal != 1) return kErrArg;
     if (T > kMaxTokens || static_cast<long long>(T) * Hq >= (1LL << 31)) return kErrArg;
-    const int bf16 = cache->dtype == ATTN_BF16;
-    const long long per = bf16 ? 8 : 4;
+    const long long per = w.bits == 32 ? 4 : 8;
     // (the stride of a dimension of one element means nothing)
     if (T == 1) q_token_stride = o_token_stride = 0;
     if (Hq == 1) q_head_stride = o_head_stride = 0;
@@ -591,18 +679,15 @@ int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, 
     if (T == 0 || n == 0) return kOk;
     if (max_q <= 0 || max_q > T) return kErrArg;
     // rows of O must not overlap: one of the strides steps over all of the other's range
-    const long long ht = o_head_stride, tt = o_token_stride, d = cache->d;
-    const bool heads_in = (Hq == 1 || ht >= d) && (T == 1 || steps_over(tt, Hq, ht, d));
-    const bool tokens_in = (T == 1 || tt >= d) && (Hq == 1 || steps_over(ht, T, tt, d));
-    if (!heads_in && !tokens_in) return kErrArg;
+    if (!rows_apart(T, Hq, o_token_stride, o_head_stride, cache->d)) return kErrArg;
     if (!Q || !O || !q_start || !aligned16(Q) || !aligned16(O) || !aligned4(q_start) || !aligned4(seqs) || !aligned4(LSE) ||
         !aligned4(granted))
         return kErrArg;
-    rc = check_workspace(workspace, ws_bytes, paged_workspace_bytes(Hq / w.heads, max_q, cache->d, bf16));
+    rc = check_workspace(workspace, ws_bytes, paged_workspace_bytes(Hq / w.heads, max_q, cache->d, w.bits));
     if (rc != kOk) return rc;
     rc = check_device();
     if (rc != kOk) return rc;
-    const size_t es = bf16 ? 2 : 4;
+    const size_t es = w.bits == 4 ? 1 : w.bits / 8;
     PagedParams p = {};
     p.gm.page_table = w.page_table;
     p.gm.seq_lens = w.seq_lens;
@@ -637,7 +722,7 @@ int attn_paged_fwd_granted(const attn_cache_t *cache, int layer, const void *Q, 
     p.err = device_error_word();
     if (!p.err) return kErrCuda;
     const char *variant = "";
-    rc = launch_paged(p, bf16, workspace, static_cast<cudaStream_t>(stream), &variant);
+    rc = launch_paged(p, w.bits, workspace, static_cast<cudaStream_t>(stream), &variant);
     if (rc == kOk) t_last_variant = variant;
     return rc;
 }

@@ -448,7 +448,8 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const CacheVie
             atomicOr(err, kErrWordBadRow);
             src = -1;
         }
-        return Move{src, q.list[k], min(S, len - col * S)};
+        // (a block of 4-bit values is copied whole: its scales lie behind the codes)
+        return Move{src, q.list[k], c.bits == 4 ? S : min(S, len - col * S)};
     });
     pdl_done();
 }

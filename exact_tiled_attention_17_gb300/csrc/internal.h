@@ -94,8 +94,8 @@ constexpr int kPagedMaxTcCtas = 160;       // CTAs a launch may use (sizes the w
 constexpr int kPagedMaxDecodeCtas = 320;   // two,
 constexpr int kPagedMaxSimtCtas = 640;     // up to four
 struct PagedParams;
-size_t paged_workspace_bytes(int g, int max_q, int d, int bf16);
-int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant);
+size_t paged_workspace_bytes(int g, int max_q, int d, int bits);
+int launch_paged(const PagedParams &p, int bits, void *workspace, cudaStream_t stream, const char **variant);
 
 // A paged cache as the page kernels see it (cache.cu): strides in 16-byte pieces.
 struct CacheView {
@@ -106,6 +106,7 @@ struct CacheView {
     int block_vecs;   // a page of one layer
     int slot_vecs;    // distance of two slots of one head
     int row_vecs;     // one head's row of a slot
+    int bits;         // of a value: 32, 16, or 4 (a page is copied whole; slot_vecs, slot_stride_vecs and row_vecs mean nothing)
 };
 size_t cache_workspace_bytes(int pages, int n);
 int launch_cache_reserve(const CacheView &c, const int *seqs, const int *n_new, int n, int *granted, void *ws,
@@ -117,6 +118,32 @@ int launch_cache_compact(const CacheView &c, int *table_out, int *refs_out, int 
 int launch_cache_append(const CacheView &c, int layer, const void *Kn, const void *Vn, long long token_vecs,
                         long long head_vecs, int T, const int *seqs, const int *q_start, const int *granted, int n,
                         cudaStream_t stream);
+
+// Rows in and out of a cache (cache_rows.cu): rotated or 4-bit appends, and
+// reading.  Strides in bytes; rows of bf16 (caches of 16 or 4 bits) or float32.
+struct RowList {
+    const int *seqs, *q_start, *granted, *first;   // (granted, first: or null)
+    int n, T;
+};
+struct RowIn {
+    const char *K, *V, *Q;
+    char *Qout;
+    long long token_bytes, head_bytes, q_token_bytes, q_head_bytes, o_token_bytes, o_head_bytes;
+    int Hq, d;        // Hq 0: no queries
+    int lane_shift;   // (the launch sets it)
+};
+struct RowOut {
+    char *K, *V;
+    long long token_bytes, head_bytes;
+    int d;
+};
+struct Rotation {
+    const float *table;      // [rows][dims]: cosines, then sines
+    const int *positions;    // [T], or null: a token's index in its sequence
+    int rows, dims, neighbours;   // dims 0: no rotation
+};
+int launch_cache_rows_in(const CacheView &c, int layer, RowIn in, const RowList &li, const Rotation &r, cudaStream_t stream);
+int launch_cache_rows_out(const CacheView &c, int layer, const RowOut &out, const RowList &li, cudaStream_t stream);
 
 // FP32 backward on the CUDA cores (bwd_f32.cu); workspace: B*H*N floats.
 int launch_bwd_f32(const float *Q, const float *K, const float *V, const float *O, const float *dO, const float *LSE,

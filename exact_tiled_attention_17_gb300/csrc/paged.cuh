@@ -243,6 +243,7 @@ int launch_paged_few(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream);
+int launch_paged_e2m1(PagedParams p, void *workspace, cudaStream_t stream);
 
 // Tensor maps of the bf16 kernels: Q in boxes of `tokens` tokens x g heads x 64
 // columns (rows token by token), K and V in boxes of `box` slots x 64 columns of

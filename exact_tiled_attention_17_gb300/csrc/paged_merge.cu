@@ -312,23 +312,28 @@ namespace {
 // stream kernel took 38 us where the matrix kernel took 27 (16 x 1000 .. 4096).
 // float32: units of up to 8 rows are streamed through registers (32 x 8000 tokens,
 // d 128, 4 rows: 160 us, tiled 365; 16 rows, 16 x 4000: 161, tiled 106).
-enum class Path { kFew, kSimt, kDecode, kTc };
-Path path_of(int g, int max_q, int bf16) {
-    if (!bf16) return paged_simt_rows(g, max_q) <= 8 ? Path::kFew : Path::kSimt;
+enum class Path { kFew, kSimt, kDecode, kTc, kE2m1 };
+Path path_of(int g, int max_q, int bits) {
+    if (bits == 4) return Path::kE2m1;
+    if (bits == 32) return paged_simt_rows(g, max_q) <= 8 ? Path::kFew : Path::kSimt;
     return static_cast<long long>(g) * max_q <= 32 ? Path::kDecode : Path::kTc;
 }
 }  // namespace
 
-size_t paged_workspace_bytes(int g, int max_q, int d, int bf16) {
-    switch (path_of(g, max_q, bf16)) {
+size_t paged_workspace_bytes(int g, int max_q, int d, int bits) {
+    switch (path_of(g, max_q, bits)) {
+        case Path::kE2m1: return 16;
         case Path::kTc: return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
         case Path::kDecode: return paged_partial_bytes(kPagedMaxDecodeCtas, paged_decode_rows(g, max_q), d);
         default: return paged_partial_bytes(kPagedMaxSimtCtas, paged_simt_rows(g, max_q), d);
     }
 }
 
-int launch_paged(const PagedParams &p, int bf16, void *workspace, cudaStream_t stream, const char **variant) {
-    switch (path_of(p.gm.g, p.gm.max_q, bf16)) {
+int launch_paged(const PagedParams &p, int bits, void *workspace, cudaStream_t stream, const char **variant) {
+    switch (path_of(p.gm.g, p.gm.max_q, bits)) {
+        case Path::kE2m1:
+            if (variant) *variant = "paged_e2m1";
+            return launch_paged_e2m1(p, workspace, stream);
         case Path::kTc:
             if (variant) *variant = p.d <= 64 ? "paged_tc_bf16_d64" : "paged_tc_bf16_d128";
             return launch_paged_tc(p, workspace, stream);

@@ -60,7 +60,7 @@
 extern "C" {
 #endif
 
-typedef enum { ATTN_F32 = 0, ATTN_BF16 = 1, ATTN_F64 = 2 } attn_dtype_t;
+typedef enum { ATTN_F32 = 0, ATTN_BF16 = 1, ATTN_F64 = 2, ATTN_E2M1 = 3 /* caches only */ } attn_dtype_t;
 
 typedef enum {
     ATTN_OK = 0,
@@ -258,7 +258,7 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  *                token (slot_stride = heads * d, head_stride = d).  Blocks do
  *                not overlap.  Bases 16-byte aligned, strides multiples of 16
  *                bytes.
- *   dtype        ATTN_BF16 or ATTN_F32;  d in {32, 64, 96, 128};
+ *   dtype        ATTN_BF16, ATTN_F32 or ATTN_E2M1;  d in {32, 64, 96, 128};
  *   page_size    tokens to a page: 16, 32, 64, 128 or 256.
  *   page_table   [seqs][max_pages] int: the page of tokens page_size * k ..
  *                of each sequence, -1 where it has none; max_pages *
@@ -269,6 +269,23 @@ int attn_decode_fwd(const void *Q, const void *K, const void *V, void *O, float 
  * A new cache has page_table all -1, seq_lens and ref_counts 0.  Slots at and
  * past a sequence's length may hold anything, NaN included; what lies before
  * it must be finite.
+ *
+ * A cache of ATTN_E2M1 holds 4-bit values, 4.5 bits each with their scales; what
+ * goes in and out of it (new keys and values, queries, outputs) is bfloat16.
+ * Strides count bytes.  A page of one layer is, for each head, page_size * d / 2
+ * bytes of codes (slot by slot, two columns to a byte, the even one in the low four
+ * bits) and then page_size * d / 16 bytes of scales (slot by slot, one to 16
+ * columns): head_stride = page_size * 9 * d / 16, slot_stride = d / 2, head by head
+ * only.  A code is sign, two exponent bits and a fraction bit: 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6.  A scale has five exponent bits and three fraction bits: bits 14 .. 7 of a
+ * float16.  A value is code * scale, which float16 and bfloat16 hold exactly.  With
+ * amax the largest magnitude of 16 columns,
+ *     scale = amax / 6, rounded to nearest, ties to even, at most 10240
+ *             (below 2^-14 a multiple of 2^-17),
+ *     code  = x / scale, rounded to nearest, ties to even, at most 6,
+ * so a value is off by at most 0.18 amax + 2^-15 (amax up to 61440; more is cut to
+ * that); where all 16 are at most 6 * 2^-18 in magnitude they become 0.  A group
+ * with a NaN or an infinity becomes NaN.
  *
  * Lists (seqs, n_new, parents, ...) are int arrays in device memory, of at most
  * 2^20 entries, that overlap nothing a call writes.  Every decision is taken on the device: no
@@ -370,6 +387,55 @@ int attn_cache_append(const attn_cache_t *cache, int layer, const void *Knew, co
 int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew,
                               long long token_stride, long long head_stride, int T, const int *seqs, const int *q_start,
                               const int *granted, int n, void *stream);
+
+/*
+ * attn_cache_append_rotated — attn_cache_append_granted with the position rotation
+ * applied to the keys on the way, and to the queries of the same tokens: a pair of
+ * columns (a, b) of every row of Knew and Q becomes (a cos - b sin, b cos + a sin),
+ * Vnew goes as it is.  Products and sums are rounded to float32 one by one, the
+ * result once to the cache's type (to bfloat16, then no further, for the queries of
+ * an ATTN_E2M1 cache; keys go from float32 to 4 bits).
+ *
+ * rotation->table: [rows][dims] float32, 16-byte aligned, of each position first
+ * dims / 2 cosines and then as many sines (so any scaling of the angles is the
+ * caller's).  dims: columns that turn, even, at most d; the others go as they are.
+ * Pair i is columns i and i + dims / 2 (neighbours = 0) or 2 i and 2 i + 1
+ * (neighbours = 1).  A token's position is its index in its sequence, or
+ * positions[t] ([T] int).  A token whose position is not in 0 .. rows - 1 is left
+ * out (attn_status returns ATTN_ERR_ARG).
+ *
+ * Q: T rows of Hq heads as for attn_paged_fwd, of the cache's type (bfloat16 for
+ * ATTN_E2M1); Qout: where they go, either Q itself with the same strides, or memory
+ * that overlaps no input; rows of Qout do not overlap.  Queries of tokens that are
+ * not written are left as they were.  Hq = 0: keys and values only (Q, Qout NULL).
+ * 2 * heads + Hq at most 2^20.  dims that are multiples of 32 (neighbours: of 16)
+ * are fastest.  Asynchronous.
+ */
+typedef struct {
+    const float *table;
+    const int *positions;   /* or NULL */
+    int rows, dims, neighbours;
+} attn_rotation_t;
+int attn_cache_append_rotated(const attn_cache_t *cache, int layer, const void *Knew, const void *Vnew,
+                              long long token_stride, long long head_stride, const void *Q, void *Qout, int Hq,
+                              long long q_token_stride, long long q_head_stride, long long o_token_stride,
+                              long long o_head_stride, int T, const int *seqs, const int *q_start, const int *granted, int n,
+                              const attn_rotation_t *rotation, void *stream);
+
+/*
+ * attn_cache_read — copies tokens of one layer out of the cache.  Entry i of the
+ * list is sequence seqs[i] (NULL: sequence i); rows q_start[i] .. q_start[i+1] - 1 of
+ * Kout and Vout receive its tokens first[i], first[i] + 1, ... (first NULL: its last
+ * tokens).  Rows are of the cache's type, of an ATTN_E2M1 cache bfloat16 (exact).
+ * Kout, Vout: strides as for attn_cache_append; their rows do not overlap.  A
+ * sequence may be named more than once.  Rows of tokens that the sequence does not
+ * have, or whose page the table does not name, are left as they were, and
+ * attn_status returns ATTN_ERR_ARG; so are rows outside q_start[0] .. q_start[n] - 1.
+ * 2 * heads at most 2^20.  Asynchronous.
+ */
+int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout, long long token_stride,
+                    long long head_stride, int T, const int *seqs, const int *q_start, const int *first, int n,
+                    void *stream);
 
 /*
  * attn_paged_fwd — attention of new tokens over one layer of a paged cache.
