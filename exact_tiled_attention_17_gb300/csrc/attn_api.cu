@@ -480,6 +480,9 @@ int check_append(const attn_cache_t *cache, int layer, const void *K, const void
     if (w.heads == 1) head_stride = 0;
     const long long es = w.bits == 32 ? 4 : 2, per = 16 / es;
     if (token_stride < 0 || head_stride < 0 || token_stride % per || head_stride % per) return kErrArg;
+    in.token_bytes = token_stride * es;
+    in.head_bytes = head_stride * es;
+    in.d = cache->d;
     none = li.n == 0 || li.T == 0;
     if (none) return kOk;
     if (!K || !V || !li.q_start || !aligned16(K) || !aligned16(V) || !aligned4(li.q_start) || !aligned4(li.seqs) ||
@@ -487,9 +490,6 @@ int check_append(const attn_cache_t *cache, int layer, const void *K, const void
         return kErrArg;
     in.K = static_cast<const char *>(K);
     in.V = static_cast<const char *>(V);
-    in.token_bytes = token_stride * es;
-    in.head_bytes = head_stride * es;
-    in.d = cache->d;
     return kOk;
 }
 constexpr long long kMaxRows = 1LL << 20;   // rows of a token (K, V and Q) in the calls that count them in 32 bits
