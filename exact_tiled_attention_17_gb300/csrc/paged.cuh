@@ -233,6 +233,7 @@ int launch_paged_merge(const PagedParams &p, int bf16, int ctas, int sms, cudaSt
 // whichever holds an entry.  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
 // the one that tiles).
 inline int paged_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 16 ? 16 : 32; }
+inline int paged4_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 8 ? 8 : 16; }
 inline int paged_simt_rows(int g, int max_q) {
     const long long rows = static_cast<long long>(g) * max_q;
     return rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -244,11 +245,17 @@ int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_e2m1(PagedParams p, void *workspace, cudaStream_t stream);
+int launch_paged4_decode(PagedParams p, void *workspace, cudaStream_t stream);
 
 // Tensor maps of the bf16 kernels: Q in boxes of `tokens` tokens x g heads x 64
 // columns (rows token by token), K and V in boxes of `box` slots x 64 columns of
 // one page and head.
 bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
+
+// Tensor maps of the 4-bit stream kernel: Q as above but rows whole and in their own
+// order, codes of K and V in boxes of `box` slots of one page and head (rows of 64
+// bytes swizzled within 64 bytes).
+bool paged4_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
 
 // Workspace: headers, m, l, o for `ctas` CTAs and units of `rows` rows.
 inline size_t paged_partial_bytes(int ctas, int rows, int d) {
