@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libattn.so")
 
 SOURCES = ["attn_api.cu", "fwd_tc.cu", "fwd_f32.cu", "naive.cu", "deviation.cu", "emul.cu", "decode.cu", "bwd_tc.cu", "bwd_f32.cu",
            "cache.cu", "paged_merge.cu", "paged_simt.cu", "paged_tc.cu", "paged_decode.cu", "paged_few.cu",
-           "cache_rows.cu", "paged_e2m1.cu", "paged4_decode.cu"]
+           "cache_rows.cu", "paged4_decode.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("ptx.cuh", "internal.h", "paged.cuh", "paged_index.h", "launch.cuh", "e2m1.cuh")] + [os.path.join(INCLUDE, "attn.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -244,18 +244,18 @@ int launch_paged_few(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_simt(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged_decode(PagedParams p, void *workspace, cudaStream_t stream);
-int launch_paged_e2m1(PagedParams p, void *workspace, cudaStream_t stream);
 int launch_paged4_decode(PagedParams p, void *workspace, cudaStream_t stream);
+int launch_paged4_tc(PagedParams p, void *workspace, cudaStream_t stream);
 
 // Tensor maps of the bf16 kernels: Q in boxes of `tokens` tokens x g heads x 64
 // columns (rows token by token), K and V in boxes of `box` slots x 64 columns of
 // one page and head.
 bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
 
-// Tensor maps of the 4-bit stream kernel: Q as above but rows whole and in their own
-// order, codes of K and V in boxes of `box` slots of one page and head (rows of 64
+// Tensor maps for 4-bit values: Q as above (tc), or with whole rows in their own
+// order; codes of K and V in boxes of `box` slots of one page and head (rows of 64
 // bytes swizzled within 64 bytes).
-bool paged4_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
+bool paged4_maps(const PagedParams &p, int tokens, int box, bool tc, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
 
 // Workspace: headers, m, l, o for `ctas` CTAs and units of `rows` rows.
 inline size_t paged_partial_bytes(int ctas, int rows, int d) {

@@ -90,12 +90,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
     paged4_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
@@ -268,13 +262,13 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                     }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int up = top == 0u ? 0 : min(14 + 127 - static_cast<int>(top >> 23), 126);
+                const int up = f16_shift(top);
                 const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
                 const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) qf[nt][k][e] = pack_h2(bf16lo_to_f32(x[k][e]) * f, bf16hi_to_f32(x[k][e]) * f);
+                    for (int e = 0; e < 2; ++e) qf[nt][k][e] = pack_f16x2(bf16lo_to_f32(x[k][e]) * f, bf16hi_to_f32(x[k][e]) * f);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) mult[nt][i] = __shfl_sync(0xffffffffu, back, (2 * c + i) * 4);
             }
@@ -406,7 +400,7 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                             const float p0 = ex2(s[nt][0][2 * h] - mu[nt][0]), p1 = ex2(s[nt][0][2 * h + 1] - mu[nt][1]);
                             l[nt][0] += p0;
                             l[nt][1] += p1;
-                            pf[nt][h] = transpose8(pack_h2(p0, p1));
+                            pf[nt][h] = transpose8(pack_f16x2(p0, p1));
                         }
                     // ---------------- O^T += V^T P^T ----------------
                     const uint8_t *vt = tile + S::OFF_V + step * (16 * S::CB), *vst = tile + S::OFF_V + S::OFF_KS + step * (16 * S::SB);
@@ -551,7 +545,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.min_share = S::KEYS;
     paged_derive(p.gm);
     CUtensorMap tq, kc, vc;
-    if (!paged4_maps(p, p.gm.tpu, std::min(p.gm.page_size, S::KEYS), &tq, &kc, &vc)) return kErrCuda;
+    if (!paged4_maps(p, p.gm.tpu, std::min(p.gm.page_size, S::KEYS), false, &tq, &kc, &vc)) return kErrCuda;
     paged_carve(p, workspace, grid, S::ROWS);
     const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, stream, tq, kc, vc, p);
     if (rc != kOk) return rc;

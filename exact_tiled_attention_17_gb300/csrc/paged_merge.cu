@@ -304,18 +304,18 @@ bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUte
            make_bf16_map(tv, p.V, 4, kd, ks, kb);
 }
 
-bool paged4_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv) {
+bool paged4_maps(const PagedParams &p, int tokens, int box, bool tc, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv) {
     const PagedGeom &gm = p.gm;
     const cuuint64_t qd[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(gm.T)};
     const cuuint64_t qs[2] = {static_cast<cuuint64_t>(p.q_head) * 2, static_cast<cuuint64_t>(p.q_token) * 2};
-    const cuuint32_t qb[3] = {static_cast<cuuint32_t>(p.d), static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t qb[3] = {tc ? 64u : static_cast<cuuint32_t>(p.d), static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tokens)};
     const cuuint64_t kd[4] = {static_cast<cuuint64_t>(p.d / 2), static_cast<cuuint64_t>(gm.page_size),
                               static_cast<cuuint64_t>(gm.heads), static_cast<cuuint64_t>(gm.pages)};
     const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.d / 2), static_cast<cuuint64_t>(p.head_stride),
                               static_cast<cuuint64_t>(p.page_stride)};
     const cuuint32_t kb[4] = {static_cast<cuuint32_t>(p.d / 2), static_cast<cuuint32_t>(box), 1u, 1u};
     const auto sw = p.d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    return make_map(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_NONE, p.Q, 3, qd, qs, qb) &&
+    return make_map(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, tc ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, p.Q, 3, qd, qs, qb) &&
            make_map(tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.K, 4, kd, ks, kb) &&
            make_map(tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.V, 4, kd, ks, kb);
 }
@@ -328,9 +328,9 @@ namespace {
 // stream kernel took 38 us where the matrix kernel took 27 (16 x 1000 .. 4096).
 // float32: units of up to 8 rows are streamed through registers (32 x 8000 tokens,
 // d 128, 4 rows: 160 us, tiled 365; 16 rows, 16 x 4000: 161, tiled 106).
-enum class Path { kFew, kSimt, kDecode, kTc, kE2m1, kDecode4 };
+enum class Path { kFew, kSimt, kDecode, kTc, kDecode4, kTc4 };
 Path path_of(int g, int max_q, int bits) {
-    if (bits == 4) return static_cast<long long>(g) * max_q <= 16 ? Path::kDecode4 : Path::kE2m1;
+    if (bits == 4) return static_cast<long long>(g) * max_q <= 16 ? Path::kDecode4 : Path::kTc4;
     if (bits == 32) return paged_simt_rows(g, max_q) <= 8 ? Path::kFew : Path::kSimt;
     return static_cast<long long>(g) * max_q <= 32 ? Path::kDecode : Path::kTc;
 }
@@ -338,8 +338,8 @@ Path path_of(int g, int max_q, int bits) {
 
 size_t paged_workspace_bytes(int g, int max_q, int d, int bits) {
     switch (path_of(g, max_q, bits)) {
-        case Path::kE2m1: return 16;
         case Path::kDecode4: return paged_partial_bytes(kPagedMaxDecodeCtas, paged4_decode_rows(g, max_q), d);
+        case Path::kTc4:
         case Path::kTc: return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
         case Path::kDecode: return paged_partial_bytes(kPagedMaxDecodeCtas, paged_decode_rows(g, max_q), d);
         default: return paged_partial_bytes(kPagedMaxSimtCtas, paged_simt_rows(g, max_q), d);
@@ -351,9 +351,9 @@ int launch_paged(const PagedParams &p, int bits, void *workspace, cudaStream_t s
         case Path::kDecode4:
             if (variant) *variant = "paged_decode_e2m1";
             return launch_paged4_decode(p, workspace, stream);
-        case Path::kE2m1:
-            if (variant) *variant = "paged_e2m1";
-            return launch_paged_e2m1(p, workspace, stream);
+        case Path::kTc4:
+            if (variant) *variant = "paged_tc_e2m1";
+            return launch_paged4_tc(p, workspace, stream);
         case Path::kTc:
             if (variant) *variant = p.d <= 64 ? "paged_tc_bf16_d64" : "paged_tc_bf16_d128";
             return launch_paged_tc(p, workspace, stream);

@@ -43,6 +43,7 @@
 #include <mutex>
 #include <type_traits>
 
+#include "e2m1.cuh"
 #include "launch.cuh"
 #include "paged.cuh"
 
@@ -52,19 +53,25 @@ namespace {
 constexpr float kThresh = 8.0f;   // the reference maximum moves by at least this (log2 units)
 constexpr float kNegInfP = -__builtin_huge_valf();
 
-template <int DP>   // padded head dimension: 64 or 128
+template <int DP, bool Q4>   // padded head dimension: 64 or 128; whether the cache holds 4-bit values
 struct PtcShape {
     static constexpr int NQ = 2, BR = 128, BC = 128;
     static constexpr int CB = DP / 64;
     static constexpr int Q_BYTES = BR * DP * 2;
     static constexpr int SLOT_BYTES = BC * DP * 2;
     static constexpr int XCH_BYTES = NQ * 2 * 128 * 8;
-    static constexpr int NS_RAW = (222 * 1024 - NQ * Q_BYTES - XCH_BYTES) / SLOT_BYTES;
+    // 4-bit tiles as they come: codes, then scales
+    static constexpr int STG_BYTES = Q4 ? BC * (DP / 2 + DP / 16) : 0, NG = Q4 ? (DP == 128 ? 3 : 4) : 0;
+    static constexpr int EXP_BYTES = Q4 ? 2 * NQ * BR : 0;        // [2 units][row]: power of two that a row of Q was multiplied by
+    static constexpr int NS_RAW = ((Q4 ? 224 : 222) * 1024 - NQ * Q_BYTES - XCH_BYTES - NG * STG_BYTES - EXP_BYTES) / SLOT_BYTES;
     static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
     static constexpr int SOFTMAX_WARPS = 16, WARP_MMA = 17, WARP_TMV = 18;   // (warp 16: Q, K and the work)
-    static constexpr int THREADS = 19 * 32;
+    static constexpr int CONV_WARPS = Q4 ? 4 : 0;                            // from WARP_TMV on, which Q4 has not
+    static constexpr int THREADS = (Q4 ? WARP_TMV + CONV_WARPS : WARP_TMV + 1) * 32;
     static constexpr int OFF_RING = NQ * Q_BYTES;
-    static constexpr int OFF_XCH = OFF_RING + NS * SLOT_BYTES;
+    static constexpr int OFF_STG = OFF_RING + NS * SLOT_BYTES;
+    static constexpr int OFF_EXP = OFF_STG + NG * STG_BYTES;
+    static constexpr int OFF_XCH = OFF_EXP + EXP_BYTES;
     static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
     static constexpr int BAR_QFULL = 0;
     static constexpr int BAR_FULL = BAR_QFULL + NQ;
@@ -79,7 +86,10 @@ struct PtcShape {
     static constexpr int UB = 4;                                  // units announced ahead
     static constexpr int BAR_UFULL = BAR_TAIL + 1;
     static constexpr int BAR_UEMPTY = BAR_UFULL + UB;
-    static constexpr int NBARS = (BAR_UEMPTY + UB + 1) / 2 * 2;
+    static constexpr int BAR_GFULL = BAR_UEMPTY + UB;             // 4-bit tiles
+    static constexpr int BAR_GEMPTY = BAR_GFULL + NG;
+    static constexpr int BAR_QREADY = BAR_GEMPTY + NG;            // Q is float16
+    static constexpr int NBARS = (BAR_QREADY + (Q4 ? NQ : 0) + 1) / 2 * 2;
     static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;          // tensor-memory address, abort flag
     static constexpr int OFF_BADP = OFF_MISC + 16;                // per K tile (mod 8): missing pages, bit per 16 keys
     static constexpr int OFF_UNIT = OFF_BADP + 32;                // [UB]
@@ -89,9 +99,118 @@ struct PtcShape {
     __host__ __device__ static constexpr int s_col(int q) { return q * BC; }
     __host__ __device__ static constexpr int o_col(int q) { return NQ * BC + q * DP; }
     static_assert(NS >= 4 && SMEM_BYTES <= 227 * 1024, "shared memory");
+    static_assert(OFF_STG % 512 == 0 && STG_BYTES % 512 == 0, "the period of the codes' swizzle");
     static_assert(NQ * (BC + DP) <= 512, "tensor memory");
     static_assert(OFF_UNIT % 16 == 0, "alignment");
 };
+
+// Missing pages of a tile, one bit for each 16 keys.  missing: a bit for each box, `cols` lanes apart.
+__device__ __forceinline__ uint32_t page_bits(uint32_t missing, int boxes, int box_rows, int cols, int *err) {
+    uint32_t bits = 0;
+    if (missing) {
+        atomicOr(err, kErrWordBadRow);
+        for (int b = 0; b < boxes; ++b)
+            if ((missing >> (b * cols)) & 1u) bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
+    }
+    return bits;
+}
+
+// What the converting warps do (4-bit values): Q of a unit to float16, then each
+// tile of K and V from codes and scales to the float16 tile that the matrix
+// instruction reads (rows of 128 bytes, swizzled as a copy would leave them).  A
+// thread takes a row of Q, or a key: its scales and codes in 16-byte pieces (d 128:
+// swizzled within 64 bytes, so that 8 keys' pieces lie in different banks).  Slots
+// past the end, and of pages that do not exist, become zeros.
+template <int DP, typename UnitWait, typename UnitDone, typename Wait>
+__device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedGeom &gm, uint32_t sbase, uint8_t *smem,
+                                              const PagedUnit *units, volatile uint32_t *bad_pages, int conv_warp, int tpt,
+                                              const UnitWait &unit_wait, const UnitDone &unit_done, const Wait &wwait) {
+    using S = PtcShape<DP, true>;
+    auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
+    const int lane = threadIdx.x & 31, row = conv_warp * 32 + lane;
+    const int pieces = p.d / 32;   // of 16 bytes: 32 columns
+    const int swz = p.d == 128 ? (row >> 1) & 3 : 0;
+    auto signal = [&](int b) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+    };
+    int uo[S::NQ] = {0, 0}, kt = 0;
+    for (int u = 0;; ++u) {
+        if (!__all_sync(0xffffffffu, unit_wait(u, 72))) return;
+        const PagedUnit *w = units + u % S::UB;
+        const int tiles = w->tiles, tile0 = w->tile0, len = w->len;
+        int own[S::NQ];
+#pragma unroll
+        for (int q = 0; q < S::NQ; ++q) own[q] = w->own[q];
+        unit_done(u);
+        if (tiles == 0) return;
+#pragma unroll
+        for (int q = 0; q < S::NQ; ++q) {
+            if (own[q] == 0) continue;
+            if (!wwait(bar(S::BAR_QFULL + q), uo[q] & 1, 73)) return;
+            ++uo[q];
+            uint8_t *at = smem + q * S::Q_BYTES + row * 128;
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int i = 0; i < 8 * S::CB; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(at + (i >> 3) * (S::BR * 128) + (((i & 7) ^ (row & 7)) << 4));
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+            }
+            const int up = f16_shift(top);
+            const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll 4
+            for (int i = 0; i < 8 * S::CB; ++i) {
+                uint4 *to = reinterpret_cast<uint4 *>(at + (i >> 3) * (S::BR * 128) + (((i & 7) ^ (row & 7)) << 4));
+                const uint4 v = *to;
+                *to = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f),
+                                 pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
+                                 pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f),
+                                 pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
+            }
+            smem[S::OFF_EXP + (u & 1) * (S::NQ * S::BR) + q * S::BR + row] = static_cast<uint8_t>(static_cast<int8_t>(up));
+            fence_proxy_async_smem();
+            signal(S::BAR_QREADY + q);
+        }
+        for (int j = 0; j < tiles; ++j, ++kt) {
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                const int g = 2 * kt + v, st = g % S::NG, slot = g % S::NS;
+                if (!wwait(bar(S::BAR_GFULL + st), (g / S::NG) & 1, 74)) return;
+                const uint8_t *src = smem + S::OFF_STG + st * S::STG_BYTES;
+                const uint8_t *scales = src + S::BC * (p.d / 2) + row * (p.d / 16);
+                uint4 codes[DP / 32];
+                uint32_t sc[DP / 32];   // two bytes to a piece
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    if (i >= pieces) break;
+                    codes[i] = *reinterpret_cast<const uint4 *>(src + row * (p.d / 2) + ((i ^ swz) << 4));
+                    sc[i] = *reinterpret_cast<const uint16_t *>(scales + 2 * i);
+                }
+                const bool gone = (tile0 + j) * S::BC + row >= len || ((bad_pages[kt & 7] >> (row >> 4)) & 1u);
+                signal(S::BAR_GEMPTY + st);   // (what the tile held is in registers)
+                if (g >= S::NS && !wwait(bar(S::BAR_EMPTY + slot), (g / S::NS - 1) & 1, 75)) return;
+                uint8_t *to = smem + S::OFF_RING + slot * S::SLOT_BYTES + row * 128;
+#pragma unroll
+                for (int i = 0; i < DP / 32; ++i) {
+                    if (i >= pieces) break;
+                    const uint32_t c[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t h[4];
+                        e2m1_values(c[e], gone ? 0u : e2m1_scale_h2(e < 2 ? sc[i] & 0xffu : sc[i] >> 8), h);
+                        const int chunk = 4 * i + e;   // of 8 columns
+                        *reinterpret_cast<uint4 *>(to + (chunk >> 3) * (S::BC * 128) + (((chunk & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                signal(S::BAR_FULL + slot);
+            }
+        }
+    }
+}
 
 // N words to 16-byte aligned memory, 32 bytes at a time where that is aligned.
 template <int N>
@@ -112,11 +231,11 @@ __device__ __forceinline__ void store_words(void *dst, const uint32_t *r) {
     }
 }
 
-template <int DP>
-__global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
+template <int DP, bool Q4>
+__global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
-    using S = PtcShape<DP>;
+    using S = PtcShape<DP, Q4>;
     constexpr int NQ = S::NQ, BC = S::BC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -141,14 +260,21 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             mbar_init(bar(S::BAR_OFREE + q), 256);
         }
         for (int s = 0; s < S::NS; ++s) {
-            mbar_init(bar(S::BAR_FULL + s), 1);
+            mbar_init(bar(S::BAR_FULL + s), Q4 ? S::CONV_WARPS : 1);
             mbar_init(bar(S::BAR_EMPTY + s), 1);
+        }
+        if constexpr (Q4) {
+            for (int g = 0; g < S::NG; ++g) {
+                mbar_init(bar(S::BAR_GFULL + g), 1);
+                mbar_init(bar(S::BAR_GEMPTY + g), S::CONV_WARPS);
+            }
+            for (int q = 0; q < NQ; ++q) mbar_init(bar(S::BAR_QREADY + q), S::CONV_WARPS);
         }
         mbar_init(bar(S::BAR_DONE), 1);
         mbar_init(bar(S::BAR_TAIL), 1);
         for (int u = 0; u < S::UB; ++u) {
             mbar_init(bar(S::BAR_UFULL + u), 1);
-            mbar_init(bar(S::BAR_UEMPTY + u), S::SOFTMAX_WARPS + 2);
+            mbar_init(bar(S::BAR_UEMPTY + u), S::SOFTMAX_WARPS + 1 + (Q4 ? S::CONV_WARPS : 1));
         }
         *abort_flag = 0u;
         fence_mbar_init();
@@ -179,21 +305,27 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
         const bool leader = elect_one();
-        if (warp != S::WARP_MMA) {
+        if (Q4 && warp >= S::WARP_TMV) {
+            convert_tiles<DP>(p, gm, sbase, smem, units, bad_pages, warp - S::WARP_TMV, tpt, unit_wait, unit_done, wwait);
+        } else if (warp != S::WARP_MMA) {
             // --------------------------------------------------------------
             // TMA producers.  Lane b * CB + c copies box b (box_rows keys),
             // column block c, of a tile; tile i of K is the ring's tile 2 i, of V
             // 2 i + 1.
+            // 4-bit values: lane 2 b copies the codes of box b, lane 2 b + 1 the scales,
+            // of K and then of V; the converting warps make the ring's tiles of them.
             // --------------------------------------------------------------
-            const bool is_v = warp == S::WARP_TMV;
+            const bool is_v = !Q4 && warp == S::WARP_TMV;
             const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
             if (leader) {
                 if (!is_v) tma_prefetch_desc(&tm_q);
                 tma_prefetch_desc(tm);
+                if (Q4) tma_prefetch_desc(&tm_v);
             }
+            constexpr int COLS = Q4 ? 2 : S::CB;   // lanes to a box
             const int box_rows = min(gm.page_size, BC);
             const int boxes = BC / box_rows;
-            const int my_box = lane / S::CB, my_cb = lane % S::CB;
+            const int my_box = lane / COLS, my_cb = lane % COLS;
             const bool mine = my_box < boxes;
             const uint32_t dst = my_cb * (BC * 128) + my_box * box_rows * 128;
             const uint64_t pol_q = l2_policy_evict_first();
@@ -260,7 +392,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     n2 = n3;
                     n3 = lookup(j + 4);
                     const int t = 2 * kt + (is_v ? 1 : 0), slot = t % S::NS, round = t / S::NS;
-                    if (round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, is_v ? 19 : 1)) {
+                    if (!Q4 && round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, is_v ? 19 : 1)) {
                         ok = false;
                         break;
                     }
@@ -270,17 +402,39 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                     const bool tail = is_v && clear0 > 0 && clear0 < BC && clear1 > clear0;
                     const uint32_t full = bar(tail ? S::BAR_TAIL : S::BAR_FULL + slot);
                     const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
+                    if constexpr (Q4) {
+                        // (boxes without a page are not copied: their values are made zeros)
+                        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0 && my_cb == 0);
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const int g = 2 * kt + v, st = g % S::NG;
+                            if (g >= S::NG && !wwait(bar(S::BAR_GEMPTY + st), (g / S::NG - 1) & 1, 70)) {
+                                ok = false;
+                                break;
+                            }
+                            if (lane == 0) {
+                                if (v == 0) bad_pages[kt & 7] = page_bits(missing, boxes, box_rows, COLS, p.err);
+                                mbar_arrive_expect_tx(bar(S::BAR_GFULL + st), __popc(there) * box_rows * (p.d / 2 + p.d / 16));
+                            }
+                            __syncwarp();
+                            if (id >= 0) {
+                                const int slot_in = (j * BC + my_box * box_rows) & (gm.page_size - 1);
+                                const uint32_t to = sbase + S::OFF_STG + st * S::STG_BYTES;
+                                if (my_cb == 0)
+                                    tma_load_4d(to + my_box * box_rows * (p.d / 2), v ? &tm_v : &tm_k, bar(S::BAR_GFULL + st), 0, slot_in, w.head, id);
+                                else
+                                    bulk_load(to + BC * (p.d / 2) + my_box * box_rows * (p.d / 16),
+                                              static_cast<const char *>(v ? p.V : p.K) + id * p.page_stride + w.head * p.head_stride +
+                                                  gm.page_size * (p.d / 2) + slot_in * (p.d / 16),
+                                              box_rows * (p.d / 16), bar(S::BAR_GFULL + st), pol_q);
+                            }
+                        }
+                        if (!ok) break;
+                        continue;
+                    }
                     if (leader) {
                         if (!is_v) {
-                            // one bit for each 16 keys
-                            uint32_t bits = 0;
-                            if (missing) {
-                                atomicOr(p.err, kErrWordBadRow);
-                                for (int b = 0; b < boxes; ++b)
-                                    if ((missing >> (b * S::CB)) & 1u)
-                                        bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
-                            }
-                            bad_pages[kt & 7] = bits;
+                            bad_pages[kt & 7] = page_bits(missing, boxes, box_rows, S::CB, p.err);
                         }
                         mbar_arrive_expect_tx(full, S::SLOT_BYTES);
                     }
@@ -307,9 +461,13 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             }
             if (!is_v) feed.finish(p, cta);
             // every copy this warp started has landed before the CTA may exit
-            for (int i = max(0, kt - (S::NS + 1) / 2); i < kt; ++i) {
-                const int t = 2 * i + (is_v ? 1 : 0);
-                if (t + S::NS >= 2 * kt) wwait(bar(S::BAR_FULL + t % S::NS), (t / S::NS) & 1, 2);
+            if constexpr (Q4) {
+                for (int g = max(0, 2 * kt - S::NG); g < 2 * kt; ++g) wwait(bar(S::BAR_GFULL + g % S::NG), (g / S::NG) & 1, 71);
+            } else {
+                for (int i = max(0, kt - (S::NS + 1) / 2); i < kt; ++i) {
+                    const int t = 2 * i + (is_v ? 1 : 0);
+                    if (t + S::NS >= 2 * kt) wwait(bar(S::BAR_FULL + t % S::NS), (t / S::NS) & 1, 2);
+                }
             }
             if (!is_v) {
 #pragma unroll
@@ -322,8 +480,8 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             // MMA issuer (one elected lane); the order of the contiguous
             // forward: P_0 V_j, S_0(j+1), P_1 V_j, S_1(j+1).
             // --------------------------------------------------------------
-            constexpr uint32_t idesc_s = idesc_bf16_f32(128, BC, false, false);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(128, DP, false, true);
+            constexpr uint32_t idesc_s = Q4 ? idesc_f16_f32(128, BC, false, false) : idesc_bf16_f32(128, BC, false, false);
+            constexpr uint32_t idesc_o = Q4 ? idesc_f16_f32(128, DP, false, true) : idesc_bf16_f32(128, DP, false, true);
             const uint64_t qdesc0 = sdesc_sw128(sQ, 16, 1024);
             const uint64_t kdesc0 = sdesc_sw128(sRing, 16, 1024);
             const uint64_t vdesc0 = sdesc_sw128(sRing, BC * 128, 1024);
@@ -345,7 +503,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 unit_done(u);
 #pragma unroll
                 for (int q = 0; q < NQ; ++q)
-                    if (ok && nkv[q] > 0) ok = wwait(bar(S::BAR_QFULL + q), uo[q] & 1, 10);
+                    if (ok && nkv[q] > 0) ok = wwait(bar((Q4 ? S::BAR_QREADY : S::BAR_QFULL) + q), uo[q] & 1, 10);
                 if (!ok) break;
                 auto full_wait = [&](int tt, int site) -> bool {
                     const int tg = t_base + tt;
@@ -443,7 +601,9 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
         const uint32_t t_lane = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + t_lane + S::s_col(q);
         const uint32_t tO = tmem + t_lane + S::o_col(q);
-        const float sl2 = p.scale_log2;
+        float sl2 = p.scale_log2;   // (4-bit values: of the unit, by the power of two in this row of Q)
+        // weights are 2^(score - m + UP): float16 has fewer exponents than bf16 (UP + kThresh: at most 2^15)
+        constexpr float UP = Q4 ? 7.f : 0.f;
         constexpr int OC = DP / 64;   // 32-column chunks of O of this warpgroup
         // this row's token within the unit, or one that no unit has (g need not divide 128)
         auto token_in = [&]() { return row_in < tpt * gm.g ? q * tpt + paged_token(gm, row_in) : 256; };
@@ -469,6 +629,11 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             for (int j = 0; j < nkvq; ++j) {
                 if (!mbar_wait(bar(S::BAR_SFULL + q), (sq + j) & 1, abort_flag, p.err, 20)) ok = false;
                 tc_fence_after();
+                if constexpr (Q4) {
+                    if (j == 0)
+                        sl2 = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(
+                                  127 - static_cast<int8_t>(smem[S::OFF_EXP + (u & 1) * (NQ * S::BR) + q * S::BR + row_in])) << 23);
+                }
                 const bool edge = j >= inner || bad_pages[(kt + j) & 7] != 0u;
                 uint32_t sr[2][32];
                 float mxc[2], mx = kNegInfP;
@@ -512,7 +677,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                 const float a = moved ? ex2(m - m_new) : 1.f;
                 m = m_new;
                 const float m_use = (m == kNegInfP) ? 0.f : m;
-                const uint64_t negm2 = f2_pack(-m_use, -m_use);
+                const uint64_t negm2 = f2_pack(UP - m_use, UP - m_use);
                 uint64_t ls2 = f2_pack(0.f, 0.f);
                 auto exps = [&](auto edge_c) {
                     constexpr bool EDGE = decltype(edge_c)::value;
@@ -529,7 +694,7 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
                             float y0, y1;
                             f2_unpack(y, y0, y1);
                             const float p0 = ex2(y0), p1 = ex2(y1);
-                            pk[e] = pack_bf16x2(p0, p1);
+                            pk[e] = Q4 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
                             ls2 = f2_add(ls2, f2_pack(p0, p1));
                         }
                         tmem_st16(tS + h * 64 + 16 * c, pk);
@@ -608,9 +773,9 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
             }
             if (h == 0 && store) {
                 if (whole) {
-                    if (p.LSE) p.LSE[tok * p.Hq + head] = any ? (m + log2f(l)) * kPagedLn2 : kNegInfP;
+                    if (p.LSE) p.LSE[tok * p.Hq + head] = any ? ((m - UP) + log2f(l)) * kPagedLn2 : kNegInfP;
                 } else {
-                    p.part_m[prow] = nkvq > 0 ? paged_part_max(m, l) : kNegInfP;
+                    p.part_m[prow] = nkvq > 0 ? paged_part_max(m - UP, l) : kNegInfP;
                     p.part_l[prow] = l;
                 }
             }
@@ -631,10 +796,10 @@ __global__ void __launch_bounds__(PtcShape<DP>::THREADS, 1)
 constexpr int kMaxDev = 64;
 std::mutex g_mu;
 
-template <int DP>
+template <int DP, bool Q4>
 int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
-    using S = PtcShape<DP>;
-    auto kern = paged_tc_kernel<DP>;
+    using S = PtcShape<DP, Q4>;
+    auto kern = paged_tc_kernel<DP, Q4>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return kErrCuda;
     static std::atomic<int> sms[kMaxDev];   // 0: not set up yet
@@ -649,7 +814,8 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     const PagedGeom &gm = p.gm;
     const int tpt = 128 / gm.g;
     CUtensorMap tq, tk, tv;
-    if (!paged_maps(p, tpt, std::min(gm.page_size, S::BC), &tq, &tk, &tv)) return kErrCuda;
+    const int box = std::min(gm.page_size, S::BC);
+    if (!(Q4 ? paged4_maps(p, tpt, box, true, &tq, &tk, &tv) : paged_maps(p, tpt, box, &tq, &tk, &tv))) return kErrCuda;
     const int ctas = std::min(nsm, kPagedMaxTcCtas);
     p.gm.tpu = S::NQ * tpt;
     p.gm.tk = S::BC;
@@ -665,7 +831,10 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
 }  // namespace
 
 int launch_paged_tc(PagedParams p, void *workspace, cudaStream_t stream) {
-    return p.d <= 64 ? launch_dp<64>(p, workspace, stream) : launch_dp<128>(p, workspace, stream);
+    return p.d <= 64 ? launch_dp<64, false>(p, workspace, stream) : launch_dp<128, false>(p, workspace, stream);
+}
+int launch_paged4_tc(PagedParams p, void *workspace, cudaStream_t stream) {
+    return p.d <= 64 ? launch_dp<64, true>(p, workspace, stream) : launch_dp<128, true>(p, workspace, stream);
 }
 
 }  // namespace eta

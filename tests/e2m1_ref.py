@@ -6,6 +6,8 @@ from types import SimpleNamespace
 
 import torch
 
+from paged_ref import attention, gather
+
 STEPS = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
 # every finite scale that is written, by its byte: bits 14 .. 7 of a float16, up to 10240
 SCALES = (torch.arange(0xE3, dtype=torch.int16) << 7).view(torch.float16).double()
@@ -131,3 +133,40 @@ def rows_of(cache, layer, row, first, n):
         id_, slot = table[t // cache.page_size], t % cache.page_size
         out.append(values(codes[id_, :, slot], scales[id_, :, slot]))
     return out
+
+
+def check_attention4(q, held, layer, seqs, q_start, causal, scale, o, lse, untouched):
+    """Every row of the list against the definition; the others as `untouched` says.
+
+    The bounds are paged_ref's (a weight rounded once to bf16; here it is float16,
+    eight times finer), and one more term: float16 has no numbers below 2^-24.  A
+    weight is rounded as p = 2^(s - m + 7), where the reference m is at most the
+    row's largest score (it is a maximum of scores, and only ever grows to another),
+    so below 2^-14 it is off by 2^-25 at most, while the sum of weights is at least
+    2^7 (the largest score's own): O is off by 2^-32 sum |v| more, over the keys that
+    are there.  (In a part of the keys the same holds against the part's largest
+    score, and parts are joined with weights of at most 1.)  It shows where the
+    largest weight's key has a 0 in a column: of 16 values one or two are."""
+    ref = attention(q, held, layer, seqs, q_start, causal, scale)
+    og, lg = o.cpu().double(), lse.cpu().double()
+    rows = seqs.tolist() if seqs is not None else range(q_start.numel() - 1)
+    g = q.shape[1] // held.heads
+    mass = {}
+    for i, row in enumerate(rows):
+        _, v, there = gather(held, layer, row, int(held.seq_lens[row]))
+        for t in range(int(q_start[i]), int(q_start[i + 1])):
+            mass[t] = v[:, there].abs().sum(1).repeat_interleave(g, 0)
+    for r in range(q.shape[0]):
+        if r not in ref:
+            assert torch.equal(og[r], untouched[0][r].cpu().double()), f"row {r} was written"
+            assert torch.equal(lg[r], untouched[1][r].cpu().double()), f"LSE of row {r} was written"
+            continue
+        ro, rl, to, tl = ref[r]
+        to = to + 2.0 ** -32 * mass[r] * 1.01
+        assert not torch.isnan(og[r]).any() and not torch.isnan(lg[r]).any(), f"NaN in row {r}"
+        err = (og[r] - ro).abs()
+        assert (err <= to).all(), f"row {r}: off by {(err / to).max():.3g} of the bound"
+        inf = torch.isinf(rl)
+        assert torch.equal(torch.isinf(lg[r]) & (lg[r] < 0), inf), f"LSE of row {r}"
+        assert (og[r][inf] == 0).all()
+        assert ((lg[r] - rl).abs()[~inf] <= tl[~inf]).all(), f"LSE of row {r}: {(lg[r] - rl).abs()[~inf].max():.3g}"

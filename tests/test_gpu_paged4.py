@@ -1,15 +1,14 @@
 """Attention over a paged cache of 4-bit values on the GPU, against the
 definition in float64 on the values that the cache holds (bounds derived in
-paged_ref.py: products with a rounded P once, a bound that the kernels meet with
-room to spare), and the page operators on such a cache."""
+e2m1_ref.py and paged_ref.py), and the page operators on such a cache."""
 import math
 import random
 
 import pytest
 import torch
 
-from e2m1_ref import angles, build4, ints, quantize, rows_of, starts, turned, values
-from paged_ref import Pages, check_attention
+from e2m1_ref import angles, build4, check_attention4, ints, quantize, rows_of, starts, turned, values
+from paged_ref import Pages
 
 pytestmark = pytest.mark.gpu
 BF16, E2M1 = torch.bfloat16, torch.float4_e2m1fn_x2
@@ -39,7 +38,7 @@ def attend(eta, cache, held, new, g, seqs=None, causal=True, layer=0, seed=0, be
     eta.attn_paged_fwd(q, cache, layer, sq, qs, max_q=max_q or max(max(new), 1), causal=causal, scale=scale, out=o, lse=lse, **kw)
     torch.cuda.synchronize()
     assert eta.attn_status() == status
-    check_attention(q, held, layer, sq, qs, causal, scale if scale is not None else 1 / math.sqrt(cache.d), o, lse, was)
+    check_attention4(q, held, layer, sq, qs, causal, scale if scale is not None else 1 / math.sqrt(cache.d), o, lse, was)
     return o, lse
 
 
