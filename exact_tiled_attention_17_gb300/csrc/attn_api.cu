@@ -107,22 +107,21 @@ bool make_bf16_rows_map(CUtensorMap *m, const void *base, int D, int N, int BH, 
     return true;
 }
 
-bool make_map(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *base, int rank,
-              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+bool make_map(CUtensorMap *m, CUtensorMapSwizzle swizzle, const void *base, int rank, const cuuint64_t *dims,
+              const cuuint64_t *strides, const cuuint32_t *box) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (rank < 1 || rank > 5 || !enc) return false;
-    const cuuint64_t es = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
     cuuint64_t st[4] = {};
     // a dimension of one element may come with any stride: give it a valid one
-    for (int i = 1; i < rank; ++i) st[i - 1] = dims[i] > 1 ? strides[i - 1] : 16 * ((dims[0] * es + 15) / 16);
+    for (int i = 1; i < rank; ++i) st[i - 1] = dims[i] > 1 ? strides[i - 1] : 16 * ((dims[0] * 2 + 15) / 16);
     const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
-    return enc(m, type, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, st, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, st, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool make_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box) {
-    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides, box);
+    return make_map(m, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides, box);
 }
 
 int *device_error_word() {

@@ -34,9 +34,9 @@ bool make_bf16_rows_map(CUtensorMap *m, const void *base, int D, int N, int BH, 
 bool make_bf16_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box);
 
-// The same for a tensor of any element type and swizzle.
-bool make_map(CUtensorMap *m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *base, int rank,
-              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box);
+// The same with any swizzle.
+bool make_map(CUtensorMap *m, CUtensorMapSwizzle swizzle, const void *base, int rank, const cuuint64_t *dims,
+              const cuuint64_t *strides, const cuuint32_t *box);
 
 // Error-word bit set by the emulation kernel for an out-of-range row id
 // (timed-out waits use the low bits).

@@ -249,13 +249,33 @@ int launch_paged4_tc(PagedParams p, void *workspace, cudaStream_t stream);
 
 // Tensor maps of the bf16 kernels: Q in boxes of `tokens` tokens x g heads x 64
 // columns (rows token by token), K and V in boxes of `box` slots x 64 columns of
-// one page and head.
+// one page and head (box 0: Q alone).
 bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
 
-// Tensor maps for 4-bit values: Q as above (tc), or with whole rows in their own
-// order; codes of K and V in boxes of `box` slots of one page and head (rows of 64
-// bytes swizzled within 64 bytes).
-bool paged4_maps(const PagedParams &p, int tokens, int box, bool tc, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv);
+// A tile of `keys` keys of 4-bit K or V in shared memory: boxes of min(page_size,
+// keys) slots one after the other, each as it lies in its page, codes and then
+// scales.  (One copy of a page of up to `keys` tokens; of longer ones two.)
+struct Paged4Box {
+    int shift;    // slots of a box: 1 << shift
+    int codes;    // bytes of codes of a box
+    int bytes;    // of a box
+};
+__device__ __forceinline__ Paged4Box paged4_box(int page_shift, int keys_shift, int d) {
+    const int sh = min(page_shift, keys_shift);
+    return Paged4Box{sh, (d / 2) << sh, (d / 16 * 9) << sh};
+}
+// Copies slots slot .. of a page (the block of one head at `block`) as a box; one lane.
+__device__ __forceinline__ void paged4_copy(const Paged4Box &b, uint32_t to, const char *block, int slot, int page_size, int d,
+                                            uint32_t bar) {
+    if ((1 << b.shift) == page_size) {
+        bulk_load(to, block, b.bytes, bar);
+    } else {
+        bulk_load(to, block + slot * (d / 2), b.codes, bar);
+        bulk_load(to + b.codes, block + page_size * (d / 2) + slot * (d / 16), b.bytes - b.codes, bar);
+    }
+}
+// Tensor map of Q for the 4-bit stream kernel: as above, but rows whole and in their own order.
+bool paged4_q_map(const PagedParams &p, int tokens, CUtensorMap *tq);
 
 // Workspace: headers, m, l, o for `ctas` CTAs and units of `rows` rows.
 inline size_t paged_partial_bytes(int ctas, int rows, int d) {

@@ -7,8 +7,8 @@
 // (e2m1 to float16), a multiplication by the scale, and a share of a matrix
 // instruction.
 //
-//   producer warp  finds the CTA's work; TMA: tiles of 128 keys, page by page, codes
-//                  and scales of K and V on one barrier, and the next unit's Q rows.
+//   producer warp  finds the CTA's work; bulk copies of tiles of 128 keys, page by page,
+//                  K and V on one barrier, and (TMA) of the next unit's Q rows.
 //   other warps    consumers, 16 keys of a tile at a time, each with a running
 //                  maximum, sum and output of its own for all rows and columns; no
 //                  exchange between warps before the unit's end.
@@ -23,7 +23,8 @@
 //                  bytes are exchanged before the conversion (4 instructions to 16
 //                  values).  P^T comes from S^T by transposing 8 x 8 blocks in registers.
 // Which key stands in which row of the instruction is free too, as long as S and P V
-// agree; an order is taken that keeps the reads of shared memory free of conflicts.
+// agree; an order is taken that keeps the reads of K free of bank conflicts (of V,
+// two-way at d = 128, where four keys' rows of 64 bytes cannot avoid one another).
 //
 // Numbers.  Values are exact in float16.  A row of Q is multiplied by a power of two
 // that brings its largest column to 2^14 .. 2^15 (bf16 has more exponents than
@@ -37,6 +38,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "e2m1.cuh"
 #include "launch.cuh"
@@ -48,12 +50,11 @@ namespace {
 template <int D_, int NT_>   // head dimension, blocks of 8 query rows
 struct P4Shape {
     static constexpr int D = D_, NT = NT_, ROWS = 8 * NT;
-    static constexpr int NW = NT == 1 ? 8 : 4;                // consumer warps
+    static constexpr int NW = 4, SPW = 2;                     // consumer warps, blocks of 16 keys of a tile to each
     static constexpr int THREADS = 32 * (NW + 1);
-    static constexpr int KEYS = 128, CTAS = 2;
+    static constexpr int KEYS = 16 * NW * SPW, CTAS = 2;
     static constexpr int CB = D / 2, SB = D / 16;             // bytes of a row: codes, scales
-    static constexpr int OFF_KS = KEYS * CB;                  // of a stage: K codes, K scales, V codes, V scales
-    static constexpr int OFF_V = KEYS * (CB + SB);
+    static constexpr int OFF_V = KEYS * (CB + SB);            // of a stage: K, V
     static constexpr int STAGE = 2 * OFF_V;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OS = D + 4;                          // floats from row to row of an output in shared memory
@@ -69,13 +70,12 @@ struct P4Shape {
     static constexpr int OFF_UNIT = OFF_BADP + (NS * 4 + 15) / 16 * 16;   // [2]
     static constexpr int SMEM_BYTES = OFF_UNIT + 2 * static_cast<int>(sizeof(PagedUnit)) + 1024;
     static_assert(SMEM_BYTES <= 113 * 1024, "shared memory");
-    static_assert(STAGE % 128 == 0 && OFF_KS % 128 == 0 && OFF_V % 128 == 0 && Q_BYTES % 128 == 0 && OFF_MISC % 16 == 0, "alignment");
-    static_assert(D != 128 || (STAGE % 512 == 0 && OFF_V % 512 == 0), "the swizzle's period");
+    static_assert(OFF_Q % 128 == 0 && Q_BYTES % 128 == 0 && OFF_MISC % 16 == 0, "alignment");
     // a lane's run of K: words (8 columns each), and of V: bytes (2 columns each)
     static constexpr int KW = D / 32, KS = 2 * KW;
     static constexpr int VB = D == 96 ? 8 : D / 16;           // (d 96: 6 lanes of 8 bytes; 2 repeat the last run)
     // the key (of 8) in row i of the matrix instruction: nibble i
-    static constexpr uint32_t ORDER = D == 128 ? 0x65742130u : 0x67453210u;
+    static constexpr uint32_t ORDER = 0x67453210u;
 };
 
 __device__ __forceinline__ void mma16816h(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -92,8 +92,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 template <int D, int NT>
 __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
-    paged4_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kc,
-                         const __grid_constant__ CUtensorMap tm_vc, const PagedParams p) {
+    paged4_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const PagedParams p) {
     using S = P4Shape<D, NT>;
     constexpr int NS = S::NS, ROWS = S::ROWS, NW = S::NW, KEYS = S::KEYS, KW = S::KW, KS = S::KS, VB = S::VB;
     extern __shared__ uint8_t smem_raw[];
@@ -118,32 +117,24 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (warp == NW && lane == 0) {
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_kc);
-        tma_prefetch_desc(&tm_vc);
-    }
+    if (warp == NW && lane == 0) tma_prefetch_desc(&tm_q);
+    const Paged4Box box = paged4_box(gm.page_shift, 7, D);
     __syncthreads();
     paged_touch(p);
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == NW) {
         // ------------------------------------------------------------------
-        // Producer.  Lane (part, box) issues that copy of a tile; parts: K codes,
-        // K scales, V codes, V scales.
+        // Producer.  Lane (K or V, box) issues that copy of a tile.
         // ------------------------------------------------------------------
         auto wwait = [&](uint32_t b, uint32_t parity, int site) -> bool {
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
-        const int box_rows = min(gm.page_size, KEYS);
-        const int boxes = KEYS / box_rows;   // 1 .. 8
-        const int part = lane / boxes, my_box = lane % boxes;
-        const bool mine = lane < 4 * boxes, scales = part & 1;
-        const CUtensorMap *tm = part < 2 ? &tm_kc : &tm_vc;
-        const char *pool = static_cast<const char *>(part < 2 ? p.K : p.V) + gm.page_size * S::CB;   // of the scales
-        const uint32_t dst = (part >> 1) * S::OFF_V + (scales ? S::OFF_KS + my_box * box_rows * S::SB : my_box * box_rows * S::CB);
-        const uint32_t box_bytes = 2 * box_rows * (S::CB + S::SB);   // of all parts
-        const uint64_t policy = l2_policy_evict_first();
+        const int boxes = KEYS >> box.shift;   // 1 .. 8
+        const int my_kv = lane / boxes, my_box = lane % boxes;
+        const bool mine = lane < 2 * boxes;
+        const char *pool = static_cast<const char *>(my_kv ? p.V : p.K);
+        const uint32_t dst = my_kv * S::OFF_V + my_box * box.bytes;
         int t = 0, u = 0;
         bool ok = true;
         PagedFeed feed;
@@ -167,7 +158,7 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
             feed.report(p, w);
             const int j1 = w.tile0 + w.tiles;
             auto lookup = [&](int j) -> int {   // page of this lane's box: -1 past the end, -2 missing
-                const int key = j * KEYS + my_box * box_rows;
+                const int key = j * KEYS + (my_box << box.shift);
                 if (!mine || key >= w.len) return -1;
                 const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                 return id < 0 ? -2 : id;
@@ -184,25 +175,23 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                     break;
                 }
                 // (boxes without a page are not copied: nothing of them is used)
-                const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && part == 0);
-                const uint32_t there = __ballot_sync(0xffffffffu, id >= 0 && part == 0);
+                const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_kv == 0);
+                const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
                 if (lane == 0) {
                     uint32_t bits = 0;
                     if (missing) {
                         atomicOr(p.err, kErrWordBadRow);
+                        const int groups = 1 << (box.shift - 4);
                         for (int b = 0; b < boxes; ++b)
-                            if ((missing >> b) & 1u) bits |= ((1u << (box_rows / 16)) - 1u) << (b * (box_rows / 16));
+                            if ((missing >> b) & 1u) bits |= ((1u << groups) - 1u) << (b * groups);
                     }
                     bad_pages[st] = bits;
-                    mbar_arrive_expect_tx(bar(S::BAR_FULL + st), __popc(there) * box_bytes);
+                    mbar_arrive_expect_tx(bar(S::BAR_FULL + st), __popc(there) * box.bytes);
                 }
                 __syncwarp();
-                if (id >= 0) {
-                    const int slot = (j * KEYS + my_box * box_rows) & (gm.page_size - 1);
-                    const uint32_t to = sbase + st * S::STAGE + dst;
-                    if (scales) bulk_load(to, pool + id * p.page_stride + w.head * p.head_stride + slot * S::SB, box_rows * S::SB, bar(S::BAR_FULL + st), policy);
-                    else tma_load_4d(to, tm, bar(S::BAR_FULL + st), 0, slot, w.head, id);
-                }
+                if (id >= 0)
+                    paged4_copy(box, sbase + st * S::STAGE + dst, pool + id * p.page_stride + w.head * p.head_stride,
+                                (j * KEYS + (my_box << box.shift)) & (gm.page_size - 1), gm.page_size, D, bar(S::BAR_FULL + st));
             }
         }
         feed.finish(p, cta);
@@ -220,19 +209,20 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
         auto order = [](int i) -> int { return (S::ORDER >> (4 * i)) & 7; };
         const int key_r = order(r), key_a = order(2 * c), key_b = order(2 * c + 1);
         const int vr = D == 96 ? min(r, 5) : r;   // the lane's run of V
-        // (d 128: 16-byte pieces of the 64-byte rows are swizzled by bits 1 and 2 of the row)
-        auto k_at = [&](int key) -> int {
-            if constexpr (D == 128) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-            else return key * S::CB + c * (D / 8);
-        };
-        auto v_at = [&](int key) -> int {
-            if constexpr (D == 128) return key * 64 + (((r >> 1) ^ ((key >> 1) & 3)) << 4) + (r & 1) * 8;
-            else return key * S::CB + vr * VB;
-        };
-        const int k_off = k_at(key_r), va_off = v_at(key_a), vb_off = v_at(key_b);
-        const int ks_off = key_r * S::SB + c * (D / 8) / 8;
-        const int vs_group = vr * VB / 8, vsa_off = key_a * S::SB + vs_group, vsb_off = key_b * S::SB + vs_group;
-        int t = 0;
+        // where this lane's bytes of the warp's blocks lie in a tile
+        int k_at[S::SPW], ks_at[S::SPW], va_at[S::SPW], vb_at[S::SPW], vsa_at[S::SPW], vsb_at[S::SPW];
+#pragma unroll
+        for (int b = 0; b < S::SPW; ++b) {
+            const int key = (warp + b * NW) * 16, in = key & ((1 << box.shift) - 1), at = (key >> box.shift) * box.bytes;
+            const int codes = at + in * S::CB, scales = at + box.codes + in * S::SB;
+            k_at[b] = codes + key_r * S::CB + c * (D / 8);
+            ks_at[b] = scales + key_r * S::SB + c * (D / 8) / 8;
+            va_at[b] = S::OFF_V + codes + key_a * S::CB + vr * VB;
+            vb_at[b] = S::OFF_V + codes + key_b * S::CB + vr * VB;
+            vsa_at[b] = S::OFF_V + scales + key_a * S::SB + vr * VB / 8;
+            vsb_at[b] = S::OFF_V + scales + key_b * S::SB + vr * VB / 8;
+        }
+        int st = 0, phase = 0;   // stage of the next tile
         for (int u = 0;; ++u) {
             const int qb = u & 1;
             // (all consumers leave together: what one reads of a unit that never came, the others read too)
@@ -284,14 +274,13 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                 }
             const int vis_all = paged_unit_visible(gm, w, 0);              // what every row sees
             const int vis_any = paged_unit_visible(gm, w, w.ntok - 1);     // what some row sees
-            // mu: the reference less 7; lim: what a score must exceed to move it
-            float mu[NT][2], lim[NT][2], l[NT][2], o[NT][VB][4];
+            // mu: the reference less 7 (-inf: no key yet)
+            float mu[NT][2], l[NT][2], o[NT][VB][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    mu[nt][i] = 0.f;
-                    lim[nt][i] = -INFINITY;
+                    mu[nt][i] = -INFINITY;
                     l[nt][i] = 0.f;
                 }
 #pragma unroll
@@ -299,157 +288,173 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][m][e] = 0.f;
             }
-            for (int j = w.tile0; j < j1; ++j, ++t) {
-                const int st = t % NS;
-                mbar_wait(bar(S::BAR_FULL + st), (t / NS) & 1, abort_flag, p.err, 65);
-                const uint8_t *tile = smem + st * S::STAGE;
-                const uint32_t bad = bad_pages[st];
-#pragma unroll 1
-                for (int step = warp; step < KEYS / 16; step += NW) {
-                    const int key0 = j * KEYS + step * 16;
-                    if (key0 >= vis_any || ((bad >> step) & 1u)) continue;
-                    const uint8_t *kt = tile + step * (16 * S::CB), *kst = tile + S::OFF_KS + step * (16 * S::SB);
-                    // ---------------- S^T = K Q^T ----------------
-                    uint32_t kw[2][KW], ksc[2][2];
+            // One block of 16 keys from key0 on.  EDGE: some row does not see all of them.
+            auto block = [&](auto edge_c, const uint8_t *tile, int b, int key0) {
+                constexpr bool EDGE = decltype(edge_c)::value;
+                // ---------------- S^T = K Q^T ----------------
+                uint32_t kw[2][KW], ksc[2][2];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint8_t *at = kt + k_off + h * (8 * S::CB), *as = kst + ks_off + h * (8 * S::SB);
-                        if constexpr (D == 128) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(at);
-                            kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
-                            const uint32_t b = *reinterpret_cast<const uint16_t *>(as);
-                            ksc[h][0] = e2m1_scale_h2(b & 0xffu);
-                            ksc[h][1] = e2m1_scale_h2(b >> 8);
-                        } else if constexpr (D == 96) {
+                for (int h = 0; h < 2; ++h) {
+                    const uint8_t *at = tile + k_at[b] + h * (8 * S::CB), *as = tile + ks_at[b] + h * (8 * S::SB);
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                        kw[h][0] = v.x, kw[h][1] = v.y, kw[h][2] = v.z, kw[h][3] = v.w;
+                        const uint32_t x = *reinterpret_cast<const uint16_t *>(as);
+                        ksc[h][0] = e2m1_scale_h2(x & 0xffu);
+                        ksc[h][1] = e2m1_scale_h2(x >> 8);
+                    } else if constexpr (D == 96) {
 #pragma unroll
-                            for (int x = 0; x < 3; ++x) kw[h][x] = *reinterpret_cast<const uint32_t *>(at + 4 * x);
-                            ksc[h][0] = e2m1_scale_h2(as[0]);
-                            ksc[h][1] = e2m1_scale_h2(as[1]);
-                        } else if constexpr (D == 64) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                            kw[h][0] = v.x, kw[h][1] = v.y;
-                            ksc[h][0] = ksc[h][1] = e2m1_scale_h2(as[0]);
-                        } else {
-                            kw[h][0] = *reinterpret_cast<const uint32_t *>(at);
-                            ksc[h][0] = ksc[h][1] = e2m1_scale_h2(as[0]);
-                        }
+                        for (int x = 0; x < 3; ++x) kw[h][x] = *reinterpret_cast<const uint32_t *>(at + 4 * x);
+                        ksc[h][0] = e2m1_scale_h2(as[0]);
+                        ksc[h][1] = e2m1_scale_h2(as[1]);
+                    } else if constexpr (D == 64) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                        kw[h][0] = v.x, kw[h][1] = v.y;
+                        ksc[h][0] = ksc[h][1] = e2m1_scale_h2(as[0]);
+                    } else {
+                        kw[h][0] = *reinterpret_cast<const uint32_t *>(at);
+                        ksc[h][0] = ksc[h][1] = e2m1_scale_h2(as[0]);
                     }
-                    float s[NT][2][4];   // (two chains of sums)
+                }
+                float s[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+                for (int x = 0; x < KW; ++x) {
+                    uint32_t h[2][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        // (d 96: the middle word belongs to the first group in even c, to the second in odd c)
+                        const uint32_t sc = D == 128 ? ksc[y][x >> 1] : D == 96 ? (x == 0 ? ksc[y][0] : x == 2 ? ksc[y][1] : c & 1 ? ksc[y][1] : ksc[y][0]) : ksc[y][0];
+                        e2m1_values(kw[y][x], sc, h[y]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t a[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816h(s[nt], a, qf[nt][2 * x + k][0], qf[nt][2 * x + k][1]);
+                    }
+                }
+                // ---------------- weights ----------------
+                // element e = 2 h + i: key key_r + 8 h, row 2c + i.  y: the weight's exponent
+                float y[NT][4];
+                bool move = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = e & 1;
+                        y[nt][e] = fmaf(s[nt][e], mult[nt][i], -mu[nt][i]);
+                        if (EDGE && key0 + key_r + (e >> 1) * 8 >= vis[nt][i]) y[nt][e] = -INFINITY;
+                        move = move || y[nt][e] > 15.f;
+                    }
+                if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
+                        for (int i = 0; i < 2; ++i) {
+                            float x[2];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) s[nt][x][e] = 0.f;
+                            for (int h = 0; h < 2; ++h) {
+                                x[h] = s[nt][2 * h + i] * mult[nt][i];
+                                if (EDGE && key0 + key_r + h * 8 >= vis[nt][i]) x[h] = -INFINITY;
+                            }
+                            float v = fmaxf(x[0], x[1]);
 #pragma unroll
-                    for (int x = 0; x < KW; ++x) {
-                        uint32_t h[2][4];
+                            for (int z = 4; z < 32; z <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, z));
+                            if (v - mu[nt][i] > 15.f) {
+                                const float a = ex2(mu[nt][i] - (v - 7.f));   // (the first time: 0)
+                                mu[nt][i] = v - 7.f;
+                                l[nt][i] *= a;
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            // (d 96: the middle word belongs to the first group in even c, to the second in odd c)
-                            const uint32_t sc = D == 128 ? ksc[y][x >> 1] : D == 96 ? (x == 0 ? ksc[y][0] : x == 2 ? ksc[y][1] : c & 1 ? ksc[y][1] : ksc[y][0]) : ksc[y][0];
-                            e2m1_values(kw[y][x], sc, h[y]);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t a[4] = {h[0][2 * k], h[1][2 * k], h[0][2 * k + 1], h[1][2 * k + 1]};
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816h(s[nt][k], a, qf[nt][2 * x + k][0], qf[nt][2 * x + k][1]);
-                        }
-                    }
-                    // ---------------- weights ----------------
-                    // element e = 2 h + i: key key_r + 8 h, row 2c + i
-                    const bool edge = key0 + 16 > vis_all;
-                    bool move = false;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int i = e & 1;
-                            float x = (s[nt][0][e] + s[nt][1][e]) * mult[nt][i];
-                            if (edge) x = key0 + key_r + (e >> 1) * 8 < vis[nt][i] ? x : -INFINITY;
-                            s[nt][0][e] = x;
-                            move = move || x > lim[nt][i];
-                        }
-                    if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                float v = fmaxf(s[nt][0][i], s[nt][0][2 + i]);
-#pragma unroll
-                                for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-                                if (v > lim[nt][i]) {
-                                    const float a = lim[nt][i] == -INFINITY ? 0.f : ex2(mu[nt][i] - (v - 7.f));
-                                    mu[nt][i] = v - 7.f;
-                                    lim[nt][i] = v + 8.f;
-                                    l[nt][i] *= a;
-#pragma unroll
-                                    for (int m = 0; m < VB; ++m) {
-                                        o[nt][m][i] *= a;
-                                        o[nt][m][2 + i] *= a;
-                                    }
+                                for (int m = 0; m < VB; ++m) {
+                                    o[nt][m][i] *= a;
+                                    o[nt][m][2 + i] *= a;
                                 }
                             }
-                    }
-                    uint32_t pf[NT][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float p0 = ex2(s[nt][0][2 * h] - mu[nt][0]), p1 = ex2(s[nt][0][2 * h + 1] - mu[nt][1]);
-                            l[nt][0] += p0;
-                            l[nt][1] += p1;
-                            pf[nt][h] = transpose8(pack_f16x2(p0, p1));
+                            for (int h = 0; h < 2; ++h) y[nt][2 * h + i] = x[h] == -INFINITY ? -INFINITY : x[h] - mu[nt][i];
                         }
-                    // ---------------- O^T += V^T P^T ----------------
-                    const uint8_t *vt = tile + S::OFF_V + step * (16 * S::CB), *vst = tile + S::OFF_V + S::OFF_KS + step * (16 * S::SB);
-                    uint32_t sc[2];   // of keys (a, b) and (a + 8, b + 8)
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t b0 = vst[vsa_off + h * (8 * S::SB)], b1 = vst[vsb_off + h * (8 * S::SB)];
-                        if (edge) {
-                            if (key0 + h * 8 + key_a >= w.len) b0 = 0u;
-                            if (key0 + h * 8 + key_b >= w.len) b1 = 0u;
-                        }
-                        sc[h] = (b0 | b1 << 16) << 7;
+                        const float p0 = ex2(y[nt][2 * h]), p1 = ex2(y[nt][2 * h + 1]);
+                        l[nt][0] += p0;
+                        l[nt][1] += p1;
+                        pf[nt][h] = transpose8(pack_f16x2(p0, p1));
                     }
-                    constexpr int VW = VB >= 4 ? VB / 4 : 1;
-                    uint32_t vw[2][2][VW];   // [h][a or b]
+                // ---------------- O^T += V^T P^T ----------------
+                uint32_t sc[2];   // of keys (a, b) and (a + 8, b + 8)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t b0 = tile[vsa_at[b] + h * (8 * S::SB)], b1 = tile[vsb_at[b] + h * (8 * S::SB)];
+                    if (EDGE) {
+                        if (key0 + h * 8 + key_a >= w.len) b0 = 0u;
+                        if (key0 + h * 8 + key_b >= w.len) b1 = 0u;
+                    }
+                    sc[h] = b1 * 0x800000u + b0 * 0x80u;
+                }
+                constexpr int VW = VB >= 4 ? VB / 4 : 1;
+                uint32_t vw[2][2][VW];   // [h][a or b]
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint8_t *at = vt + (x ? vb_off : va_off) + h * (8 * S::CB);
-                            if constexpr (VB == 8) {
-                                const uint2 v = *reinterpret_cast<const uint2 *>(at);
-                                vw[h][x][0] = v.x;
-                                vw[h][x][VW - 1] = v.y;
-                            } else if constexpr (VB == 4) {
-                                vw[h][x][0] = *reinterpret_cast<const uint32_t *>(at);
-                            } else {
-                                vw[h][x][0] = *reinterpret_cast<const uint16_t *>(at);
-                            }
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint8_t *at = tile + (x ? vb_at[b] : va_at[b]) + h * (8 * S::CB);
+                        if constexpr (VB == 8) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                            vw[h][x][0] = v.x;
+                            vw[h][x][VW - 1] = v.y;
+                        } else if constexpr (VB == 4) {
+                            vw[h][x][0] = *reinterpret_cast<const uint32_t *>(at);
+                        } else {
+                            vw[h][x][0] = *reinterpret_cast<const uint16_t *>(at);
                         }
+                    }
 #pragma unroll
-                    for (int x = 0; x < VW; ++x) {
-                        uint32_t h[4][4];   // a0 .. a3 of four blocks
+                for (int x = 0; x < VW; ++x) {
+                    uint32_t h[4][4];   // a0 .. a3 of four blocks
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const uint32_t a = vw[y][0][x], b = vw[y][1][x];
-                            e2m1_values((a & 0x0f0f0f0fu) | ((b << 4) & 0xf0f0f0f0u), sc[y], h[2 * y]);
-                            e2m1_values(((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u), sc[y], h[2 * y + 1]);
-                        }
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t va = vw[z][0][x], vb = vw[z][1][x];
+                        e2m1_values((va & 0x0f0f0f0fu) | ((vb << 4) & 0xf0f0f0f0u), sc[z], h[2 * z]);
+                        e2m1_values(((va >> 4) & 0x0f0f0f0fu) | (vb & 0xf0f0f0f0u), sc[z], h[2 * z + 1]);
+                    }
 #pragma unroll
-                        for (int m = 0; m < 4 && 4 * x + m < VB; ++m) {
-                            const uint32_t a[4] = {h[0][m], h[1][m], h[2][m], h[3][m]};
+                    for (int m = 0; m < 4 && 4 * x + m < VB; ++m) {
+                        const uint32_t a[4] = {h[0][m], h[1][m], h[2][m], h[3][m]};
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816h(o[nt][4 * x + m], a, pf[nt][0], pf[nt][1]);
-                        }
+                        for (int nt = 0; nt < NT; ++nt) mma16816h(o[nt][4 * x + m], a, pf[nt][0], pf[nt][1]);
+                    }
+                }
+            };
+            for (int j = w.tile0; j < j1; ++j) {
+                mbar_wait(bar(S::BAR_FULL + st), phase, abort_flag, p.err, 65);
+                const uint8_t *tile = smem + st * S::STAGE;
+                const uint32_t bad = bad_pages[st];
+                if ((j + 1) * KEYS <= vis_all && bad == 0u) {
+#pragma unroll
+                    for (int b = 0; b < S::SPW; ++b) block(std::false_type{}, tile, b, 0);
+                } else {
+#pragma unroll 1
+                    for (int b = 0; b < S::SPW; ++b) {
+                        const int key0 = j * KEYS + (warp + b * NW) * 16;
+                        if (key0 >= vis_any || ((bad >> (warp + b * NW)) & 1u)) continue;
+                        if (b == 0) block(std::true_type{}, tile, 0, key0);
+                        else block(std::true_type{}, tile, S::SPW - 1, key0);
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_EMPTY + st));
+                if (++st == NS) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
             // ---------------- the unit's end: the warps' parts are joined ----------------
             float *o_sh = reinterpret_cast<float *>(smem + S::OFF_O);
@@ -544,10 +549,10 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
     p.gm.unit_cost = S::KEYS;
     p.gm.min_share = S::KEYS;
     paged_derive(p.gm);
-    CUtensorMap tq, kc, vc;
-    if (!paged4_maps(p, p.gm.tpu, std::min(p.gm.page_size, S::KEYS), false, &tq, &kc, &vc)) return kErrCuda;
+    CUtensorMap tq;
+    if (!paged4_q_map(p, p.gm.tpu, &tq)) return kErrCuda;
     paged_carve(p, workspace, grid, S::ROWS);
-    const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, stream, tq, kc, vc, p);
+    const int rc = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), S::THREADS, S::SMEM_BYTES, stream, tq, p);
     if (rc != kOk) return rc;
     return launch_paged_merge(p, 1, grid, grid / S::CTAS, stream);
 }

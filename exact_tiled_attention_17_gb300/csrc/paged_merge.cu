@@ -300,24 +300,17 @@ bool paged_maps(const PagedParams &p, int tokens, int box, CUtensorMap *tq, CUte
     const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.slot_stride) * 2, static_cast<cuuint64_t>(p.head_stride) * 2,
                               static_cast<cuuint64_t>(p.page_stride) * 2};
     const cuuint32_t kb[4] = {64u, static_cast<cuuint32_t>(box), 1u, 1u};
+    if (!box) return make_bf16_map(tq, p.Q, 3, qd, qs, qb);
     return make_bf16_map(tq, p.Q, 3, qd, qs, qb) && make_bf16_map(tk, p.K, 4, kd, ks, kb) &&
            make_bf16_map(tv, p.V, 4, kd, ks, kb);
 }
 
-bool paged4_maps(const PagedParams &p, int tokens, int box, bool tc, CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv) {
+bool paged4_q_map(const PagedParams &p, int tokens, CUtensorMap *tq) {
     const PagedGeom &gm = p.gm;
     const cuuint64_t qd[3] = {static_cast<cuuint64_t>(p.d), static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(gm.T)};
     const cuuint64_t qs[2] = {static_cast<cuuint64_t>(p.q_head) * 2, static_cast<cuuint64_t>(p.q_token) * 2};
-    const cuuint32_t qb[3] = {tc ? 64u : static_cast<cuuint32_t>(p.d), static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tokens)};
-    const cuuint64_t kd[4] = {static_cast<cuuint64_t>(p.d / 2), static_cast<cuuint64_t>(gm.page_size),
-                              static_cast<cuuint64_t>(gm.heads), static_cast<cuuint64_t>(gm.pages)};
-    const cuuint64_t ks[3] = {static_cast<cuuint64_t>(p.d / 2), static_cast<cuuint64_t>(p.head_stride),
-                              static_cast<cuuint64_t>(p.page_stride)};
-    const cuuint32_t kb[4] = {static_cast<cuuint32_t>(p.d / 2), static_cast<cuuint32_t>(box), 1u, 1u};
-    const auto sw = p.d == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    return make_map(tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, tc ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, p.Q, 3, qd, qs, qb) &&
-           make_map(tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.K, 4, kd, ks, kb) &&
-           make_map(tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, sw, p.V, 4, kd, ks, kb);
+    const cuuint32_t qb[3] = {static_cast<cuuint32_t>(p.d), static_cast<cuuint32_t>(gm.g), static_cast<cuuint32_t>(tokens)};
+    return make_map(tq, CU_TENSOR_MAP_SWIZZLE_NONE, p.Q, 3, qd, qs, qb);
 }
 
 namespace {

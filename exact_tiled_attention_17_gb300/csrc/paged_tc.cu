@@ -50,6 +50,8 @@
 namespace eta {
 namespace {
 
+// Registers a thread of the 4-bit kernel: 512 x 96 + 256 x 48 = 768 x 80, what the block is launched with.
+constexpr int kRegsSoftmax = 96, kRegsOther = 48;
 constexpr float kThresh = 8.0f;   // the reference maximum moves by at least this (log2 units)
 constexpr float kNegInfP = -__builtin_huge_valf();
 
@@ -62,16 +64,14 @@ struct PtcShape {
     static constexpr int XCH_BYTES = NQ * 2 * 128 * 8;
     // 4-bit tiles as they come: codes, then scales
     static constexpr int STG_BYTES = Q4 ? BC * (DP / 2 + DP / 16) : 0, NG = Q4 ? (DP == 128 ? 3 : 4) : 0;
-    static constexpr int EXP_BYTES = Q4 ? 2 * NQ * BR : 0;        // [2 units][row]: power of two that a row of Q was multiplied by
-    static constexpr int NS_RAW = ((Q4 ? 224 : 222) * 1024 - NQ * Q_BYTES - XCH_BYTES - NG * STG_BYTES - EXP_BYTES) / SLOT_BYTES;
+    static constexpr int NS_RAW = ((Q4 ? 224 : 222) * 1024 - NQ * Q_BYTES - XCH_BYTES - NG * STG_BYTES) / SLOT_BYTES;
     static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
     static constexpr int SOFTMAX_WARPS = 16, WARP_MMA = 17, WARP_TMV = 18;   // (warp 16: Q, K and the work)
-    static constexpr int CONV_WARPS = Q4 ? 4 : 0;                            // from WARP_TMV on, which Q4 has not
-    static constexpr int THREADS = (Q4 ? WARP_TMV + CONV_WARPS : WARP_TMV + 1) * 32;
+    static constexpr int CONV_WARPS = Q4 ? 4 : 0, WARP_CONV = 20;            // (Q4: warps 18 and 19 fill up a warpgroup)
+    static constexpr int THREADS = (Q4 ? WARP_CONV + CONV_WARPS : WARP_TMV + 1) * 32;
     static constexpr int OFF_RING = NQ * Q_BYTES;
     static constexpr int OFF_STG = OFF_RING + NS * SLOT_BYTES;
-    static constexpr int OFF_EXP = OFF_STG + NG * STG_BYTES;
-    static constexpr int OFF_XCH = OFF_EXP + EXP_BYTES;
+    static constexpr int OFF_XCH = OFF_STG + NG * STG_BYTES;
     static constexpr int OFF_BAR = OFF_XCH + XCH_BYTES;
     static constexpr int BAR_QFULL = 0;
     static constexpr int BAR_FULL = BAR_QFULL + NQ;
@@ -99,7 +99,6 @@ struct PtcShape {
     __host__ __device__ static constexpr int s_col(int q) { return q * BC; }
     __host__ __device__ static constexpr int o_col(int q) { return NQ * BC + q * DP; }
     static_assert(NS >= 4 && SMEM_BYTES <= 227 * 1024, "shared memory");
-    static_assert(OFF_STG % 512 == 0 && STG_BYTES % 512 == 0, "the period of the codes' swizzle");
     static_assert(NQ * (BC + DP) <= 512, "tensor memory");
     static_assert(OFF_UNIT % 16 == 0, "alignment");
 };
@@ -115,94 +114,77 @@ __device__ __forceinline__ uint32_t page_bits(uint32_t missing, int boxes, int b
     return bits;
 }
 
-// What the converting warps do (4-bit values): Q of a unit to float16, then each
-// tile of K and V from codes and scales to the float16 tile that the matrix
-// instruction reads (rows of 128 bytes, swizzled as a copy would leave them).  A
-// thread takes a row of Q, or a key: its scales and codes in 16-byte pieces (d 128:
-// swizzled within 64 bytes, so that 8 keys' pieces lie in different banks).  Slots
-// past the end, and of pages that do not exist, become zeros.
+// What the converting warps do (4-bit values): each tile of K and V from codes and
+// scales to the float16 tile that the matrix instruction reads (rows of 128 bytes,
+// swizzled as a copy would leave them).  A warp takes 32 keys, DP / 32 lanes a key, each
+// with 16 bytes of its codes, 32 columns (at d 96 and 32 the last lane has none): pieces
+// are read in the order in which they lie, without bank conflicts, and written without.
+// Slots past the end, and of pages that do not exist, become zeros.
 template <int DP, typename UnitWait, typename UnitDone, typename Wait>
 __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedGeom &gm, uint32_t sbase, uint8_t *smem,
-                                              const PagedUnit *units, volatile uint32_t *bad_pages, int conv_warp, int tpt,
+                                              const PagedUnit *units, volatile uint32_t *bad_pages, int conv_warp,
                                               const UnitWait &unit_wait, const UnitDone &unit_done, const Wait &wwait) {
     using S = PtcShape<DP, true>;
+    constexpr int IT = DP / 32, STEP = 32 / IT;   // keys to a lane, and how far they are apart
     auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
-    const int lane = threadIdx.x & 31, row = conv_warp * 32 + lane;
-    const int pieces = p.d / 32;   // of 16 bytes: 32 columns
-    const int swz = p.d == 128 ? (row >> 1) & 3 : 0;
+    const int lane = threadIdx.x & 31;
+    const int row0 = conv_warp * 32 + lane / IT, piece = lane % IT;
+    const bool mine = piece < p.d / 32;
+    const Paged4Box box = paged4_box(gm.page_shift, 7, p.d);
     auto signal = [&](int b) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
     };
-    int uo[S::NQ] = {0, 0}, kt = 0;
+    int code_at[IT], scale_at[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int row = row0 + i * STEP, in = row & ((1 << box.shift) - 1), at = (row >> box.shift) * box.bytes;
+        code_at[i] = at + in * (p.d / 2) + piece * 16;
+        scale_at[i] = at + box.codes + in * (p.d / 16) + piece * 2;
+    }
+    // (d 128: the upper half's lanes take their words in another order, or two of a row would write to one bank)
+    const bool other = DP == 128 && (piece & 2);
+    const int chunk0 = (4 * (piece & 1)) ^ (row0 & 7) ^ (other ? 2 : 0);
+    const int to0 = S::OFF_RING + (piece >> 1) * (S::BC * 128) + row0 * 128;
+    int kt = 0;
     for (int u = 0;; ++u) {
         if (!__all_sync(0xffffffffu, unit_wait(u, 72))) return;
         const PagedUnit *w = units + u % S::UB;
         const int tiles = w->tiles, tile0 = w->tile0, len = w->len;
-        int own[S::NQ];
-#pragma unroll
-        for (int q = 0; q < S::NQ; ++q) own[q] = w->own[q];
         unit_done(u);
         if (tiles == 0) return;
-#pragma unroll
-        for (int q = 0; q < S::NQ; ++q) {
-            if (own[q] == 0) continue;
-            if (!wwait(bar(S::BAR_QFULL + q), uo[q] & 1, 73)) return;
-            ++uo[q];
-            uint8_t *at = smem + q * S::Q_BYTES + row * 128;
-            uint32_t top = 0;
-#pragma unroll 4
-            for (int i = 0; i < 8 * S::CB; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(at + (i >> 3) * (S::BR * 128) + (((i & 7) ^ (row & 7)) << 4));
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
-            }
-            const int up = f16_shift(top);
-            const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-#pragma unroll 4
-            for (int i = 0; i < 8 * S::CB; ++i) {
-                uint4 *to = reinterpret_cast<uint4 *>(at + (i >> 3) * (S::BR * 128) + (((i & 7) ^ (row & 7)) << 4));
-                const uint4 v = *to;
-                *to = make_uint4(pack_f16x2(bf16lo_to_f32(v.x) * f, bf16hi_to_f32(v.x) * f),
-                                 pack_f16x2(bf16lo_to_f32(v.y) * f, bf16hi_to_f32(v.y) * f),
-                                 pack_f16x2(bf16lo_to_f32(v.z) * f, bf16hi_to_f32(v.z) * f),
-                                 pack_f16x2(bf16lo_to_f32(v.w) * f, bf16hi_to_f32(v.w) * f));
-            }
-            smem[S::OFF_EXP + (u & 1) * (S::NQ * S::BR) + q * S::BR + row] = static_cast<uint8_t>(static_cast<int8_t>(up));
-            fence_proxy_async_smem();
-            signal(S::BAR_QREADY + q);
-        }
         for (int j = 0; j < tiles; ++j, ++kt) {
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
                 const int g = 2 * kt + v, st = g % S::NG, slot = g % S::NS;
                 if (!wwait(bar(S::BAR_GFULL + st), (g / S::NG) & 1, 74)) return;
                 const uint8_t *src = smem + S::OFF_STG + st * S::STG_BYTES;
-                const uint8_t *scales = src + S::BC * (p.d / 2) + row * (p.d / 16);
-                uint4 codes[DP / 32];
-                uint32_t sc[DP / 32];   // two bytes to a piece
+                const int left = len - (tile0 + j) * S::BC;
+                const uint32_t bad = bad_pages[kt & 7];
+                uint4 codes[IT];
+                uint32_t sc[IT];   // two bytes
 #pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
-                    if (i >= pieces) break;
-                    codes[i] = *reinterpret_cast<const uint4 *>(src + row * (p.d / 2) + ((i ^ swz) << 4));
-                    sc[i] = *reinterpret_cast<const uint16_t *>(scales + 2 * i);
+                for (int i = 0; i < IT; ++i) {
+                    codes[i] = make_uint4(0u, 0u, 0u, 0u);
+                    sc[i] = 0u;
+                    const int row = row0 + i * STEP;
+                    if (!mine) continue;
+                    codes[i] = *reinterpret_cast<const uint4 *>(src + code_at[i]);
+                    if (row < left && !((bad >> (row >> 4)) & 1u)) sc[i] = *reinterpret_cast<const uint16_t *>(src + scale_at[i]);
                 }
-                const bool gone = (tile0 + j) * S::BC + row >= len || ((bad_pages[kt & 7] >> (row >> 4)) & 1u);
                 signal(S::BAR_GEMPTY + st);   // (what the tile held is in registers)
                 if (g >= S::NS && !wwait(bar(S::BAR_EMPTY + slot), (g / S::NS - 1) & 1, 75)) return;
-                uint8_t *to = smem + S::OFF_RING + slot * S::SLOT_BYTES + row * 128;
+                uint8_t *to = smem + slot * S::SLOT_BYTES + to0;
 #pragma unroll
-                for (int i = 0; i < DP / 32; ++i) {
-                    if (i >= pieces) break;
-                    const uint32_t c[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                for (int i = 0; i < IT; ++i) {
+                    const uint32_t c[4] = {other ? codes[i].z : codes[i].x, other ? codes[i].w : codes[i].y,
+                                           other ? codes[i].x : codes[i].z, other ? codes[i].y : codes[i].w};
+                    const uint32_t s0 = e2m1_scale_h2(other ? sc[i] >> 8 : sc[i] & 0xffu), s1 = e2m1_scale_h2(other ? sc[i] & 0xffu : sc[i] >> 8);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t h[4];
-                        e2m1_values(c[e], gone ? 0u : e2m1_scale_h2(e < 2 ? sc[i] & 0xffu : sc[i] >> 8), h);
-                        const int chunk = 4 * i + e;   // of 8 columns
-                        *reinterpret_cast<uint4 *>(to + (chunk >> 3) * (S::BC * 128) + (((chunk & 7) ^ (row & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
+                        e2m1_values(c[e], e < 2 ? s0 : s1, h);
+                        *reinterpret_cast<uint4 *>(to + i * (STEP * 128) + ((chunk0 ^ e) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -210,6 +192,32 @@ __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedG
             }
         }
     }
+}
+
+// Q of a tile to float16 in place (4-bit values), by the tile's 256 threads, two to a
+// row: 64 columns each, or (DP 64) 32.  other(x): the larger of x and what the other
+// half's thread has.  Returns the power of two that the row was multiplied by.
+template <int DP, typename Other>
+__device__ __forceinline__ int convert_q(uint8_t *tile, int row, int h, const Other &other) {
+    constexpr int N = DP / 16;   // 16-byte pieces to a thread
+    uint8_t *at = tile + (DP == 128 ? h * (128 * 128) : 0) + row * 128;
+    const int first = DP == 128 ? 0 : 4 * h;
+    uint4 v[N];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = *reinterpret_cast<const uint4 *>(at + (((first + i) ^ (row & 7)) << 4));
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max((x[e] << 16) & 0x7fff0000u, x[e] & 0x7fff0000u));
+    }
+    const int up = f16_shift(other(top));
+    const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+    auto two = [&](uint32_t x) { return pack_f16x2(bf16lo_to_f32(x) * f, bf16hi_to_f32(x) * f); };
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        *reinterpret_cast<uint4 *>(at + (((first + i) ^ (row & 7)) << 4)) = make_uint4(two(v[i].x), two(v[i].y), two(v[i].z), two(v[i].w));
+    return up;
 }
 
 // N words to 16-byte aligned memory, 32 bytes at a time where that is aligned.
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                 mbar_init(bar(S::BAR_GFULL + g), 1);
                 mbar_init(bar(S::BAR_GEMPTY + g), S::CONV_WARPS);
             }
-            for (int q = 0; q < NQ; ++q) mbar_init(bar(S::BAR_QREADY + q), S::CONV_WARPS);
+            for (int q = 0; q < NQ; ++q) mbar_init(bar(S::BAR_QREADY + q), 256);
         }
         mbar_init(bar(S::BAR_DONE), 1);
         mbar_init(bar(S::BAR_TAIL), 1);
@@ -305,24 +313,25 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
         const bool leader = elect_one();
+        if constexpr (Q4) regs_dec<kRegsOther>();
         if (Q4 && warp >= S::WARP_TMV) {
-            convert_tiles<DP>(p, gm, sbase, smem, units, bad_pages, warp - S::WARP_TMV, tpt, unit_wait, unit_done, wwait);
+            if (warp >= S::WARP_CONV)
+                convert_tiles<DP>(p, gm, sbase, smem, units, bad_pages, warp - S::WARP_CONV, unit_wait, unit_done, wwait);
         } else if (warp != S::WARP_MMA) {
             // --------------------------------------------------------------
             // TMA producers.  Lane b * CB + c copies box b (box_rows keys),
             // column block c, of a tile; tile i of K is the ring's tile 2 i, of V
             // 2 i + 1.
-            // 4-bit values: lane 2 b copies the codes of box b, lane 2 b + 1 the scales,
-            // of K and then of V; the converting warps make the ring's tiles of them.
+            // 4-bit values: lane b copies box b of K and then of V; the converting
+            // warps make the ring's tiles of them.
             // --------------------------------------------------------------
             const bool is_v = !Q4 && warp == S::WARP_TMV;
             const CUtensorMap *tm = is_v ? &tm_v : &tm_k;
             if (leader) {
                 if (!is_v) tma_prefetch_desc(&tm_q);
-                tma_prefetch_desc(tm);
-                if (Q4) tma_prefetch_desc(&tm_v);
+                if (!Q4) tma_prefetch_desc(tm);
             }
-            constexpr int COLS = Q4 ? 2 : S::CB;   // lanes to a box
+            constexpr int COLS = Q4 ? 1 : S::CB;   // lanes to a box
             const int box_rows = min(gm.page_size, BC);
             const int boxes = BC / box_rows;
             const int my_box = lane / COLS, my_cb = lane % COLS;
@@ -404,7 +413,8 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                     const uint32_t missing = __ballot_sync(0xffffffffu, id == -2 && my_cb == 0);
                     if constexpr (Q4) {
                         // (boxes without a page are not copied: their values are made zeros)
-                        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0 && my_cb == 0);
+                        const uint32_t there = __ballot_sync(0xffffffffu, id >= 0);
+                        const Paged4Box box = paged4_box(gm.page_shift, 7, p.d);
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
                             const int g = 2 * kt + v, st = g % S::NG;
@@ -413,21 +423,14 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                                 break;
                             }
                             if (lane == 0) {
-                                if (v == 0) bad_pages[kt & 7] = page_bits(missing, boxes, box_rows, COLS, p.err);
-                                mbar_arrive_expect_tx(bar(S::BAR_GFULL + st), __popc(there) * box_rows * (p.d / 2 + p.d / 16));
+                                if (v == 0) bad_pages[kt & 7] = page_bits(missing, boxes, box_rows, 1, p.err);
+                                mbar_arrive_expect_tx(bar(S::BAR_GFULL + st), __popc(there) * box.bytes);
                             }
                             __syncwarp();
-                            if (id >= 0) {
-                                const int slot_in = (j * BC + my_box * box_rows) & (gm.page_size - 1);
-                                const uint32_t to = sbase + S::OFF_STG + st * S::STG_BYTES;
-                                if (my_cb == 0)
-                                    tma_load_4d(to + my_box * box_rows * (p.d / 2), v ? &tm_v : &tm_k, bar(S::BAR_GFULL + st), 0, slot_in, w.head, id);
-                                else
-                                    bulk_load(to + BC * (p.d / 2) + my_box * box_rows * (p.d / 16),
-                                              static_cast<const char *>(v ? p.V : p.K) + id * p.page_stride + w.head * p.head_stride +
-                                                  gm.page_size * (p.d / 2) + slot_in * (p.d / 16),
-                                              box_rows * (p.d / 16), bar(S::BAR_GFULL + st), pol_q);
-                            }
+                            if (id >= 0)
+                                paged4_copy(box, sbase + S::OFF_STG + st * S::STG_BYTES + my_box * box.bytes,
+                                            static_cast<const char *>(v ? p.V : p.K) + id * p.page_stride + w.head * p.head_stride,
+                                            (j * BC + my_box * box_rows) & (gm.page_size - 1), gm.page_size, p.d, bar(S::BAR_GFULL + st));
                         }
                         if (!ok) break;
                         continue;
@@ -596,6 +599,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
         // ------------------------------------------------------------------
         // Softmax warpgroup h of query tile q.
         // ------------------------------------------------------------------
+        if constexpr (Q4) regs_inc<kRegsSoftmax>();
         const int q = warp >> 3, h = (warp >> 2) & 1, wq = warp & 3;
         const int row_in = wq * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(wq * 32) << 16;
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
             pair_sync();
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ao) : "r"(xch(1 - h)) : "memory");
         };
-        int sq = 0, kt = 0;
+        int sq = 0, kt = 0, uq = 0;
         bool ok = true;
         for (int u = 0;; ++u) {
             // (the tile's two warpgroups leave together, whichever wait gave up)
@@ -622,6 +626,22 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
             const PagedUnit *w = units + u % S::UB;
             if (w->tiles == 0) break;
             const int nkvq = w->own[q], inner = w->inner[q];
+            if constexpr (Q4) {
+                if (nkvq > 0) {
+                    // (a wait that gave up: the others' run out too)
+                    if (!mbar_wait(bar(S::BAR_QFULL + q), uq & 1, abort_flag, p.err, 73)) ok = false;
+                    ++uq;
+                    const int up = convert_q<DP>(smem + q * S::Q_BYTES, row_in, h, [&](uint32_t top) {
+                        float mine = __uint_as_float(top), far;
+                        exchange(mine, far);
+                        return max(top, __float_as_uint(far));
+                    });
+                    pair_sync();   // (the exchange's memory is used again)
+                    sl2 = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                    fence_proxy_async_smem();
+                    mbar_arrive(bar(S::BAR_QREADY + q));
+                }
+            }
             // (a row that is none has a reference that no maximum exceeds)
             float m = token_in() < w->ntok ? kNegInfP : -kNegInfP, l = 0.f;
             // (a wait that gives up is recorded and does not end the loop: every
@@ -629,11 +649,6 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
             for (int j = 0; j < nkvq; ++j) {
                 if (!mbar_wait(bar(S::BAR_SFULL + q), (sq + j) & 1, abort_flag, p.err, 20)) ok = false;
                 tc_fence_after();
-                if constexpr (Q4) {
-                    if (j == 0)
-                        sl2 = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(
-                                  127 - static_cast<int8_t>(smem[S::OFF_EXP + (u & 1) * (NQ * S::BR) + q * S::BR + row_in])) << 23);
-                }
                 const bool edge = j >= inner || bad_pages[(kt + j) & 7] != 0u;
                 uint32_t sr[2][32];
                 float mxc[2], mx = kNegInfP;
@@ -813,9 +828,8 @@ int launch_dp(PagedParams &p, void *workspace, cudaStream_t stream) {
     }
     const PagedGeom &gm = p.gm;
     const int tpt = 128 / gm.g;
-    CUtensorMap tq, tk, tv;
-    const int box = std::min(gm.page_size, S::BC);
-    if (!(Q4 ? paged4_maps(p, tpt, box, true, &tq, &tk, &tv) : paged_maps(p, tpt, box, &tq, &tk, &tv))) return kErrCuda;
+    CUtensorMap tq, tk = {}, tv = {};   // (4-bit values are copied without a map)
+    if (!paged_maps(p, tpt, Q4 ? 0 : std::min(gm.page_size, S::BC), &tq, &tk, &tv)) return kErrCuda;
     const int ctas = std::min(nsm, kPagedMaxTcCtas);
     p.gm.tpu = S::NQ * tpt;
     p.gm.tk = S::BC;
