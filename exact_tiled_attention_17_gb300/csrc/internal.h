@@ -96,6 +96,7 @@ int launch_decode(const void *Q, const void *K, const void *V, void *O, float *L
 // in paged.cuh.
 constexpr int kPagedMaxTcCtas = 160;       // CTAs a launch may use (sizes the workspace): one per SM,
 constexpr int kPagedMaxDecodeCtas = 320;   // two,
+constexpr int kPagedMaxDecode4Ctas = 480;  // three (4-bit values),
 constexpr int kPagedMaxSimtCtas = 640;     // up to four
 struct PagedParams;
 size_t paged_workspace_bytes(int g, int max_q, int d, int bits);

@@ -274,6 +274,33 @@ __device__ __forceinline__ void paged4_copy(const Paged4Box &b, uint32_t to, con
         bulk_load(to + b.codes, block + page_size * (d / 2) + slot * (d / 16), b.bytes - b.codes, bar);
     }
 }
+// The pages of a sequence from some column on, for the warp that copies them: 32
+// table entries to a read, one to a lane, and the next 32 on their way.  (A read of
+// each tile's entries two tiles ahead did not do: where a loop carries a value on its
+// way from one register to another, it waits for it.)
+struct PagedColumns {
+    int chunk, cur, nxt, last;   // entries 32 chunk + lane, the 32 after; columns that hold tokens
+    __device__ __forceinline__ int read(const PagedGeom &gm, int seq, int k) const {
+        const int col = 32 * k + static_cast<int>(threadIdx.x & 31);
+        return col < last ? paged_page(gm, seq, col) : -1;
+    }
+    __device__ __forceinline__ void start(const PagedGeom &gm, int seq, int len, int col) {
+        last = (len + gm.page_size - 1) >> gm.page_shift;
+        chunk = col >> 5;
+        cur = read(gm, seq, chunk);
+        nxt = read(gm, seq, chunk + 1);
+    }
+    // Whole warp, columns in increasing order: `first` is the lowest one asked for.  The page of column col, or -1.
+    __device__ __forceinline__ int get(const PagedGeom &gm, int seq, int first, int col) {
+        if (first >> 5 != chunk) {
+            ++chunk;
+            cur = nxt;
+            nxt = read(gm, seq, chunk + 1);
+        }
+        return __shfl_sync(0xffffffffu, cur, col & 31);
+    }
+};
+
 // Tensor map of Q for the 4-bit stream kernel: as above, but rows whole and in their own order.
 bool paged4_q_map(const PagedParams &p, int tokens, CUtensorMap *tq);
 

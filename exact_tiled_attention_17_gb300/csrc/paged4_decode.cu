@@ -52,24 +52,25 @@ struct P4Shape {
     static constexpr int D = D_, NT = NT_, ROWS = 8 * NT;
     static constexpr int NW = 4, SPW = 2;                     // consumer warps, blocks of 16 keys of a tile to each
     static constexpr int THREADS = 32 * (NW + 1);
-    static constexpr int KEYS = 16 * NW * SPW, CTAS = 2;
+    static constexpr int KEYS = 16 * NW * SPW, CTAS = NT == 1 ? 3 : 2;
     static constexpr int CB = D / 2, SB = D / 16;             // bytes of a row: codes, scales
     static constexpr int OFF_V = KEYS * (CB + SB);            // of a stage: K, V
     static constexpr int STAGE = 2 * OFF_V;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OS = D + 4;                          // floats from row to row of an output in shared memory
-    static constexpr int REST = 2 * Q_BYTES + NW * ROWS * (OS + 2) * 4 + 1024 + 512;
-    static constexpr int NS_RAW = (113 * 1024 - REST) / STAGE, NS = NS_RAW < 6 ? NS_RAW : 6;
+    static constexpr int MOST = 228 * 1024 / CTAS - 1024;     // bytes a CTA
+    static constexpr int REST = 2 * Q_BYTES + NW * ROWS * (OS / 2 + 2) * 4 + 1024 + 512;
+    static constexpr int NS_RAW = (MOST - REST) / STAGE, NS = NS_RAW < 6 ? NS_RAW : 6;
     static constexpr int OFF_Q = NS * STAGE;                  // [2]
-    static constexpr int OFF_O = OFF_Q + 2 * Q_BYTES;         // [NW][ROWS][OS]
-    static constexpr int OFF_ML = OFF_O + NW * ROWS * OS * 4; // [2][NW][ROWS]
+    static constexpr int OFF_O = OFF_Q + 2 * Q_BYTES;         // [NW][ROWS / 2][OS]: every other row
+    static constexpr int OFF_ML = OFF_O + NW * ROWS / 2 * OS * 4;   // [2][NW][ROWS]
     static constexpr int OFF_BAR = OFF_ML + 2 * NW * ROWS * 4;
     static constexpr int BAR_FULL = 0, BAR_EMPTY = NS, BAR_QFULL = 2 * NS, BAR_QEMPTY = BAR_QFULL + 2;
     static constexpr int OFF_MISC = OFF_BAR + (BAR_QEMPTY + 2) * 8;
     static constexpr int OFF_BADP = OFF_MISC + 16;            // per stage: missing pages, bit per 16 keys
     static constexpr int OFF_UNIT = OFF_BADP + (NS * 4 + 15) / 16 * 16;   // [2]
     static constexpr int SMEM_BYTES = OFF_UNIT + 2 * static_cast<int>(sizeof(PagedUnit)) + 1024;
-    static_assert(SMEM_BYTES <= 113 * 1024, "shared memory");
+    static_assert(SMEM_BYTES <= MOST && NS >= 3, "shared memory");
     static_assert(OFF_Q % 128 == 0 && Q_BYTES % 128 == 0 && OFF_MISC % 16 == 0, "alignment");
     // a lane's run of K: words (8 columns each), and of V: bytes (2 columns each)
     static constexpr int KW = D / 32, KS = 2 * KW;
@@ -157,18 +158,13 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
             if (w.tiles == 0) break;
             feed.report(p, w);
             const int j1 = w.tile0 + w.tiles;
-            auto lookup = [&](int j) -> int {   // page of this lane's box: -1 past the end, -2 missing
-                const int key = j * KEYS + (my_box << box.shift);
-                if (!mine || key >= w.len) return -1;
-                const int id = paged_page(gm, w.seq, key >> gm.page_shift);
-                return id < 0 ? -2 : id;
-            };
-            // table entries two tiles ahead
-            int next0 = lookup(w.tile0), next1 = w.tiles > 1 ? lookup(w.tile0 + 1) : -1;
+            PagedColumns pages;
+            pages.start(gm, w.seq, w.len, w.tile0 * KEYS >> gm.page_shift);
             for (int j = w.tile0; j < j1; ++j, ++t) {
-                const int id = next0;
-                next0 = next1;
-                if (j + 2 < j1) next1 = lookup(j + 2);
+                const int key = j * KEYS + (my_box << box.shift);
+                const bool held = mine && key < w.len;
+                const int page = pages.get(gm, w.seq, j * KEYS >> gm.page_shift, key >> gm.page_shift);
+                const int id = !held ? -1 : page < 0 ? -2 : page;   // of this lane's box: -1 past the end, -2 missing
                 const int st = t % NS;
                 if (t >= NS && !wwait(bar(S::BAR_EMPTY + st), (t / NS - 1) & 1, 61)) {
                     ok = false;
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                 __syncwarp();
                 if (id >= 0)
                     paged4_copy(box, sbase + st * S::STAGE + dst, pool + id * p.page_stride + w.head * p.head_stride,
-                                (j * KEYS + (my_box << box.shift)) & (gm.page_size - 1), gm.page_size, D, bar(S::BAR_FULL + st));
+                                key & (gm.page_size - 1), gm.page_size, D, bar(S::BAR_FULL + st));
             }
         }
         feed.finish(p, cta);
@@ -457,12 +453,15 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                 }
             }
             // ---------------- the unit's end: the warps' parts are joined ----------------
+            // (even rows, then odd ones, through the same memory)
             float *o_sh = reinterpret_cast<float *>(smem + S::OFF_O);
             float *m_sh = reinterpret_cast<float *>(smem + S::OFF_ML), *l_sh = m_sh + NW * ROWS;
+            const bool whole = w.slot < 0;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i) {
+                if (i > 0) named_bar_sync(1, 32 * NW);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int nt = 0; nt < NT; ++nt) {
                     const int row = nt * 8 + 2 * c + i;
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
@@ -471,50 +470,50 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                         l_sh[warp * ROWS + row] = l[nt][i];
                     }
                     if (D != 96 || r < 6) {
-                        float *at = o_sh + (warp * ROWS + row) * S::OS + r * (2 * VB);
+                        float *at = o_sh + (warp * (ROWS / 2) + nt * 4 + c) * S::OS + r * (2 * VB);
 #pragma unroll
                         for (int m = 0; m < VB; m += 2)
                             *reinterpret_cast<float4 *>(at + 2 * m) =
                                 make_float4(o[nt][m][i], o[nt][m][2 + i], o[nt][m + 1][i], o[nt][m + 1][2 + i]);
                     }
                 }
-            named_bar_sync(1, 32 * NW);
-            const bool whole = w.slot < 0;
-            for (int x = threadIdx.x; x < ROWS * (D / 4); x += 32 * NW) {
-                const int row = x / (D / 4), col = x % (D / 4) * 4;
-                if (row >= rows || *abort_flag) continue;
-                float M = -INFINITY;
+                named_bar_sync(1, 32 * NW);
+                for (int x = threadIdx.x; x < ROWS / 2 * (D / 4); x += 32 * NW) {
+                    const int half = x / (D / 4), row = 2 * half + i, col = x % (D / 4) * 4;
+                    if (row >= rows || *abort_flag) continue;
+                    float M = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < NW; ++k) M = fmaxf(M, m_sh[k * ROWS + row]);
-                float L = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < NW; ++k) M = fmaxf(M, m_sh[k * ROWS + row]);
+                    float L = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < NW; ++k) {
-                    const float mk = m_sh[k * ROWS + row];
-                    const float wt = mk == -INFINITY ? 0.f : ex2(mk - M);
-                    const float4 v = *reinterpret_cast<const float4 *>(o_sh + (k * ROWS + row) * S::OS + col);
-                    if (wt != 0.f) {
-                        L = fmaf(wt, l_sh[k * ROWS + row], L);
-                        acc.x = fmaf(wt, v.x, acc.x);
-                        acc.y = fmaf(wt, v.y, acc.y);
-                        acc.z = fmaf(wt, v.z, acc.z);
-                        acc.w = fmaf(wt, v.w, acc.w);
+                    for (int k = 0; k < NW; ++k) {
+                        const float mk = m_sh[k * ROWS + row];
+                        const float wt = mk == -INFINITY ? 0.f : ex2(mk - M);
+                        const float4 v = *reinterpret_cast<const float4 *>(o_sh + (k * (ROWS / 2) + half) * S::OS + col);
+                        if (wt != 0.f) {
+                            L = fmaf(wt, l_sh[k * ROWS + row], L);
+                            acc.x = fmaf(wt, v.x, acc.x);
+                            acc.y = fmaf(wt, v.y, acc.y);
+                            acc.z = fmaf(wt, v.z, acc.z);
+                            acc.w = fmaf(wt, v.w, acc.w);
+                        }
                     }
-                }
-                const int tr = paged_token(gm, row);
-                const long long tok = w.tok0 + tr;
-                const int head = w.head * gm.g + row - tr * gm.g;
-                if (whole) {
-                    const float inv = L != 0.f ? 1.f / L : 0.f;   // (a NaN goes on)
-                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + tok * p.o_token + static_cast<long long>(head) * p.o_head + col;
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                    if (col == 0 && p.LSE) p.LSE[tok * p.Hq + head] = L != 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
-                } else {
-                    const size_t prow = static_cast<size_t>(w.slot) * p.part_rows + row;
-                    *reinterpret_cast<float4 *>(p.part_o + prow * D + col) = acc;
-                    if (col == 0) {
-                        p.part_m[prow] = paged_part_max(M, L);
-                        p.part_l[prow] = L;
+                    const int tr = paged_token(gm, row);
+                    const long long tok = w.tok0 + tr;
+                    const int head = w.head * gm.g + row - tr * gm.g;
+                    if (whole) {
+                        const float inv = L != 0.f ? 1.f / L : 0.f;   // (a NaN goes on)
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.O) + tok * p.o_token + static_cast<long long>(head) * p.o_head + col;
+                        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                        if (col == 0 && p.LSE) p.LSE[tok * p.Hq + head] = L != 0.f ? (M + log2f(L)) * kPagedLn2 : -INFINITY;
+                    } else {
+                        const size_t prow = static_cast<size_t>(w.slot) * p.part_rows + row;
+                        *reinterpret_cast<float4 *>(p.part_o + prow * D + col) = acc;
+                        if (col == 0) {
+                            p.part_m[prow] = paged_part_max(M, L);
+                            p.part_l[prow] = L;
+                        }
                     }
                 }
             }
@@ -541,7 +540,7 @@ int launch_one(PagedParams &p, void *workspace, cudaStream_t stream) {
             cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, S::THREADS, S::SMEM_BYTES) != cudaSuccess)
             return kErrCuda;
-        grid = std::min(nsm * std::max(per, 1), kPagedMaxDecodeCtas);
+        grid = std::min(nsm * std::max(per, 1), kPagedMaxDecode4Ctas);
         grids[dev].store(grid, std::memory_order_release);
     }
     p.gm.tpu = S::ROWS / p.gm.g;

@@ -331,7 +331,7 @@ Path path_of(int g, int max_q, int bits) {
 
 size_t paged_workspace_bytes(int g, int max_q, int d, int bits) {
     switch (path_of(g, max_q, bits)) {
-        case Path::kDecode4: return paged_partial_bytes(kPagedMaxDecodeCtas, paged4_decode_rows(g, max_q), d);
+        case Path::kDecode4: return paged_partial_bytes(kPagedMaxDecode4Ctas, paged4_decode_rows(g, max_q), d);
         case Path::kTc4:
         case Path::kTc: return paged_partial_bytes(kPagedMaxTcCtas, 256, d);
         case Path::kDecode: return paged_partial_bytes(kPagedMaxDecodeCtas, paged_decode_rows(g, max_q), d);

@@ -378,7 +378,16 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                     const int id = paged_page(gm, w.seq, key >> gm.page_shift);
                     return id < 0 ? -2 : id;
                 };
-                int n0 = lookup(j0), n1 = lookup(j0 + 1), n2 = lookup(j0 + 2), n3 = lookup(j0 + 3);
+                int n0 = -1, n1 = -1, n2 = -1, n3 = -1;
+                PagedColumns pages = {};
+                if constexpr (Q4) {
+                    pages.start(gm, w.seq, w.len, j0 * BC >> gm.page_shift);
+                } else {
+                    n0 = lookup(j0);
+                    n1 = lookup(j0 + 1);
+                    n2 = lookup(j0 + 2);
+                    n3 = lookup(j0 + 3);
+                }
                 if (!is_v) {
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
@@ -395,11 +404,17 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                     }
                 }
                 for (int j = j0; ok && j < j1; ++j, ++kt) {
-                    const int id = n0;
-                    n0 = n1;
-                    n1 = n2;
-                    n2 = n3;
-                    n3 = lookup(j + 4);
+                    int id = n0;
+                    if constexpr (Q4) {
+                        const int key = j * BC + my_box * box_rows;
+                        const int page = pages.get(gm, w.seq, j * BC >> gm.page_shift, key >> gm.page_shift);
+                        id = !mine || key >= w.len ? -1 : page < 0 ? -2 : page;
+                    } else {
+                        n0 = n1;
+                        n1 = n2;
+                        n2 = n3;
+                        n3 = lookup(j + 4);
+                    }
                     const int t = 2 * kt + (is_v ? 1 : 0), slot = t % S::NS, round = t / S::NS;
                     if (!Q4 && round > 0 && !wwait(bar(S::BAR_EMPTY + slot), (round - 1) & 1, is_v ? 19 : 1)) {
                         ok = false;
