@@ -58,9 +58,10 @@ struct P4Shape {
     static constexpr int STAGE = 2 * OFF_V;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OS = D + 4;                          // floats from row to row of an output in shared memory
+    // (16 rows, d 128: with 4 stages 146 us for 64 x 8000 tokens, with 3 and the L1 that leaves for spilled registers 134)
     static constexpr int MOST = 228 * 1024 / CTAS - 1024;     // bytes a CTA
     static constexpr int REST = 2 * Q_BYTES + NW * ROWS * (OS / 2 + 2) * 4 + 1024 + 512;
-    static constexpr int NS_RAW = (MOST - REST) / STAGE, NS = NS_RAW < 6 ? NS_RAW : 6;
+    static constexpr int NS_RAW = (MOST - REST) / STAGE, NS_MAX = NT == 2 ? 3 : 6, NS = NS_RAW < NS_MAX ? NS_RAW : NS_MAX;
     static constexpr int OFF_Q = NS * STAGE;                  // [2]
     static constexpr int OFF_O = OFF_Q + 2 * Q_BYTES;         // [NW][ROWS / 2][OS]: every other row
     static constexpr int OFF_ML = OFF_O + NW * ROWS / 2 * OS * 4;   // [2][NW][ROWS]

@@ -50,8 +50,11 @@
 namespace eta {
 namespace {
 
-// Registers a thread of the 4-bit kernel: 512 x 96 + 256 x 48 = 768 x 80, what the block is launched with.
-constexpr int kRegsSoftmax = 96, kRegsOther = 48;
+// Registers a thread of the 4-bit kernel.  512 x softmax + 256 x other = 768 x 80, what
+// the block is launched with.  At d 128 the converting warps bound it (four chunks of
+// 511 .. 1024 tokens: 337 us, 354 with 96 and 48), at d 64 the softmax (239 us, 254 with 88 and 64).
+__host__ __device__ constexpr int regs_softmax(int dp) { return dp == 128 ? 88 : 96; }
+__host__ __device__ constexpr int regs_other(int dp) { return dp == 128 ? 64 : 48; }
 constexpr float kThresh = 8.0f;   // the reference maximum moves by at least this (log2 units)
 constexpr float kNegInfP = -__builtin_huge_valf();
 
@@ -125,7 +128,7 @@ __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedG
                                               const PagedUnit *units, volatile uint32_t *bad_pages, int conv_warp,
                                               const UnitWait &unit_wait, const UnitDone &unit_done, const Wait &wwait) {
     using S = PtcShape<DP, true>;
-    constexpr int IT = DP / 32, STEP = 32 / IT;   // keys to a lane, and how far they are apart
+    constexpr int IT = DP / 32;   // keys to a lane: 8 apart, or (DP 64) 16
     auto bar = [&](int i) -> uint32_t { return sbase + S::OFF_BAR + 8 * i; };
     const int lane = threadIdx.x & 31;
     const int row0 = conv_warp * 32 + lane / IT, piece = lane % IT;
@@ -135,13 +138,10 @@ __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedG
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(b));
     };
-    int code_at[IT], scale_at[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int row = row0 + i * STEP, in = row & ((1 << box.shift) - 1), at = (row >> box.shift) * box.bytes;
-        code_at[i] = at + in * (p.d / 2) + piece * 16;
-        scale_at[i] = at + box.codes + in * (p.d / 16) + piece * 2;
-    }
+    // (16 keys on, which may be the next box)
+    const int in0 = row0 & ((1 << box.shift) - 1), at0 = (row0 >> box.shift) * box.bytes;
+    const int code_at = at0 + in0 * (p.d / 2) + piece * 16, scale_at = at0 + box.codes + in0 * (p.d / 16) + piece * 2;
+    const int code_step = box.shift == 4 ? box.bytes : 8 * p.d, scale_step = box.shift == 4 ? box.bytes : p.d;
     // (d 128: the upper half's lanes take their words in another order, or two of a row would write to one bank)
     const bool other = DP == 128 && (piece & 2);
     const int chunk0 = (4 * (piece & 1)) ^ (row0 & 7) ^ (other ? 2 : 0);
@@ -161,30 +161,39 @@ __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedG
                 const uint8_t *src = smem + S::OFF_STG + st * S::STG_BYTES;
                 const int left = len - (tile0 + j) * S::BC;
                 const uint32_t bad = bad_pages[kt & 7];
-                uint4 codes[IT];
-                uint32_t sc[IT];   // two bytes
-#pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    codes[i] = make_uint4(0u, 0u, 0u, 0u);
-                    sc[i] = 0u;
-                    const int row = row0 + i * STEP;
-                    if (!mine) continue;
-                    codes[i] = *reinterpret_cast<const uint4 *>(src + code_at[i]);
-                    if (row < left && !((bad >> (row >> 4)) & 1u)) sc[i] = *reinterpret_cast<const uint16_t *>(src + scale_at[i]);
-                }
-                signal(S::BAR_GEMPTY + st);   // (what the tile held is in registers)
-                if (g >= S::NS && !wwait(bar(S::BAR_EMPTY + slot), (g / S::NS - 1) & 1, 75)) return;
                 uint8_t *to = smem + slot * S::SLOT_BYTES + to0;
+                // 16 keys of the warp's 32 at a time (few registers: the softmax warps have them)
 #pragma unroll
-                for (int i = 0; i < IT; ++i) {
-                    const uint32_t c[4] = {other ? codes[i].z : codes[i].x, other ? codes[i].w : codes[i].y,
-                                           other ? codes[i].x : codes[i].z, other ? codes[i].y : codes[i].w};
-                    const uint32_t s0 = e2m1_scale_h2(other ? sc[i] >> 8 : sc[i] & 0xffu), s1 = e2m1_scale_h2(other ? sc[i] & 0xffu : sc[i] >> 8);
+                for (int half = 0; half < 2; ++half) {
+                    constexpr int N = IT / 2;
+                    uint4 codes[N];
+                    uint32_t sc[N];   // two bytes
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t h[4];
-                        e2m1_values(c[e], e < 2 ? s0 : s1, h);
-                        *reinterpret_cast<uint4 *>(to + i * (STEP * 128) + ((chunk0 ^ e) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int i = 0; i < N; ++i) {
+                        codes[i] = make_uint4(0u, 0u, 0u, 0u);
+                        sc[i] = 0u;
+                        const int row = row0 + half * 16 + i * 8;
+                        if (!mine) continue;
+                        codes[i] = *reinterpret_cast<const uint4 *>(src + code_at + half * code_step + i * 4 * p.d);
+                        if (row < left && !((bad >> (row >> 4)) & 1u))
+                            sc[i] = *reinterpret_cast<const uint16_t *>(src + scale_at + half * scale_step + i * (p.d / 2));
+                    }
+                    if (half == 0) {
+                        if (g >= S::NS && !wwait(bar(S::BAR_EMPTY + slot), (g / S::NS - 1) & 1, 75)) return;
+                    } else {
+                        signal(S::BAR_GEMPTY + st);   // (what the tile held is in registers)
+                    }
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const uint32_t c[4] = {other ? codes[i].z : codes[i].x, other ? codes[i].w : codes[i].y,
+                                               other ? codes[i].x : codes[i].z, other ? codes[i].y : codes[i].w};
+                        const uint32_t s0 = e2m1_scale_h2(other ? sc[i] >> 8 : sc[i] & 0xffu), s1 = e2m1_scale_h2(other ? sc[i] & 0xffu : sc[i] >> 8);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t h[4];
+                            e2m1_values(c[e], e < 2 ? s0 : s1, h);
+                            *reinterpret_cast<uint4 *>(to + (half * 16 + i * 8) * 128 + ((chunk0 ^ e) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
                 fence_proxy_async_smem();
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
             return __all_sync(0xffffffffu, mbar_wait(b, parity, abort_flag, p.err, site));
         };
         const bool leader = elect_one();
-        if constexpr (Q4) regs_dec<kRegsOther>();
+        if constexpr (Q4) regs_dec<regs_other(DP)>();
         if (Q4 && warp >= S::WARP_TMV) {
             if (warp >= S::WARP_CONV)
                 convert_tiles<DP>(p, gm, sbase, smem, units, bad_pages, warp - S::WARP_CONV, unit_wait, unit_done, wwait);
@@ -614,7 +623,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
         // ------------------------------------------------------------------
         // Softmax warpgroup h of query tile q.
         // ------------------------------------------------------------------
-        if constexpr (Q4) regs_inc<kRegsSoftmax>();
+        if constexpr (Q4) regs_inc<regs_softmax(DP)>();
         const int q = warp >> 3, h = (warp >> 2) & 1, wq = warp & 3;
         const int row_in = wq * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(wq * 32) << 16;
