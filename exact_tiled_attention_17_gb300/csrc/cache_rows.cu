@@ -9,10 +9,12 @@
 //
 // 4-bit rows (e2m1.cuh): 16 columns share a scale.
 //
-// A lane owns 16 columns of a row: two runs of 8, contiguous, or (halves rotated)
-// 8 columns of the lower half and their partners in the upper one, so a pair is
-// in one lane and a group of 16 columns in two neighbouring ones.  All lanes of a
-// row are in one warp.
+// A CTA takes TOK consecutive tokens; warp w finds where token w lies.  A lane owns 16
+// columns of a row: two runs of 8, contiguous, or (halves rotated) 8 columns of the
+// lower half and their partners in the upper one, so a pair is in one lane and a group
+// of 16 columns in two neighbouring ones.  All lanes of a row are in one warp.  The
+// CTA's threads go through the rows of all its tokens in one line, each with the next
+// two on their way.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -26,6 +28,7 @@ namespace eta {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kManyTokens = 8;   // to a CTA, where there are many; else one
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_done() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -121,10 +124,10 @@ struct Run8<__nv_bfloat16> {
             x[2 * e + 1] = bf16hi_to_f32(u[e]);
         }
     }
-    static __device__ __forceinline__ void put(char *p, const float (&x)[8]) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                                   pack_bf16x2(x[6], x[7]));
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
+    static __device__ __forceinline__ void put(char *p, const float (&x)[8]) { *reinterpret_cast<uint4 *>(p) = pack(x); }
     static __device__ __forceinline__ float one(const char *p) { return __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p)); }
 };
 template <>
@@ -142,6 +145,7 @@ struct Run8<float> {
         *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<float4 *>(p + 16) = make_float4(x[4], x[5], x[6], x[7]);
     }
+    static __device__ __forceinline__ uint4 pack(const float (&)[8]) { return make_uint4(0, 0, 0, 0); }   // (16-bit rows only)
     static __device__ __forceinline__ float one(const char *p) { return *reinterpret_cast<const float *>(p); }
 };
 
@@ -151,62 +155,83 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
     a = x;
 }
 
+// 32 bytes to 32-byte aligned memory in one piece (whole sectors), or in two to what is aligned to 16.
+__device__ __forceinline__ void put32(char *dst, const uint4 &a, const uint4 &b) {
+    if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                     "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4 *>(dst) = a;
+        *reinterpret_cast<uint4 *>(dst + 16) = b;
+    }
+}
+
+// How columns are paired.  Halves: of a multiple of 16 columns each, so that a
+// lane holds whole pairs; others, whose partners a lane reads one by one.
+enum class Turn { kNone, kHalves, kNeighbours, kOddHalves };
+
+// A row of a CTA's tokens; the CTA's threads step through them together.
+struct RowAt {
+    int tok, row;
+    __device__ __forceinline__ void next(int step, int rows) {
+        row += step;
+        while (row >= rows) {
+            row -= rows;
+            ++tok;
+        }
+    }
+};
+
 // T: the type of the rows that come in.  Q4: the cache holds 4-bit values.
-template <typename T, bool Q4, int TOK>
-__global__ void __launch_bounds__(kRowThreads) append_rows_kernel(const CacheView c, int layer, const RowIn in, const RowList li,
-                                                                  const Rotation r, int *err) {
+template <typename T, bool Q4, Turn TURN, int TOK>
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 4 : 3) append_rows_kernel(const CacheView c, int layer, const RowIn in,
+                                                                                          const RowList li, const Rotation r, int *err) {
     static_assert(TOK <= kRowThreads / 32, "one warp finds one token's place");
     constexpr int ES = sizeof(T);
     __shared__ Place places[TOK];
     pdl_wait();
     const int t0 = blockIdx.x * TOK, ntok = min(TOK, li.T - t0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lpr = 1 << in.lane_shift;              // lanes of a row (d / 16, up to a power of two)
-    const int rows = 2 * c.heads + in.Hq;            // of a token: K, V, Q
-    const int items = ntok * rows * lpr;
-    const int l = threadIdx.x & (lpr - 1);
-    const bool halves = r.dims > 0 && !r.neighbours, fast = halves && r.dims % 32 == 0;
+    const int turning = c.heads + in.Hq, rows = turning + c.heads;    // of a token: K, Q, V
+    const int lpr = 1 << in.lane_shift, l = threadIdx.x & (lpr - 1);   // lanes of a row (d / 16, up to a power of two)
+    const int step = kRowThreads >> in.lane_shift;                     // rows that the CTA takes at once
     const int half = r.dims / 2;
+    const bool mine = 16 * l < in.d;
+    const bool mixed = TURN == Turn::kHalves && 16 * l < r.dims;       // this lane's runs of a turning row are a half apart
 
-    // what a lane works on: the row's address, its first columns, whether it turns
+    auto address = [&](const RowAt &a) -> const char * {
+        const long long t = t0 + a.tok;
+        return a.row < c.heads ? in.K + t * in.token_bytes + a.row * in.head_bytes
+               : a.row < turning ? in.Q + t * in.q_token_bytes + (a.row - c.heads) * in.q_head_bytes
+                                 : in.V + t * in.token_bytes + (a.row - turning) * in.head_bytes;
+    };
     struct Item {
-        const char *src;
-        int tok, row, c0, c1;
-        bool rot;
         Run8<T> x0, x1;
     };
-    auto fetch = [&](int at, Item &w) {
-        w.tok = -1;
+    RowAt ahead{0, 0};
+    ahead.next(static_cast<int>(threadIdx.x) >> in.lane_shift, rows);
+    RowAt now = ahead;
+    auto fetch = [&](Item &w) {
         w.x0.zero();
         w.x1.zero();
-        w.c0 = 16 * l;
-        w.c1 = 16 * l + 8;
-        w.rot = false;
-        w.row = 0;
-        w.src = nullptr;
-        if (at >= items || 16 * l >= in.d) return;
-        const int y = at >> in.lane_shift;
-        w.tok = y / rows;
-        w.row = y - w.tok * rows;
-        const long long t = t0 + w.tok;
-        if (w.row < c.heads) w.src = in.K + t * in.token_bytes + w.row * in.head_bytes;
-        else if (w.row < 2 * c.heads) w.src = in.V + t * in.token_bytes + (w.row - c.heads) * in.head_bytes;
-        else w.src = in.Q + t * in.q_token_bytes + (w.row - 2 * c.heads) * in.q_head_bytes;
-        w.rot = w.c0 < r.dims && (w.row < c.heads || w.row >= 2 * c.heads);
-        if (w.rot && fast) {
-            w.c0 = 8 * l;
-            w.c1 = half + 8 * l;
+        if (ahead.tok < ntok && mine) {
+            const char *src = address(ahead);
+            const bool m = mixed && ahead.row < turning;
+            w.x0.load(src + (m ? 8 * l : 16 * l) * ES);
+            w.x1.load(src + (m ? half + 8 * l : 16 * l + 8) * ES);
         }
-        w.x0.load(w.src + w.c0 * ES);
-        w.x1.load(w.src + w.c1 * ES);
+        ahead.next(step, rows);
     };
-    Item cur;
-    fetch(threadIdx.x, cur);
+    // (rows do not depend on where they go: the first are read before the places are known)
+    Item buf[2];
+    fetch(buf[0]);
+    fetch(buf[1]);
     if (warp < TOK) {
         Place p{-1, 0, 0};
         if (t0 + warp < li.T) {
             p = find_place<true>(c, li, layer, t0 + warp, err);
-            if (r.dims > 0 && p.block >= 0) {
+            if (TURN != Turn::kNone && p.block >= 0) {
                 if (r.positions) p.pos = r.positions[t0 + warp];
                 if (p.pos < 0 || p.pos >= r.rows) {   // no such row of the table
                     p.block = -1;
@@ -219,93 +244,110 @@ __global__ void __launch_bounds__(kRowThreads) append_rows_kernel(const CacheVie
     if (blockIdx.x == 0 && warp == kRowThreads / 32 - 1) check_ranges(li, err);
     __syncthreads();
 
-    for (int at = threadIdx.x; at - static_cast<int>(threadIdx.x) < items; at += kRowThreads) {
-        Item w = cur;
-        fetch(at + kRowThreads, cur);
-        const Place p = w.tok >= 0 ? places[w.tok] : Place{-1, 0, 0};
-        const bool live = p.block >= 0;
+    auto finish = [&](const Item &w) {
+        const Place p = now.tok < ntok ? places[now.tok] : Place{-1, 0, 0};
+        const bool live = mine && p.block >= 0, turns = now.row < turning, m = mixed && turns;
+        const int c0 = m ? 8 * l : 16 * l, c1 = m ? half + 8 * l : 16 * l + 8;
         float x0[8], x1[8];
         w.x0.get(x0);
         w.x1.get(x1);
-        if (w.rot && live) {
+        if (TURN != Turn::kNone && live && turns) {
             const float *cs = r.table + static_cast<long long>(p.pos) * r.dims;
-            if (fast) {
-                float co[8], si[8];
+            if constexpr (TURN == Turn::kHalves) {
+                if (m) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 a = __ldg(reinterpret_cast<const float4 *>(cs + w.c0 + e));
-                    const float4 b = __ldg(reinterpret_cast<const float4 *>(cs + half + w.c0 + e));
-                    co[e] = a.x, co[e + 1] = a.y, co[e + 2] = a.z, co[e + 3] = a.w;
-                    si[e] = b.x, si[e + 1] = b.y, si[e + 2] = b.z, si[e + 3] = b.w;
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 a = __ldg(reinterpret_cast<const float4 *>(cs + c0 + e));
+                        const float4 b = __ldg(reinterpret_cast<const float4 *>(cs + half + c0 + e));
+                        turn(x0[e], x1[e], a.x, b.x);
+                        turn(x0[e + 1], x1[e + 1], a.y, b.y);
+                        turn(x0[e + 2], x1[e + 2], a.z, b.z);
+                        turn(x0[e + 3], x1[e + 3], a.w, b.w);
+                    }
                 }
+            } else if constexpr (TURN == Turn::kNeighbours) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) turn(x0[e], x1[e], co[e], si[e]);
-            } else if (!halves) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    if (w.c0 + e < r.dims) turn(x0[e], x0[e + 1], __ldg(cs + (w.c0 + e) / 2), __ldg(cs + half + (w.c0 + e) / 2));
-                    if (w.c1 + e < r.dims) turn(x1[e], x1[e + 1], __ldg(cs + (w.c1 + e) / 2), __ldg(cs + half + (w.c1 + e) / 2));
+                for (int e = 0; e < 4; ++e) {
+                    const int i = c0 / 2 + e, k = c1 / 2 + e;
+                    if (i < half) turn(x0[2 * e], x0[2 * e + 1], __ldg(cs + i), __ldg(cs + half + i));
+                    if (k < half) turn(x1[2 * e], x1[2 * e + 1], __ldg(cs + k), __ldg(cs + half + k));
                 }
             } else {
-                // halves that do not fall on runs of 16: the partners are read one by one
+                const char *src = address(now);
                 auto other = [&](float &x, int col) {
                     if (col >= r.dims) return;
                     const bool lower = col < half;
                     const int j = lower ? col : col - half;
-                    float y = Run8<T>::one(w.src + (lower ? col + half : j) * ES);
+                    float y = Run8<T>::one(src + (lower ? col + half : j) * ES);
                     const float co = __ldg(cs + j), si = __ldg(cs + half + j);
                     if (lower) turn(x, y, co, si);
                     else turn(y, x, co, si);
                 };
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    other(x0[e], w.c0 + e);
-                    other(x1[e], w.c1 + e);
+                    other(x0[e], c0 + e);
+                    other(x1[e], c1 + e);
                 }
             }
         }
         __syncwarp();   // (Q may be turned in place: every lane of the row has read what it needs)
+        const bool v = !turns, query = turns && now.row >= c.heads;
+        const int h = v ? now.row - turning : now.row;
         if constexpr (Q4) {
             // the groups of columns c0 and c1: one lane's own 16 columns, or 8 of this lane and 8 of its neighbour
             uint32_t a0 = e2m1_amax(x0), a1 = e2m1_amax(x1);
             const uint32_t n0 = __shfl_xor_sync(0xffffffffu, a0, 1), n1 = __shfl_xor_sync(0xffffffffu, a1, 1);
-            const bool split = w.rot && fast;
-            a0 = max(a0, split ? n0 : a1);
-            a1 = split ? max(a1, n1) : a0;
-            if (live && w.row < 2 * c.heads) {
-                const bool v = w.row >= c.heads;
-                const int h = v ? w.row - c.heads : w.row;
+            a0 = max(a0, m ? n0 : a1);
+            a1 = m ? max(a1, n1) : a0;
+            if (live && !query) {
                 char *blk = reinterpret_cast<char *>(v ? c.v : c.k) + p.block + h * c.head_stride_vecs * 16;
                 char *codes = blk + p.slot * (in.d / 2);
                 char *scales = blk + c.page_size * (in.d / 2) + p.slot * (in.d / 16);
                 const int s0 = e2m1_scale(a0), s1 = e2m1_scale(a1);
-                *reinterpret_cast<uint32_t *>(codes + w.c0 / 2) = e2m1_pack(x0, s0);
-                *reinterpret_cast<uint32_t *>(codes + w.c1 / 2) = e2m1_pack(x1, s1);
-                if (!split) scales[l] = static_cast<char>(s0);
-                else if (l & 1) scales[w.c1 / 16] = static_cast<char>(s1);
-                else scales[w.c0 / 16] = static_cast<char>(s0);
+                const uint32_t w0 = e2m1_pack(x0, s0), w1 = e2m1_pack(x1, s1);
+                if (m) {
+                    *reinterpret_cast<uint32_t *>(codes + c0 / 2) = w0;
+                    *reinterpret_cast<uint32_t *>(codes + c1 / 2) = w1;
+                    scales[l & 1 ? c1 / 16 : c0 / 16] = static_cast<char>(l & 1 ? s1 : s0);
+                } else {
+                    *reinterpret_cast<uint2 *>(codes + c0 / 2) = make_uint2(w0, w1);
+                    scales[l] = static_cast<char>(s0);
+                }
             }
-        } else if (live && w.row < 2 * c.heads) {
-            const bool v = w.row >= c.heads;
-            const int h = v ? w.row - c.heads : w.row;
-            char *dst = reinterpret_cast<char *>(v ? c.v : c.k) + p.block + (h * c.head_stride_vecs + p.slot * c.slot_stride_vecs) * 16;
-            Run8<T>::put(dst + w.c0 * ES, x0);
-            Run8<T>::put(dst + w.c1 * ES, x1);
         }
-        if (live && w.row >= 2 * c.heads) {
-            char *dst = in.Qout + (t0 + w.tok) * in.o_token_bytes + (w.row - 2 * c.heads) * in.o_head_bytes;
-            Run8<T>::put(dst + w.c0 * ES, x0);
-            Run8<T>::put(dst + w.c1 * ES, x1);
+        if (live && (query || !Q4)) {
+            char *dst = query ? in.Qout + (t0 + now.tok) * in.o_token_bytes + (h - c.heads) * in.o_head_bytes
+                              : reinterpret_cast<char *>(v ? c.v : c.k) + p.block + (h * c.head_stride_vecs + p.slot * c.slot_stride_vecs) * 16;
+            if (ES == 2 && !m) {
+                put32(dst + c0 * ES, Run8<T>::pack(x0), Run8<T>::pack(x1));
+            } else {
+                Run8<T>::put(dst + c0 * ES, x0);
+                Run8<T>::put(dst + c1 * ES, x1);
+            }
+        }
+        now.next(step, rows);
+    };
+    // (whole warps: a row's lanes are in one, and the first row of the CTA's is the first to reach an end)
+    const int rounds = (ntok * rows + step - 1) / step;
+    for (int k = 0; k < rounds; k += 2) {
+        const Item a = buf[0];
+        fetch(buf[0]);
+        finish(a);
+        if (k + 1 < rounds) {
+            const Item b = buf[1];
+            fetch(buf[1]);
+            finish(b);
         }
     }
     pdl_done();
 }
 
-// Reading: a lane takes 16 columns of a 4-bit row, or a 16-byte piece of another.
+// Reading: a lane takes 16 columns of a 4-bit row, or a 16-byte piece of another, four of them at once.
 template <bool Q4, int TOK>
 __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const CacheView c, int layer, const RowOut out, const RowList li,
                                                                 int *err) {
     static_assert(TOK <= kRowThreads / 32, "one warp finds one token's place");
+    constexpr int U = 4;
     __shared__ Place places[TOK];
     pdl_wait();
     const int t0 = blockIdx.x * TOK, ntok = min(TOK, li.T - t0);
@@ -318,30 +360,47 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const CacheView 
     if (blockIdx.x == 0 && warp == kRowThreads / 32 - 1) check_ranges(li, err);
     __syncthreads();
     const int per = Q4 ? out.d / 16 : c.row_vecs, rows = 2 * c.heads, items = ntok * rows * per;
-    for (int at = threadIdx.x; at < items; at += kRowThreads) {
-        const int y = at / per, l = at - y * per, tok = y / rows, row = y - tok * rows;
-        const Place p = places[tok];
-        if (p.block < 0) continue;
-        const bool v = row >= c.heads;
-        const int h = v ? row - c.heads : row;
-        const char *blk = reinterpret_cast<const char *>(v ? c.v : c.k) + p.block + h * c.head_stride_vecs * 16;
-        char *dst = (v ? out.V : out.K) + (t0 + tok) * out.token_bytes + h * out.head_bytes;
-        if constexpr (Q4) {
-            const uint2 codes = *reinterpret_cast<const uint2 *>(blk + p.slot * (out.d / 2) + 8 * l);
-            const uint32_t s2 = e2m1_scale_h2(*reinterpret_cast<const uint8_t *>(blk + c.page_size * (out.d / 2) + p.slot * (out.d / 16) + l));
-            uint32_t h2[8], w[8];
-            e2m1_values(codes.x, s2, h2);
-            e2m1_values(codes.y, s2, h2 + 4);
+    for (int at0 = threadIdx.x; at0 < items; at0 += U * kRowThreads) {
+        uint4 x[U];
+        uint32_t sc[U];
+        char *to[U];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {   // (at most 6 significant bits: exact in bf16)
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(h2 + e));
-                w[e] = pack_bf16x2(f.x, f.y);
+        for (int u = 0; u < U; ++u) {
+            const int at = at0 + u * kRowThreads;
+            to[u] = nullptr;
+            if (at >= items) continue;
+            const int y = at / per, l = at - y * per, tok = y / rows, row = y - tok * rows;
+            const Place p = places[tok];
+            if (p.block < 0) continue;
+            const bool v = row >= c.heads;
+            const int h = v ? row - c.heads : row;
+            const char *blk = reinterpret_cast<const char *>(v ? c.v : c.k) + p.block + h * c.head_stride_vecs * 16;
+            to[u] = (v ? out.V : out.K) + (t0 + tok) * out.token_bytes + h * out.head_bytes + l * (Q4 ? 32 : 16);
+            if constexpr (Q4) {
+                const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(blk + p.slot * (out.d / 2) + 8 * l));
+                x[u].x = w.x;
+                x[u].y = w.y;
+                sc[u] = *reinterpret_cast<const uint8_t *>(blk + c.page_size * (out.d / 2) + p.slot * (out.d / 16) + l);
+            } else {
+                x[u] = __ldcs(reinterpret_cast<const uint4 *>(blk + p.slot * c.slot_stride_vecs * 16 + 16 * l));
             }
-            uint4 *to = reinterpret_cast<uint4 *>(dst + 32 * l);
-            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-            reinterpret_cast<uint4 *>(dst)[l] = *reinterpret_cast<const uint4 *>(blk + p.slot * c.slot_stride_vecs * 16 + 16 * l);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!to[u]) continue;
+            if constexpr (Q4) {
+                uint32_t h2[8], w[8];
+                e2m1_values(x[u].x, e2m1_scale_h2(sc[u]), h2);
+                e2m1_values(x[u].y, e2m1_scale_h2(sc[u]), h2 + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {   // (at most 6 significant bits: exact in bf16)
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(h2 + e));
+                    w[e] = pack_bf16x2(f.x, f.y);
+                }
+                put32(to[u], make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+            } else {
+                *reinterpret_cast<uint4 *>(to[u]) = x[u];
+            }
         }
     }
     pdl_done();
@@ -349,11 +408,21 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const CacheView 
 
 unsigned blocks(int T, int tok) { return static_cast<unsigned>((static_cast<long long>(T) + tok - 1) / tok); }
 
+template <typename T, bool Q4, Turn TURN>
+int launch_turn(const CacheView &c, int layer, const RowIn &in, const RowList &li, const Rotation &r, int *err, cudaStream_t stream) {
+    if (li.T <= 1024)
+        return launch_dependent(append_rows_kernel<T, Q4, TURN, 1>, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, in, li, r, err);
+    return launch_dependent(append_rows_kernel<T, Q4, TURN, kManyTokens>, dim3(blocks(li.T, kManyTokens)), kRowThreads, 0, stream, c, layer,
+                            in, li, r, err);
+}
 template <typename T, bool Q4>
 int launch_append(const CacheView &c, int layer, const RowIn &in, const RowList &li, const Rotation &r, int *err, cudaStream_t stream) {
-    if (li.T <= 4096)
-        return launch_dependent(append_rows_kernel<T, Q4, 2>, dim3(blocks(li.T, 2)), kRowThreads, 0, stream, c, layer, in, li, r, err);
-    return launch_dependent(append_rows_kernel<T, Q4, 8>, dim3(blocks(li.T, 8)), kRowThreads, 0, stream, c, layer, in, li, r, err);
+    if constexpr (Q4) {
+        if (r.dims == 0) return launch_turn<T, Q4, Turn::kNone>(c, layer, in, li, r, err, stream);
+    }
+    if (r.neighbours) return launch_turn<T, Q4, Turn::kNeighbours>(c, layer, in, li, r, err, stream);
+    if (r.dims % 32 == 0) return launch_turn<T, Q4, Turn::kHalves>(c, layer, in, li, r, err, stream);
+    return launch_turn<T, Q4, Turn::kOddHalves>(c, layer, in, li, r, err, stream);
 }
 
 }  // namespace
@@ -370,11 +439,12 @@ int launch_cache_rows_in(const CacheView &c, int layer, RowIn in, const RowList 
 int launch_cache_rows_out(const CacheView &c, int layer, const RowOut &out, const RowList &li, cudaStream_t stream) {
     int *err = device_error_word();
     if (!err) return kErrCuda;
-    auto go = [&](auto kern, int tok) {
-        return launch_dependent(kern, dim3(blocks(li.T, tok)), kRowThreads, 0, stream, c, layer, out, li, err);
+    auto go = [&](auto one, auto many) {
+        if (li.T <= 1024) return launch_dependent(one, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, out, li, err);
+        return launch_dependent(many, dim3(blocks(li.T, kManyTokens)), kRowThreads, 0, stream, c, layer, out, li, err);
     };
-    if (c.bits == 4) return go(read_rows_kernel<true, 4>, 4);
-    return go(read_rows_kernel<false, 4>, 4);
+    return c.bits == 4 ? go(read_rows_kernel<true, 1>, read_rows_kernel<true, kManyTokens>)
+                       : go(read_rows_kernel<false, 1>, read_rows_kernel<false, kManyTokens>);
 }
 
 }  // namespace eta
