@@ -181,7 +181,10 @@ __device__ __forceinline__ void convert_tiles(const PagedParams &p, const PagedG
                     if (half == 0) {
                         if (g >= S::NS && !wwait(bar(S::BAR_EMPTY + slot), (g / S::NS - 1) & 1, 75)) return;
                     } else {
-                        signal(S::BAR_GEMPTY + st);   // (what the tile held is in registers)
+                        // (the reads are done before the next copy may write there: without the fence
+                        // the arrival overtook reads that the matrix instruction's kept waiting)
+                        fence_proxy_async_smem();
+                        signal(S::BAR_GEMPTY + st);
                     }
 #pragma unroll
                     for (int i = 0; i < N; ++i) {

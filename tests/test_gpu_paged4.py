@@ -318,3 +318,60 @@ def test_graph_of_a_step(eta):
         assert ((o.cpu().double() - want).abs() <= 2.0 ** -8 * (size + want.abs()) * 1.05).all()
         assert ((lse.cpu().double() - torch.logsumexp(s, 2)).abs() <= 1e-4).all()
     assert eta.attn_status() == 0 and cache.seq_lens.tolist() == [40] * B
+
+
+def fill(cache, lens, gen, size=1.0):
+    """Random 4-bit values for whole sequences, through the append."""
+    for r, n in enumerate(lens):
+        x = (size * torch.randn((n, 2 * cache.heads, cache.d), generator=gen, device="cuda")).to(BF16)
+        eta_append(cache, x[:, :cache.heads], x[:, cache.heads:], r, n)
+
+
+def eta_append(cache, k, v, r, n):
+    import exact_tiled_attention_17_gb300 as m
+    m.attn_cache_append(cache, 0, k, v, ints([r]), ints([0, n]))
+
+
+@pytest.mark.parametrize("lens,new,heads,g,d,page", [
+    ([5200, 3100, 4500], [640, 511, 300], 8, 4, 128, 64),
+    ([5200, 3100, 4500], [640, 511, 300], 8, 4, 64, 16),
+    ([4000, 2500], [400, 513], 6, 5, 96, 32),
+    ([6000, 100], [300, 100], 4, 8, 32, 256),
+    ([30000], [140], 4, 4, 128, 16),
+    ([3000 + 61 * i for i in range(32)], [1] * 32, 8, 4, 128, 64),
+    ([3000 + 61 * i for i in range(32)], [1] * 32, 8, 2, 64, 16),
+    ([2000 + 61 * i for i in range(24)], [4] * 24, 4, 4, 128, 32),
+    ([2000 + 61 * i for i in range(24)], [1] * 24, 4, 7, 96, 128),
+])
+def test_large_batches_again_and_again(eta, lens, new, heads, g, d, page):
+    """Many units to a CTA and full pipelines: every output against the definition in float64 (on the GPU), and the same
+    bits each time.  Weights are rounded once to float16 (2^-11), O to bf16 (2^-8), a weight is off by 2^-32 of the
+    largest at least, and sums of up to 2^15 float32 numbers add 2^-9 at most where all errors have one sign."""
+    gen = torch.Generator(device="cuda").manual_seed(d + page)
+    cache = eta.PagedCache.empty(1, sum(-(-n // page) for n in lens) + 5, heads, page, d, len(lens), max(lens) // page + 2, dtype=E2M1)
+    for pool in (cache.k, cache.v):
+        pool.fill_(255)
+    assert eta.attn_cache_reserve(cache, ints(list(range(len(lens)))), ints(lens)).tolist() == [1] * len(lens)
+    fill(cache, lens, gen)
+    T, Hq, at = sum(new), heads * g, starts(new)
+    q = (1.5 * torch.randn((T, Hq, d), generator=gen, device="cuda")).to(BF16)
+    runs = [eta.attn_paged_fwd(q, cache, 0, None, ints(at), max_q=max(new)) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert eta.attn_status() == 0
+    for o, lse in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+    o, lse = runs[0]
+    for i, n in enumerate(lens):
+        k, v = eta.attn_cache_read(cache, 0, ints([i]), ints([0, n]), n)
+        a, b = at[i], at[i + 1]
+        see = torch.arange(n, device="cuda")[None] <= n - (b - a) + torch.arange(b - a, device="cuda")[:, None]
+        for h in range(heads):
+            kd, vd = k[:, h].double(), v[:, h].double()
+            for j in range(h * g, h * g + g):
+                s = (q[a:b, j].double() @ kd.T / math.sqrt(d)).masked_fill(~see, -math.inf)
+                w = torch.softmax(s, 1)
+                want, size = w @ vd, w @ vd.abs()
+                tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -9) * size + 2.0 ** -32 * vd.abs().sum(0)
+                err = (o[a:b, j].double() - want).abs()
+                assert (err <= tol).all(), f"entry {i}, head {j}: off by {(err / tol).max():.3g} of the bound"
+                assert ((lse[a:b, j].double() - torch.logsumexp(s, 1)).abs() <= 1e-4).all()
