@@ -73,7 +73,8 @@ def test_long_and_split(eta, n, new):
 
 
 @pytest.mark.parametrize("d", [32, 64, 96, 128])
-@pytest.mark.parametrize("g,new", [(1, 1), (3, 1), (2, 2), (8, 1), (1, 7), (5, 2), (4, 4), (3, 9), (8, 4), (17, 1), (16, 2), (11, 3)])
+@pytest.mark.parametrize("g,new", [(1, 1), (3, 1), (2, 2), (8, 1), (1, 7), (5, 2), (4, 4), (3, 9), (8, 4), (17, 1), (16, 2), (11, 3),
+                                   (6, 5), (9, 3), (13, 2)])
 def test_few_rows(eta, d, g, new):
     """Every size of the units for few rows: short lengths, ends inside a tile, entries with less than the most tokens."""
     lens = [1, 700, 2, 15, 33, 0, 64, 65, 5, 1291]
