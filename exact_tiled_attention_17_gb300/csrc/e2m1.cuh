@@ -99,5 +99,9 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, uint32_t scale2, uint32_
 __device__ __forceinline__ int f16_shift(uint32_t top) {
     return top == 0u ? 0 : min(14 + 127 - static_cast<int>(top >> 23), 126);
 }
+// What turns a product with such a row back into a score; a number, or a score of 0 would be NaN.
+__device__ __forceinline__ float f16_back(float scale, int up) {
+    return fminf(scale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), 3.402823466e+38f);
+}
 
 }  // namespace eta

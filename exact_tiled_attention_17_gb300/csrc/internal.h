@@ -92,7 +92,7 @@ int launch_decode(const void *Q, const void *K, const void *V, void *O, float *L
                   int d, int causal, float scale, int bf16, const float *key_mask, void *workspace,
                   cudaStream_t stream);
 
-// Attention of new tokens over a paged cache (paged_*.cu); the parameters are
+// Attention of new tokens over a paged cache (paged_*.cu, paged4_*.cu; bits: of a cached value); the parameters are
 // in paged.cuh.
 constexpr int kPagedMaxTcCtas = 160;       // CTAs a launch may use (sizes the workspace): one per SM,
 constexpr int kPagedMaxDecodeCtas = 320;   // two,

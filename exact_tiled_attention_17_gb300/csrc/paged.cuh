@@ -20,7 +20,7 @@ struct PagedParams {
     void *O;
     float *LSE;                                    // [T][Hq] or null
     long long q_token, q_head, o_token, o_head;    // strides of Q and O, in elements
-    long long page_stride, head_stride, slot_stride;   // strides of one layer's K and V, in elements
+    long long page_stride, head_stride, slot_stride;   // strides of one layer's K and V, in elements (4-bit values: bytes)
     int d, Hq;
     float scale_log2;                              // scale * log2(e)
     // Partial results of units that a share's border cuts: CTA c has slot 2c
@@ -230,7 +230,7 @@ __device__ __forceinline__ PagedHdr paged_read_header(const PagedParams &p, int 
 int launch_paged_merge(const PagedParams &p, int bf16, int ctas, int sms, cudaStream_t stream);
 
 // Rows of a unit (sizes the workspace too).  The stream kernel: 16 or 32,
-// whichever holds an entry.  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
+// whichever holds an entry; over 4-bit values 8, or 16 (and several units to an entry).  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
 // the one that tiles).
 inline int paged_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 16 ? 16 : 32; }
 inline int paged4_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 8 ? 8 : 16; }

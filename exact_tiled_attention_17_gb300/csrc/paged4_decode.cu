@@ -35,6 +35,14 @@
 //
 // Pages that do not exist are not copied and their keys skipped; masked scores are
 // replaced by -inf; scales of slots past the end, which may hold anything, by 0.
+//
+// Measured, 64 sequences of 2048 .. 8191 tokens, 8 kv heads of 128, 4 query heads to
+// each: 397 MB in 80 us, 0.74 of the measured copy rate (a bf16 cache: 219 us).  The
+// copies alone take 75 and the arithmetic alone 81 (graph replays of 85): 272
+// instructions to 16 keys, of which 64 conversions (a half of the ALU's time), 64
+// multiplications and 16 matrix instructions (of the FMA pipe's).  Three CTAs an SM and
+// blocks in pairs: two CTAs 92 us, four with single blocks 101.  12 and 16 rows: 134 us.
+// 4 sequences of 300 .. 1000: 11 us, a chain of dependent reads over two launches.
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int up = f16_shift(top);
                 const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-                const float back = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                const float back = f16_back(p.scale_log2, up);
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
 #pragma unroll

@@ -1,5 +1,6 @@
 // Attention of a chunk of new tokens over a paged cache, bf16 in / f32
-// accumulate, on the tcgen05 tensor cores of sm_103a.
+// accumulate, on the tcgen05 tensor cores of sm_103a; the cache holds bf16, or 4-bit
+// values (last paragraph).
 //
 // What it computes: O = softmax(scale Q K^T) V and the row's LSE for the units
 // of paged_index.h: one kv head, a block of new tokens, all g query heads that
@@ -38,6 +39,16 @@
 // us more.  Measured: four chunks of 511 .. 1024 tokens over 4000 .. 8192 cached
 // ones, 32 query heads of 128 on 8 kv heads: 346 GFLOP in 255 us, 1.36 PFLOP/s; 128
 // tokens over 130907, 16 query heads of 64 on 4: 92 us.
+//
+// 4-bit values (Q4; e2m1.cuh).  Pages are copied as they lie, codes and scales, into
+// buffers of their own, and four warps make the ring's tiles of them: float16, which
+// holds the values exactly.  Q becomes float16 too, row by row with a power of two
+// (by the softmax warps at a unit's begin: converting warps that stopped for it cost
+// 8 us a unit), and P is 2^(s - m + 7) in float16, off by 2^-11 of itself (2^-32 of the
+// row's largest at least).  The same chunks: 333 us, 1.04 PFLOP/s; the 128 tokens: 100 us.
+// Without the conversions' arithmetic and stores 296: they share the issue slots, the
+// registers and, with the matrix instruction's operands, shared memory.  Eight
+// converting warps spill (398), two are too slow (556).
 #include <algorithm>
 #include <atomic>
 #include <mutex>
@@ -664,7 +675,7 @@ __global__ void __launch_bounds__(PtcShape<DP, Q4>::THREADS, 1)
                         return max(top, __float_as_uint(far));
                     });
                     pair_sync();   // (the exchange's memory is used again)
-                    sl2 = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+                    sl2 = f16_back(p.scale_log2, up);
                     fence_proxy_async_smem();
                     mbar_arrive(bar(S::BAR_QREADY + q));
                 }

@@ -364,7 +364,8 @@ int attn_cache_compact(const attn_cache_t *cache, int *page_table_out, int *ref_
                        void *workspace, size_t ws_bytes, void *stream);
 
 /*
- * attn_cache_append — writes the keys and values of new tokens of one layer.
+ * attn_cache_append — writes the keys and values of new tokens of one layer (of an
+ * ATTN_E2M1 cache bfloat16 rows, at most 2^19 heads, rounded to 4 bits as above).
  * Entry i of the list is sequence seqs[i] (NULL: sequence i) with the tokens
  * q_start[i] .. q_start[i+1] - 1 of Knew / Vnew; they are the sequence's last
  * tokens, so the room was reserved before.  Element (token t, head h, column
@@ -393,8 +394,8 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
  * applied to the keys on the way, and to the queries of the same tokens: a pair of
  * columns (a, b) of every row of Knew and Q becomes (a cos - b sin, b cos + a sin),
  * Vnew goes as it is.  Products and sums are rounded to float32 one by one, the
- * result once to the cache's type (to bfloat16, then no further, for the queries of
- * an ATTN_E2M1 cache; keys go from float32 to 4 bits).
+ * result once more: to the cache's type, or (ATTN_E2M1) keys to 4 bits, queries to
+ * bfloat16.
  *
  * rotation->table: [rows][dims] float32, 16-byte aligned, of each position first
  * dims / 2 cosines and then as many sines (so any scaling of the angles is the
@@ -448,7 +449,7 @@ int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout
  * a multiple, at most 64 to a head.  scale: positive, scale * log2(e) finite.
  *
  * Q, O: T rows; element (token t, head j, column c) at t * token_stride +
- * j * head_stride + c, of the cache's dtype (bases 16-byte aligned, strides
+ * j * head_stride + c, of the cache's dtype (ATTN_E2M1: bfloat16; bases 16-byte aligned, strides
  * positive multiples of 16 bytes; rows of O do not overlap, nor O and Q).  At
  * most 2^30 tokens, and T * Hq below 2^31.  LSE: [T][Hq] float32 natural log, or NULL.  Rows
  * outside q_start[0] .. q_start[n] - 1 are left as they were.  A row that
@@ -461,7 +462,12 @@ int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout
  * bf16: scores, softmax and sums in float32; probabilities are rounded to bf16
  * for the product with V, once, or where Hq / heads * max_q is at most 16 to
  * two bf16 parts (O is then off by little more than its own rounding).
- * float32: products and sums in IEEE float32, no TF32.  Both take exponentials
+ * ATTN_E2M1: the cache's values are exact in the products' float16; a row of Q
+ * is multiplied by a power of two, after which a column keeps its 8 bits down to 2^-29
+ * of the row's largest and is off by 2^-40 of it at most below; probabilities are
+ * rounded once to float16 (2^-11, or 2^-32 of the row's largest where that is more);
+ * scores, softmax and sums in float32.  Stored NaN reach every row that sees them.
+ * float32: products and sums in IEEE float32, no TF32.  All take exponentials
  * from the hardware's power of two (relative error 2^-22 at most); d in {32,
  * 64, 96, 128}.  workspace: at least attn_paged_workspace_size(Hq, heads,
  * max_q, d, dtype) bytes, 16-byte aligned.  Asynchronous: two launches.

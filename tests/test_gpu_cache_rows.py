@@ -377,3 +377,87 @@ def test_python_refusals(eta):
     with pytest.raises(ValueError):
         cache_of(eta, BF16, [20], 2, 16, 64).parts(cache.k)
     assert eta.attn_status() == eta.ATTN_OK
+
+
+@pytest.mark.parametrize("store", [BF16, F32, E2M1])
+def test_more_entries_than_few(eta, store):
+    """More tokens than the few-token variants take, one or two to an entry, entries in another order than the table."""
+    rng = random.Random(5)
+    n, heads, d = 1100, 2, 64
+    lens = [rng.randint(2, 20) for _ in range(n)]
+    seqs, new = rng.sample(range(n), n), [rng.randint(0, 2) for _ in range(n)]
+    cache = cache_of(eta, store, lens, heads, 16, d, seed=3)
+    T, at = sum(new), starts(new)
+    q, k, v = (rows(T, h, d, cache.dtype, 7 + h) for h in (4, heads, heads))
+    table = angles(32, d)
+    pos = torch.cat([torch.arange(lens[r] - m, lens[r]) for r, m in zip(seqs, new)])
+    out = eta.attn_cache_append_rotated(cache, 0, k, v, ints(seqs), ints(at), table, q=q)
+    rk, rv = eta.attn_cache_read(cache, 0, ints(seqs), ints(at), T)
+    torch.cuda.synchronize()
+    assert eta.attn_status() == eta.ATTN_OK
+    same(out.cpu(), turned(q, table, pos, False).to(cache.dtype), "q")
+    for got, x in ((rk, turned(k, table, pos, False)), (rv, v.cpu().float())):
+        same(got.cpu(), (values(*quantize(x)) if store == E2M1 else x).to(cache.dtype), "read back")
+
+
+def test_far_into_a_large_pool(eta):
+    """Pages that lie more than 2^32 bytes into their pool: written, read and attended to."""
+    heads, page, d = 8, 64, 128
+    pages = 120000     # 4.4 GB a pool
+    cache = eta.PagedCache.empty(1, pages, heads, page, d, 2, 4, dtype=E2M1)
+    ids = [pages - 1, 3, pages - 2]
+    cache.page_table[1, :3] = ints(ids)
+    cache.ref_counts[ids] = 1
+    cache.seq_lens[1] = 150
+    for pool in (cache.k, cache.v):
+        for i in ids:
+            pool[0, i].fill_(255)
+    k, v, q = rows(150, heads, d, BF16, 1), rows(150, heads, d, BF16, 2), rows(150, heads, d, BF16, 3)
+    table = angles(150, d)
+    qs = ints([0, 150])
+    qr = eta.attn_cache_append_rotated(cache, 0, k, v, ints([1]), qs, table, q=q)
+    rk, rv = eta.attn_cache_read(cache, 0, ints([1]), qs, 150)
+    pos = torch.arange(150)
+    want_k, want_v = values(*quantize(turned(k, table, pos, False))), values(*quantize(v.cpu().float()))
+    same(rk.cpu(), want_k.bfloat16(), "k")
+    same(rv.cpu(), want_v.bfloat16(), "v")
+    for n, max_q in ((150, 150), (1, 1)):
+        o, _ = eta.attn_paged_fwd(qr[150 - n:].contiguous(), cache, 0, ints([1]), ints([0, n]), max_q=max_q)
+        s = torch.einsum("hd,nhd->hn", qr[149].cpu().double(), want_k) / math.sqrt(d)
+        w = torch.softmax(s, 1)
+        want, size = torch.einsum("hn,nhd->hd", w, want_v), torch.einsum("hn,nhd->hd", w, want_v.abs())
+        assert ((o[-1].cpu().double() - want).abs() <= 2.0 ** -8 * (want.abs() + size) * 1.05).all()
+    assert eta.attn_status() == eta.ATTN_OK
+
+
+def test_threads_share_a_cache(eta):
+    """Two threads that append to and read different sequences of one cache, each on a stream of its own."""
+    import threading
+    lens = [400, 400]
+    cache = cache_of(eta, E2M1, lens, 2, 16, 64, seed=9)
+    table = angles(400, 64)
+    failed = []
+
+    def work(r):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                k, v, q = (rows(400, h, 64, BF16, 10 * r + h) for h in (2, 2, 4))
+                v = v + r
+                for i in range(30):
+                    got = eta.attn_cache_append_rotated(cache, 0, k, v, ints([r]), ints([0, 400]), table, q=q)
+                    rk, rv = eta.attn_cache_read(cache, 0, ints([r]), ints([0, 400]), 400)
+                    stream.synchronize()
+                    want = turned(k, table, torch.arange(400), False)
+                    same(rk.cpu(), values(*quantize(want)).bfloat16(), "k")
+                    same(rv.cpu(), values(*quantize(v.cpu().float())).bfloat16(), "v")
+                    same(got.cpu(), turned(q, table, torch.arange(400), False).bfloat16(), "q")
+        except Exception as e:   # noqa: BLE001 (told to the test below)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(r,)) for r in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed[0]
+    assert eta.attn_status() == eta.ATTN_OK

@@ -376,3 +376,45 @@ def test_large_batches_again_and_again(eta, lens, new, heads, g, d, page):
                 err = (o[a:b, j].double() - want).abs()
                 assert (err <= tol).all(), f"entry {i}, head {j}: off by {(err / tol).max():.3g} of the bound"
                 assert ((lse[a:b, j].double() - torch.logsumexp(s, 1)).abs() <= 1e-4).all()
+
+
+@pytest.mark.parametrize("new,g", [(1, 4), (40, 2)])
+def test_the_largest_scales(eta, new, g):
+    """Scores of 0 under the largest scales: weights are equal, not NaN (queries above 2^15 scale it up once more)."""
+    n, d = 100, 64
+    cache, held = build4(eta, [n], 1, 16, d, seed=2)
+    zero = torch.zeros((n, 1, d), dtype=BF16, device="cuda")
+    eta.attn_cache_append(cache, 0, zero, (zero + 3), None, ints([0, n]))
+    for scale in (1.0, 1e30, 2.3e38):
+        for size in (1e-20, 1.0, 1e6, 1e30):
+            o, lse = eta.attn_paged_fwd(queries(new, g, d, 1, size), cache, 0, None, ints([0, new]), max_q=new, scale=scale)
+            assert (o == 3).all()
+            want = torch.log(torch.arange(n - new + 1, n + 1, dtype=torch.float64))[:, None]
+            assert ((lse.cpu().double() - want).abs() <= 1e-5).all()
+    assert eta.attn_status() == 0
+
+
+def test_workspaces_and_streams(eta):
+    """A workspace of the caller's, calls on two streams at once, and a captured call replayed beside an eager one."""
+    cache, held = build4(eta, [900, 40], 2, 16, 64, seed=8)
+    q = queries(2, 8, 64, 4)
+    qs = ints([0, 1, 2])
+    want, want_l = eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1)
+    need = eta.attn_paged_workspace_size(8, 2, 1, 64, E2M1)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    o, _ = eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1, workspace=ws)
+    assert torch.equal(o, want)
+    with pytest.raises(eta.AttnError):
+        eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1, workspace=ws[:need - 16])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        og, lg = eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(50):
+        graph.replay()
+        with torch.cuda.stream(side):
+            o, l = eta.attn_paged_fwd(q, cache, 0, None, qs, max_q=1)
+    torch.cuda.synchronize()
+    for a, b in ((og, want), (o, want), (lg, want_l), (l, want_l)):
+        assert torch.equal(a, b)
