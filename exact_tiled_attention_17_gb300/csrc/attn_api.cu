@@ -639,7 +639,7 @@ int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout
     if (T > 0 && !rows_apart(T, w.heads, in.token_bytes / es, in.head_bytes / es, cache->d)) return kErrArg;
     if (none) return kOk;
     if (Kout == Vout || !aligned4(first)) return kErrArg;
-    const RowOut out{static_cast<char *>(Kout), static_cast<char *>(Vout), in.token_bytes, in.head_bytes, cache->d};
+    const RowOut out{static_cast<char *>(Kout), static_cast<char *>(Vout), in.token_bytes, in.head_bytes, cache->d, 0};
     return launch_cache_rows_out(w, layer, out, li, static_cast<cudaStream_t>(stream));
 }
 

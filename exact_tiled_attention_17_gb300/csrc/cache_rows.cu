@@ -362,31 +362,36 @@ __global__ void __launch_bounds__(kRowThreads) read_rows_kernel(const CacheView 
     }
     if (blockIdx.x == 0 && warp == kRowThreads / 32 - 1) check_ranges(li, err);
     __syncthreads();
-    const int per = Q4 ? out.d / 16 : c.row_vecs, rows = 2 * c.heads, items = ntok * rows * per;
-    for (int at0 = threadIdx.x; at0 < items; at0 += U * kRowThreads) {
+    const int rows = 2 * c.heads, step = kRowThreads >> out.lane_shift;
+    const int l = threadIdx.x & ((1 << out.lane_shift) - 1);
+    const bool mine = l < (Q4 ? out.d / 16 : c.row_vecs);
+    RowAt at{0, 0};
+    at.next(static_cast<int>(threadIdx.x) >> out.lane_shift, rows);
+    while (at.tok < ntok) {
         uint4 x[U];
         uint32_t sc[U];
         char *to[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int at = at0 + u * kRowThreads;
             to[u] = nullptr;
-            if (at >= items) continue;
-            const int y = at / per, l = at - y * per, tok = y / rows, row = y - tok * rows;
-            const Place p = places[tok];
-            if (p.block < 0) continue;
-            const bool v = row >= c.heads;
-            const int h = v ? row - c.heads : row;
-            const char *blk = reinterpret_cast<const char *>(v ? c.v : c.k) + p.block + h * c.head_stride_vecs * 16;
-            to[u] = (v ? out.V : out.K) + (t0 + tok) * out.token_bytes + h * out.head_bytes + l * (Q4 ? 32 : 16);
-            if constexpr (Q4) {
-                const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(blk + p.slot * (out.d / 2) + 8 * l));
-                x[u].x = w.x;
-                x[u].y = w.y;
-                sc[u] = *reinterpret_cast<const uint8_t *>(blk + c.page_size * (out.d / 2) + p.slot * (out.d / 16) + l);
-            } else {
-                x[u] = __ldcs(reinterpret_cast<const uint4 *>(blk + p.slot * c.slot_stride_vecs * 16 + 16 * l));
+            if (at.tok < ntok && mine) {
+                const Place p = places[at.tok];
+                const bool v = at.row >= c.heads;
+                const int h = v ? at.row - c.heads : at.row;
+                const char *blk = reinterpret_cast<const char *>(v ? c.v : c.k) + p.block + h * c.head_stride_vecs * 16;
+                if (p.block >= 0) {
+                    to[u] = (v ? out.V : out.K) + (t0 + at.tok) * out.token_bytes + h * out.head_bytes + l * (Q4 ? 32 : 16);
+                    if constexpr (Q4) {
+                        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(blk + p.slot * (out.d / 2) + 8 * l));
+                        x[u].x = w.x;
+                        x[u].y = w.y;
+                        sc[u] = *reinterpret_cast<const uint8_t *>(blk + c.page_size * (out.d / 2) + p.slot * (out.d / 16) + l);
+                    } else {
+                        x[u] = __ldcs(reinterpret_cast<const uint4 *>(blk + p.slot * c.slot_stride_vecs * 16 + 16 * l));
+                    }
+                }
             }
+            at.next(step, rows);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -439,9 +444,11 @@ int launch_cache_rows_in(const CacheView &c, int layer, RowIn in, const RowList 
     return launch_append<float, false>(c, layer, in, li, r, err, stream);
 }
 
-int launch_cache_rows_out(const CacheView &c, int layer, const RowOut &out, const RowList &li, cudaStream_t stream) {
+int launch_cache_rows_out(const CacheView &c, int layer, RowOut out, const RowList &li, cudaStream_t stream) {
     int *err = device_error_word();
     if (!err) return kErrCuda;
+    out.lane_shift = 0;
+    while ((1 << out.lane_shift) < (c.bits == 4 ? out.d / 16 : c.row_vecs)) ++out.lane_shift;
     auto go = [&](auto one, auto many) {
         if (li.T <= 1024) return launch_dependent(one, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, out, li, err);
         return launch_dependent(many, dim3(blocks(li.T, kReadTokens)), kRowThreads, 0, stream, c, layer, out, li, err);

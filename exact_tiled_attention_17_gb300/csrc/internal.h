@@ -141,6 +141,7 @@ struct RowOut {
     char *K, *V;
     long long token_bytes, head_bytes;
     int d;
+    int lane_shift;   // (the launch sets it)
 };
 struct Rotation {
     const float *table;      // [rows][dims]: cosines, then sines
@@ -148,7 +149,7 @@ struct Rotation {
     int rows, dims, neighbours;   // dims 0: no rotation
 };
 int launch_cache_rows_in(const CacheView &c, int layer, RowIn in, const RowList &li, const Rotation &r, cudaStream_t stream);
-int launch_cache_rows_out(const CacheView &c, int layer, const RowOut &out, const RowList &li, cudaStream_t stream);
+int launch_cache_rows_out(const CacheView &c, int layer, RowOut out, const RowList &li, cudaStream_t stream);
 
 // FP32 backward on the CUDA cores (bwd_f32.cu); workspace: B*H*N floats.
 int launch_bwd_f32(const float *Q, const float *K, const float *V, const float *O, const float *dO, const float *LSE,
