@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
                         else block(std::true_type{}, tile, S::SPW - 1, key0);
                     }
                 }
-                // (every read of the tile has fed a matrix instruction by now, or was waited for as its condition)
+                fence_proxy_async_smem();   // (the reads are done before the next copy may write there)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_EMPTY + st));
                 if (++st == NS) {
