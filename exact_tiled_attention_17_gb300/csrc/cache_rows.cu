@@ -12,7 +12,7 @@
 // A CTA takes TOK consecutive tokens; warp w finds where token w lies.  A lane owns 16
 // columns of a row: two runs of 8, contiguous, or (halves rotated) 8 columns of the
 // lower half and their partners in the upper one, so a pair is in one lane and a group
-// of 16 columns in two neighbouring ones.  All lanes of a row are in one warp.  The
+// of 16 columns in two.  All lanes of a row are in one warp.  The
 // CTA's threads go through the rows of all its tokens in one line, each with the next
 // two on their way.
 #include <algorithm>
@@ -170,9 +170,12 @@ __device__ __forceinline__ void put32(char *dst, const uint4 &a, const uint4 &b)
     }
 }
 
-// How columns are paired.  Halves: of a multiple of 16 columns each, so that a
-// lane holds whole pairs; others, whose partners a lane reads one by one.
-enum class Turn { kNone, kHalves, kNeighbours, kOddHalves };
+// How columns are paired.  Halves of a multiple of 8 columns each, so that a lane
+// holds whole pairs; others, whose partners a lane reads one by one (4 x 1500 .. 2048
+// tokens of bf16, 48 and 52 of 128 columns: 39 and 74 us).  kHalvesApart: into 4 bits,
+// halves that end inside a group of 16 (a branch instead costs the others 52 -> 55 us).
+enum class Turn { kNone, kHalves, kHalvesApart, kNeighbours, kOddHalves };
+__host__ __device__ constexpr bool in_lane_halves(Turn t) { return t == Turn::kHalves || t == Turn::kHalvesApart; }
 
 // A row of a CTA's tokens; the CTA's threads step through them together.
 struct RowAt {
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 4 : 3) append_ro
     const int step = kRowThreads >> in.lane_shift;                     // rows that the CTA takes at once
     const int half = r.dims / 2;
     const bool mine = 16 * l < in.d;
-    const bool mixed = TURN == Turn::kHalves && 16 * l < r.dims;       // this lane's runs of a turning row are a half apart
+    const bool mixed = in_lane_halves(TURN) && 16 * l < r.dims;       // this lane's runs of a turning row are a half apart
 
     auto address = [&](const RowAt &a) -> const char * {
         const long long t = t0 + a.tok;
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 4 : 3) append_ro
         w.x1.get(x1);
         if (TURN != Turn::kNone && live && turns) {
             const float *cs = r.table + static_cast<long long>(p.pos) * r.dims;
-            if constexpr (TURN == Turn::kHalves) {
+            if constexpr (in_lane_halves(TURN)) {
                 if (m) {
 #pragma unroll
                     for (int e = 0; e < 8; e += 4) {
@@ -299,7 +302,16 @@ __global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 4 : 3) append_ro
         if constexpr (Q4) {
             // the groups of columns c0 and c1: one lane's own 16 columns, or 8 of this lane and 8 of its neighbour
             uint32_t a0 = e2m1_amax(x0), a1 = e2m1_amax(x1);
-            const uint32_t n0 = __shfl_xor_sync(0xffffffffu, a0, 1), n1 = __shfl_xor_sync(0xffffffffu, a1, 1);
+            uint32_t n0 = __shfl_xor_sync(0xffffffffu, a0, 1), n1 = __shfl_xor_sync(0xffffffffu, a1, 1);
+            if constexpr (TURN == Turn::kHalvesApart) {
+                // the halves meet inside a group: the upper half's groups are lanes (1, 2), (3, 4) ..., and the last
+                // run of the lower half goes with the first of the upper one, lane 0's
+                const int lanes = half / 8, first = lane - l;
+                n1 = __shfl_sync(0xffffffffu, a1, first + ((l & 1 ? l + 1 : l - 1) & (lpr - 1)));
+                const uint32_t x = __shfl_sync(0xffffffffu, l == 0 ? a1 : a0, first + (l == 0 ? lanes - 1 : 0));
+                if (l == 0) n1 = lanes == 1 ? a0 : x;
+                if (l == lanes - 1) n0 = x;
+            }
             a0 = max(a0, m ? n0 : a1);
             a1 = m ? max(a1, n1) : a0;
             if (live && !query) {
@@ -429,7 +441,10 @@ int launch_append(const CacheView &c, int layer, const RowIn &in, const RowList 
         if (r.dims == 0) return launch_turn<T, Q4, Turn::kNone>(c, layer, in, li, r, err, stream);
     }
     if (r.neighbours) return launch_turn<T, Q4, Turn::kNeighbours>(c, layer, in, li, r, err, stream);
-    if (r.dims % 32 == 0) return launch_turn<T, Q4, Turn::kHalves>(c, layer, in, li, r, err, stream);
+    if constexpr (Q4) {
+        if (r.dims % 32 == 16) return launch_turn<T, Q4, Turn::kHalvesApart>(c, layer, in, li, r, err, stream);
+    }
+    if (r.dims % 16 == 0) return launch_turn<T, Q4, Turn::kHalves>(c, layer, in, li, r, err, stream);
     return launch_turn<T, Q4, Turn::kOddHalves>(c, layer, in, li, r, err, stream);
 }
 

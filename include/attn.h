@@ -409,8 +409,8 @@ int attn_cache_append_granted(const attn_cache_t *cache, int layer, const void *
  * ATTN_E2M1); Qout: where they go, either Q itself with the same strides, or memory
  * that overlaps no input; rows of Qout do not overlap.  Queries of tokens that are
  * not written are left as they were.  Hq = 0: keys and values only (Q, Qout NULL).
- * 2 * heads + Hq at most 2^20.  dims that are multiples of 32 (neighbours: of 16)
- * are fastest.  Asynchronous.
+ * 2 * heads + Hq at most 2^20.  Of halves, dims that are multiples of 16 are fastest.
+ * Asynchronous.
  */
 typedef struct {
     const float *table;

@@ -131,6 +131,17 @@ def test_rotated_append(eta, neighbours, store, heads, Hq, d, dims, page, layout
 
 
 @pytest.mark.parametrize("store", [BF16, F32, E2M1])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_every_width_of_halves(eta, store, d):
+    """Halves of an odd number of 8 columns meet inside a group of 16 that shares a scale."""
+    lens, new, seqs = [40, 700, 650], [20, 640, 3], [0, 1, 2]
+    for dims in range(16, d + 1, 16):
+        cache = cache_of(eta, store, lens, 2, 32, d, "head", seed=dims)
+        check_append(eta, cache, lens, new, seqs, dims, False, 3, seed=d + dims, fused=True)
+        check_append(eta, cache, lens, new, seqs, dims, False, 3, seed=d + dims + 1, in_place=True)
+
+
+@pytest.mark.parametrize("store", [BF16, F32, E2M1])
 @pytest.mark.parametrize("dims,neighbours", [(64, False), (48, False), (64, True), (20, True), (26, False)])
 def test_in_place_and_placed(eta, store, dims, neighbours):
     """Queries turned in place, positions of their own (far ones, one twice), a table row order of entries."""
