@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
             if constexpr (MT == 1) {
 #pragma unroll
                 for (int kk = 0; kk < KS; ++kk) q_frag(0, kk, qf[kk]);
+                fence_proxy_async_smem();   // (the reads are done before the next copy may write there)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));   // the next Q may overwrite it
             }
@@ -414,10 +415,12 @@ __global__ void __launch_bounds__(160, PdShape<DP, MT>::CTAS)
                         }
                     }
                 }
+                fence_proxy_async_smem();   // (the reads are done before the next copy may write there)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_EMPTY + st));
             }
             if constexpr (MT > 1) {
+                fence_proxy_async_smem();   // (the reads are done before the next copy may write there)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(S::BAR_QEMPTY + qb));
             }

@@ -246,8 +246,10 @@ __device__ __forceinline__ void tma_store_wait_read0() {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 __device__ __forceinline__ void tma_store_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Order this thread's generic-proxy shared-memory writes before later
-// async-proxy (TMA / tensor core) reads of the same memory.
+// Order this thread's generic-proxy shared-memory accesses before later
+// async-proxy ones (TMA, bulk copies, tensor core) of the same memory: writes before
+// they are read, and reads before a copy that writes there again.  (An arrival
+// that frees a buffer does not wait for reads whose registers nothing has used yet.)
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
