@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(32 * (kDecWarps + 1)) decode_partial_kernel(co
                 for (int e = 0; e < E; ++e) o[i][e] = fmaf(pj, vf[e], o[i][e]);
             }
         }
+        fence_proxy_async_smem();   // (the reads are done before the next copy may write there)
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * st);   // this stage may be refilled
     }

@@ -10,7 +10,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "exact_tiled_attention_17_gb300", "csrc")
 
 
-@pytest.mark.parametrize("name,hand_backs", [("paged_decode.cu", 3), ("paged4_decode.cu", 2)])
+@pytest.mark.parametrize("name,hand_backs", [("paged_decode.cu", 3), ("paged4_decode.cu", 2), ("decode.cu", 1)])
 def test_reads_are_fenced_before_a_buffer_is_handed_back(name, hand_backs):
     with open(os.path.join(CSRC, name)) as f:
         lines = [re.sub(r"//.*", "", x).strip() for x in f]
