@@ -500,9 +500,9 @@ __global__ void __launch_bounds__(P4Shape<D, NT>::THREADS, P4Shape<D, NT>::CTAS)
 #pragma unroll
                     for (int k = 0; k < NW; ++k) {
                         const float mk = m_sh[k * ROWS + row];
-                        const float wt = mk == -INFINITY ? 0.f : ex2(mk - M);
+                        const float wt = ex2(mk - M);
                         const float4 v = *reinterpret_cast<const float4 *>(o_sh + (k * (ROWS / 2) + half) * S::OS + col);
-                        if (wt != 0.f) {
+                        if (mk != -INFINITY) {   // (a weight of 0 still passes a NaN on)
                             L = fmaf(wt, l_sh[k * ROWS + row], L);
                             acc.x = fmaf(wt, v.x, acc.x);
                             acc.y = fmaf(wt, v.y, acc.y);

@@ -112,9 +112,9 @@ __device__ __forceinline__ void merge_row(const PagedParams &p, int ctas, int c,
         const float Mn = fmaxf(M, Mc);
         if (Mn != -INFINITY) {
             const float a = M == -INFINITY ? 0.f : ex2(M - Mn);
-            // (a weight of 0 also stands for an o that was not written)
-            const float w = m == -INFINITY ? 0.f : ex2(m - Mn);
-            float wl = w == 0.f ? 0.f : w * l;
+            // (-1: no part, whose o was not written; a weight of 0 still passes a NaN on)
+            const float w = m == -INFINITY ? -1.f : ex2(m - Mn);
+            float wl = w < 0.f ? 0.f : w * l;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
             L = L * a + wl;
@@ -126,12 +126,13 @@ __device__ __forceinline__ void merge_row(const PagedParams &p, int ctas, int c,
 #pragma unroll
                 for (int q = 0; q < F; ++q) {
                     ws[q] = __shfl_sync(0xffffffffu, w, (q0 + q) & 31);
-                    if (q0 + q >= cnt) ws[q] = 0.f;
+                    if (q0 + q >= cnt) ws[q] = -1.f;
                     const int part = base + q0 + q;
                     const size_t sl = static_cast<size_t>(part == 0 ? 2 * c + 1 : 2 * (c + part));
 #pragma unroll
                     for (int e = 0; e < E; ++e) v[q][e] = 0.f;
-                    if (ws[q] != 0.f) load_row<E>(p.part_o + (sl * p.part_rows + row) * p.d + E * lane, v[q]);
+                    if (ws[q] < 0.f) ws[q] = 0.f;
+                    else load_row<E>(p.part_o + (sl * p.part_rows + row) * p.d + E * lane, v[q]);
                 }
 #pragma unroll
                 for (int q = 0; q < F; ++q)
@@ -167,9 +168,9 @@ __device__ __forceinline__ void merge_rows4(const PagedParams &p, int c, int row
         l = __ldcg(p.part_l + x);
     }
     const float M = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    // (a weight of 0 also stands for an o that was not written)
-    const float w = m == -INFINITY ? 0.f : ex2(m - M);
-    float L = w == 0.f ? 0.f : w * l;
+    // (-1: no part, whose o was not written; a weight of 0 still passes a NaN on)
+    const float w = m == -INFINITY ? -1.f : ex2(m - M);
+    float L = w < 0.f ? 0.f : w * l;
     L += __shfl_xor_sync(0xffffffffu, L, 1);
     float v[2][4][E], ws[2][4];
 #pragma unroll
@@ -180,7 +181,8 @@ __device__ __forceinline__ void merge_rows4(const PagedParams &p, int c, int row
             ws[t][q] = __shfl_sync(0xffffffffu, w, 2 * q + t);
 #pragma unroll
             for (int e = 0; e < E; ++e) v[t][q][e] = 0.f;
-            if (ws[t][q] != 0.f) load_row<E>(p.part_o + (at + q * kMergeWarps) * p.d + E * lane, v[t][q]);
+            if (ws[t][q] < 0.f) ws[t][q] = 0.f;
+            else load_row<E>(p.part_o + (at + q * kMergeWarps) * p.d + E * lane, v[t][q]);
         }
     }
     float acc[4][E];
