@@ -466,7 +466,9 @@ int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout
  * is multiplied by a power of two, after which a column keeps its 8 bits down to 2^-29
  * of the row's largest and is off by 2^-40 of it at most below; probabilities are
  * rounded once to float16 (2^-11, or 2^-32 of the row's largest where that is more);
- * scores, softmax and sums in float32.  Stored NaN reach every row that sees them.
+ * scores, softmax and sums in float32.  A stored NaN reaches every row that sees it: in
+ * K all columns and the LSE, in V its 16 columns; in V it may reach those columns of
+ * other rows of the same entry and kv head too, and nothing else.
  * float32: products and sums in IEEE float32, no TF32.  All take exponentials
  * from the hardware's power of two (relative error 2^-22 at most); d in {32,
  * 64, 96, 128}.  workspace: at least attn_paged_workspace_size(Hq, heads,
