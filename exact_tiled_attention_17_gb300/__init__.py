@@ -50,6 +50,7 @@ EXPORTS = ("attn_fwd", "attn_fwd_host_workspace_size", "attn_fwd_host", "attn_fw
 DEVIATION_NOALLOC_MAX_N = 1 << 20
 
 _DTYPE = {torch.float32: ATTN_F32, torch.bfloat16: ATTN_BF16, torch.float64: ATTN_F64}
+_E2M1 = getattr(torch, "float4_e2m1fn_x2", object())   # (a torch without the type: equal to none, and calls with other types work)
 
 
 class AttnError(RuntimeError):
@@ -489,7 +490,7 @@ class PagedCache:
         """A new cache without sequences.  dtype: bfloat16, float32, or
         torch.float4_e2m1fn_x2 for 4-bit values.  token_major: pages lie token by
         token instead of head by head."""
-        if dtype == torch.float4_e2m1fn_x2:
+        if dtype == _E2M1:
             if token_major or d % 32:
                 raise ValueError("pages of 4-bit values lie head by head, with d a multiple of 32")
             dtype, d = torch.uint8, 9 * d // 16
@@ -786,7 +787,7 @@ def _paged_workspace_size(Hq, heads, max_q, d, dtype) -> int:
 
 def attn_paged_workspace_size(Hq: int, heads: int, max_q: int, d: int, dtype) -> int:
     """dtype: the cache's (torch.float4_e2m1fn_x2 for 4-bit values)."""
-    code = dtype if isinstance(dtype, int) else ATTN_E2M1 if dtype == torch.float4_e2m1fn_x2 else _DTYPE[dtype]
+    code = dtype if isinstance(dtype, int) else ATTN_E2M1 if dtype == _E2M1 else _DTYPE[dtype]
     return _paged_workspace_size(Hq, heads, max_q, d, code)
 
 
