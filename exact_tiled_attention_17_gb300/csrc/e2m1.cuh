@@ -95,7 +95,7 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, uint32_t scale2, uint32_
 // bf16 rows beside 4-bit values become float16 (which holds those values exactly):
 // the power of two that brings a row's largest magnitude (float bits) to 2^14 ..
 // 2^15.  A column then keeps its 8 bits down to 2^-29 of the largest, and is off by
-// 2^-40 of that at most below.  -114 .. 126.
+// 2^-39 of that at most below (half of 2^-24, beside 2^14 at least).  -114 .. 126.
 __device__ __forceinline__ int f16_shift(uint32_t top) {
     return top == 0u ? 0 : min(14 + 127 - static_cast<int>(top >> 23), 126);
 }

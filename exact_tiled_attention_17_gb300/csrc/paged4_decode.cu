@@ -29,9 +29,10 @@
 // Numbers.  Values are exact in float16.  A row of Q is multiplied by a power of two
 // that brings its largest column to 2^14 .. 2^15 (bf16 has more exponents than
 // float16): a column keeps its 8 bits down to 2^-29 of the row's largest and is off
-// by 2^-40 of it at most below.  Weights are p = 2^(s - m + 7) against a reference m
-// that moves when a score exceeds it by 8, so they reach 2^15 and are rounded once to
-// float16 (2^-11 of a weight, 2^-32 of the row's largest at least); sums stay float32.
+// by 2^-39 of it at most below (half of 2^-24, beside 2^14 at least).  Weights are
+// p = 2^(s - m + 7) against a reference m that moves when a score exceeds it by 8, so
+// they reach 2^15 and are rounded once to float16 (2^-11 of a weight, 2^-32 of the row's
+// largest at least); sums stay float32.
 //
 // Pages that do not exist are not copied and their keys skipped; masked scores are
 // replaced by -inf; scales of slots past the end, which may hold anything, by 0.

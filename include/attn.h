@@ -464,7 +464,7 @@ int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout
  * two bf16 parts (O is then off by little more than its own rounding).
  * ATTN_E2M1: the cache's values are exact in the products' float16; a row of Q
  * is multiplied by a power of two, after which a column keeps its 8 bits down to 2^-29
- * of the row's largest and is off by 2^-40 of it at most below; probabilities are
+ * of the row's largest and is off by 2^-39 of it at most below; probabilities are
  * rounded once to float16 (2^-11, or 2^-32 of the row's largest where that is more);
  * scores, softmax and sums in float32.  A stored NaN reaches every row that sees it: in
  * K all columns and the LSE, in V its 16 columns; in V it may reach those columns of
