@@ -1,11 +1,12 @@
 """What the header promises of numbers in attention over a cache of 4-bit values:
-small columns of Q."""
+weights rounded once to float16, small columns of Q."""
 import math
 
 import pytest
 import torch
 
 from e2m1_ref import build4, ints
+from paged4_bounds import two_weights
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -15,6 +16,24 @@ BF16 = torch.bfloat16
 def eta():
     import exact_tiled_attention_17_gb300 as m
     return m
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("n,new,g,page", [
+    (64, 1, 8, 16), (200, 3, 5, 64), (513, 4, 4, 16), (513, 5, 4, 128), (700, 40, 2, 32), (300, 1, 17, 16),
+    (20001, 1, 8, 16), (20001, 2, 8, 64), (20001, 9, 3, 32), (20001, 9, 4, 256),
+])
+def test_weights_are_rounded_once_to_float16(eta, n, new, g, d, page):
+    known = two_weights(n, new, g, d)
+    cache, _ = build4(eta, [n], 1, page, d, seed=1)
+    k, v = known.k[:, None].cuda(), known.v[:, None].cuda()
+    eta.attn_cache_append(cache, 0, k, v, None, ints([0, n]))
+    for got, want in zip(eta.attn_cache_read(cache, 0, None, ints([0, n]), n), (k, v)):
+        assert torch.equal(got, want)
+    o, lse = eta.attn_paged_fwd(known.q.cuda(), cache, 0, None, ints([0, new]), max_q=new, scale=known.scale)
+    torch.cuda.synchronize()
+    assert eta.attn_status() == eta.ATTN_OK
+    known.check(o, lse)
 
 
 @pytest.mark.parametrize("g", [1, 3, 17])
