@@ -230,7 +230,7 @@ __device__ __forceinline__ PagedHdr paged_read_header(const PagedParams &p, int 
 int launch_paged_merge(const PagedParams &p, int bf16, int ctas, int sms, cudaStream_t stream);
 
 // Rows of a unit (sizes the workspace too).  The stream kernel: 16 or 32,
-// whichever holds an entry; over 4-bit values 8, or 16 (and several units to an entry).  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
+// whichever holds an entry; over 4-bit values 8, or 16 (and up to two units to an entry).  The CUDA-core kernels: 4, 8, 16, 32 or 64 (from 16 on
 // the one that tiles).
 inline int paged_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 16 ? 16 : 32; }
 inline int paged4_decode_rows(int g, int max_q) { return static_cast<long long>(g) * max_q <= 8 ? 8 : 16; }
