@@ -735,7 +735,8 @@ def attn_cache_append_rotated(cache, layer: int, k_new, v_new, seqs, q_start, ta
     b = _paged_list(q_start, cache, "q_start")
     c = None if granted is None else _paged_list(granted, cache, "granted", n)
     p = None if positions is None else _paged_list(positions, cache, "positions", T)
-    rotation = RotationT(table.data_ptr(), p, table.shape[0], table.shape[1], 1 if neighbours else 0)
+    # (positions are below 2^31: rows past them are never met)
+    rotation = RotationT(table.data_ptr(), p, min(table.shape[0], 2 ** 31 - 1), table.shape[1], 1 if neighbours else 0)
     args = (layer, k_new.data_ptr(), v_new.data_ptr(), strides, q, q_out, Hq, T, a, b, c, n, rotation)
     if _paged_here(cache, stream):
         return _append_rotated(cache, _raw_stream(cache._index), *args)
