@@ -821,8 +821,9 @@ def attn_paged_fwd(q, cache, layer: int, seqs, q_start, max_q: int | None = None
     of an entry, at most T.  The default, T, is right for one entry only: it
     sends a decode batch to the kernel for chunks, which is slower there, takes
     a workspace of up to 42 MB, and rounds probabilities to bf16 once where
-    decoding (Hq / heads * max_q <= 16) keeps two bf16 parts.  granted: what attn_cache_reserve returned for these entries;
-    those that got no room are left out.  Returns (o, lse): o like q, lse [T,
+    decoding (Hq / heads * max_q <= 16) keeps two bf16 parts (over 4-bit values
+    both round them once, to float16).  granted: what attn_cache_reserve
+    returned for these entries; those that got no room are left out.  Returns (o, lse): o like q, lse [T,
     Hq] float32; rows of no entry, or of one left out, are as they were."""
     shape = q.shape
     if len(shape) != 3 or shape[2] != cache.d or q.stride(2) != 1:

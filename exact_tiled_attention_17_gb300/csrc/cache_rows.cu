@@ -14,7 +14,8 @@
 // lower half and their partners in the upper one, so a pair is in one lane and a group
 // of 16 columns in two.  All lanes of a row are in one warp.  The
 // CTA's threads go through the rows of all its tokens in one line, each with the next
-// two on their way.
+// two on their way.  (Four CTAs an SM, 64 registers: the appends of bf16 rows spill 4 to
+// 36 bytes a thread, 92 where halves end inside a group of 16.)
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -28,10 +29,14 @@ namespace eta {
 namespace {
 
 constexpr int kRowThreads = 256;
-// Tokens to a CTA, where there are many (else one).  Appending 4 x 1500 .. 2048 tokens:
-// 2, 4 and 8 take 43, 38 and 41 us; reading 16 x 1000 .. 4096 of 4 bits: 74, 52 and 44.
-// (One warp that finds the next group's places while the others copy gains nothing.)
-constexpr int kAppendTokens = 4, kReadTokens = 8;
+// Tokens to a CTA, where there are more than kFewTokens (else one).  8 kv heads of 128,
+// appending 4 x 1500 .. 2048 tokens (32 query heads): 2, 4 and 8 take 43, 38 and 41 us;
+// reading 16 x 1000 .. 4096 of 4 bits: 74, 52 and 44.  (One warp that finds the next
+// group's places while the others copy gains nothing.)
+// One against many, bf16, 512 / 1024 / 2048 tokens: 8 kv and 32 query heads 8.4 and 10.3 /
+// 12.3 and 11.3 / 17.9 and 14.7 us, 1 and 4 heads 8.7 and 8.9 / 10.7 and 8.9 / 15.0 and
+// 9.0; reading takes the same up to 1024 (8.5), then 10.1 and 8.5.
+constexpr int kAppendTokens = 4, kReadTokens = 8, kFewTokens = 1024;
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_done() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -430,7 +435,7 @@ unsigned blocks(int T, int tok) { return static_cast<unsigned>((static_cast<long
 
 template <typename T, bool Q4, Turn TURN>
 int launch_turn(const CacheView &c, int layer, const RowIn &in, const RowList &li, const Rotation &r, int *err, cudaStream_t stream) {
-    if (li.T <= 1024)
+    if (li.T <= kFewTokens)
         return launch_dependent(append_rows_kernel<T, Q4, TURN, 1>, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, in, li, r, err);
     return launch_dependent(append_rows_kernel<T, Q4, TURN, kAppendTokens>, dim3(blocks(li.T, kAppendTokens)), kRowThreads, 0, stream, c, layer,
                             in, li, r, err);
@@ -465,7 +470,7 @@ int launch_cache_rows_out(const CacheView &c, int layer, RowOut out, const RowLi
     out.lane_shift = 0;
     while ((1 << out.lane_shift) < (c.bits == 4 ? out.d / 16 : c.row_vecs)) ++out.lane_shift;
     auto go = [&](auto one, auto many) {
-        if (li.T <= 1024) return launch_dependent(one, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, out, li, err);
+        if (li.T <= kFewTokens) return launch_dependent(one, dim3(blocks(li.T, 1)), kRowThreads, 0, stream, c, layer, out, li, err);
         return launch_dependent(many, dim3(blocks(li.T, kReadTokens)), kRowThreads, 0, stream, c, layer, out, li, err);
     };
     return c.bits == 4 ? go(read_rows_kernel<true, 1>, read_rows_kernel<true, kReadTokens>)

@@ -44,7 +44,8 @@
 // copies alone take 75 and the arithmetic alone 81 (graph replays of 85): 272
 // instructions to 16 keys, of which 64 conversions (a half of the ALU's time), 64
 // multiplications and 16 matrix instructions (of the FMA pipe's).  Three CTAs an SM and
-// blocks in pairs: two CTAs 92 us, four with single blocks 101.  12 and 16 rows: 134 us.
+// blocks in pairs: two CTAs 92 us, four with single blocks 101.  12 and 16 rows: 133 us
+// (132 bytes of spills at d 128, 32 at 96).
 // 4 sequences of 300 .. 1000: 11 us, a chain of dependent reads over two launches.
 #include <algorithm>
 #include <atomic>
@@ -69,7 +70,7 @@ struct P4Shape {
     static constexpr int STAGE = 2 * OFF_V;
     static constexpr int Q_BYTES = ROWS * D * 2;
     static constexpr int OS = D + 4;                          // floats from row to row of an output in shared memory
-    // (16 rows, d 128: with 4 stages 146 us for 64 x 8000 tokens, with 3 and the L1 that leaves for spilled registers 134)
+    // (16 rows, d 128: with 4 stages 146 us for 64 x 2048 .. 8191 tokens, with 3 and the L1 that leaves for spilled registers 133)
     static constexpr int MOST = 228 * 1024 / CTAS - 1024;     // bytes a CTA
     static constexpr int REST = 2 * Q_BYTES + NW * ROWS * (OS / 2 + 2) * 4 + 1024 + 512;
     static constexpr int NS_RAW = (MOST - REST) / STAGE, NS_MAX = NT == 2 ? 3 : 6, NS = NS_RAW < NS_MAX ? NS_RAW : NS_MAX;

@@ -324,9 +324,9 @@ namespace {
 // float32: units of up to 8 rows are streamed through registers (32 x 8000 tokens,
 // d 128, 4 rows: 160 us, tiled 365; 16 rows, 16 x 4000: 161, tiled 106).
 // 4-bit values: the stream kernel takes entries of one or two units of 16 rows, which
-// hold whole tokens (64 x 1048 .. 4191 tokens, 8 heads of 128: 80 to 86 us for up to 16
-// rows, 20 rows 143, matrix kernel 166; 6 x 5, 9 x 3 and 10 x 3 rows would make three
-// units: 207 to 210, matrix 167; 16 x 1000 .. 4096, 2 heads, 20 rows: 27, 29).
+// hold whole tokens (64 x 1048 .. 4191 tokens, 8 heads of 128: 9 to 16 rows 85 us, matrix
+// kernel 165; 20 rows 143, 166; 6 x 5, 9 x 3 and 10 x 3 rows would make three units: 207
+// to 210, 167; 16 x 1000 .. 4096, 2 heads, 20 rows: 27, 29).
 enum class Path { kFew, kSimt, kDecode, kTc, kDecode4, kTc4 };
 Path path_of(int g, int max_q, int bits) {
     if (bits == 4) return g <= 16 && max_q <= 2 * (16 / g) ? Path::kDecode4 : Path::kTc4;
