@@ -759,8 +759,8 @@ def attn_cache_read(cache, layer: int, seqs, q_start, T: int | None = None, firs
     None: sequence i), whose tokens first[i], first[i] + 1, ... (first None: the
     last ones) go to rows q_start[i] .. q_start[i+1] - 1.  T: rows in all;
     k_out, v_out: [T, heads, d] of the cache's dtype with one pair of strides, or
-    new tensors (T needed).  Returns (k, v); rows of no entry, and of tokens that
-    the cache does not hold, are as they were."""
+    new tensors (T needed).  Returns (k, v); rows of no entry, of tokens that
+    the cache does not hold, and of entries with a negative first are as they were."""
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out go together")
     if k_out is not None:

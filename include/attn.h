@@ -431,7 +431,8 @@ int attn_cache_append_rotated(const attn_cache_t *cache, int layer, const void *
  * Kout, Vout: strides as for attn_cache_append; their rows do not overlap.  A
  * sequence may be named more than once.  Rows of tokens that the sequence does not
  * have, or whose page the table does not name, are left as they were, and
- * attn_status returns ATTN_ERR_ARG; so are rows outside q_start[0] .. q_start[n] - 1.
+ * attn_status returns ATTN_ERR_ARG; an entry whose first[i] is negative is left out
+ * whole.  Rows outside q_start[0] .. q_start[n] - 1 are left as they were too.
  * 2 * heads at most 2^20.  Asynchronous.
  */
 int attn_cache_read(const attn_cache_t *cache, int layer, void *Kout, void *Vout, long long token_stride,
